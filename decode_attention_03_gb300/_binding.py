@@ -28,6 +28,9 @@ GQA_ERR_CUDA = 4
 GQA_ERR_TIMEOUT = 5
 GQA_ERR_BOUNDS = 6
 GQA_BUILD_BOUNDS_CHECK = 1
+GQA_CACHE_ROWS = 0
+GQA_CACHE_VLLM = 1
+GQA_CACHE_KV8 = 2
 
 
 class GQAError(RuntimeError):
@@ -41,6 +44,16 @@ class gqa_options(ctypes.Structure):
                 ("timeout_us", ctypes.c_uint32), ("test_stall_cta", ctypes.c_int),
                 ("paged_head_group", ctypes.c_int), ("causal", ctypes.c_int), ("bf16", ctypes.c_int),
                 ("mma_path", ctypes.c_int)]
+
+
+class gqa_append_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_out")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "cos_sin", "positions", "slots", "k_cache",
+                                                "v_cache")] +
+                [(n, ctypes.c_int) for n in ("num_tokens", "h_q", "h_kv", "d_head", "max_position", "rot_dim",
+                                             "interleaved", "num_blocks", "block_size", "cache_layout", "bf16")] +
+                [("eps", ctypes.c_float)])
 
 
 def _load():
@@ -83,6 +96,11 @@ _SIGS = {
     "gqa_decode_noalloc": ([_p, _p, _p, _p, _i, _i, _i64, _i, _i, _i, _f, _p], _i),
     "gqa_decode_noalloc_check": ([_p], _i),
     "gqa_decode_paged_vllm": ([_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p], _i),
+    "gqa_kv8_block_bytes": ([_i, _i], _sz),
+    "gqa_append": ([ctypes.POINTER(gqa_append_args), _p, _sz, _p], _i),
+    "gqa_decode_kv8_workspace_size": ([_i, _i, _i, _i, _i], _sz),
+    "gqa_decode_kv8": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _p, _opt], _i),
+    "gqa_kv8_read": ([_p, _p, _p, _p, _p, _p, _i, _i64, _i, _i, _i, _i, _i, _p, _sz, _p, _opt], _i),
     "gqa_decode_paged_vllm_ex": ([_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p,
                                   _opt], _i),
 }
@@ -435,3 +453,249 @@ def gqa_decode_noalloc_check(stream=None) -> int:
     """Status of the gqa_decode_noalloc calls on the current device since the last check
     (synchronises ``stream``; GQA_OK or GQA_ERR_TIMEOUT); clears it."""
     return lib.gqa_decode_noalloc_check(_stream(stream))
+
+
+# ---------------------------------------------------------------- filling a cache; the 8-bit cache
+_HALVES = (torch.float16, torch.bfloat16)
+
+
+def _in_stream(stream):
+    """The stream as a context, so that what a call allocates belongs to the stream it runs on."""
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _here(dev: int) -> int:
+    """The raw current stream of device ``dev``, which has to be the current device."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _status_workspace(dev: int, raw: int) -> torch.Tensor:
+    """A workspace for calls that need its status word alone: the cached one of the stream, which graphs may
+    share with other calls (the kernels only set bits in it)."""
+    t = _ws_cache.get((dev, raw))
+    if t is not None:
+        return t
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(256, dtype=torch.uint8, device=torch.device("cuda", dev))
+    return workspace(256, torch.device("cuda", dev))
+
+
+def _index(t: torch.Tensor, name: str, dtype, dev: int, shape) -> int:
+    if t.dtype != dtype or t.get_device() != dev or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the device of the others")
+    return t.data_ptr()
+
+
+def _rows16(t: torch.Tensor, name: str, dtype, dev: int, tokens: int, cols: int) -> Tuple[int, int]:
+    """Pointer and row stride of a (tokens, cols) 16-bit tensor whose rows are dense."""
+    if t.dtype != dtype or t.get_device() != dev or tuple(t.shape) != (tokens, cols) or \
+            (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(tokens, cols)} with dense rows on the device of "
+                         "the others")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else cols
+
+
+def _kv8_block_size(cache: torch.Tensor, h_kv: Optional[int], d_head: int, dev: int) -> int:
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or cache.get_device() != dev or not cache.is_contiguous() or \
+            (h_kv is not None and cache.shape[1] != h_kv) or cache.shape[2] % (2 * d_head + 2):
+        raise ValueError("an 8-bit cache must be a contiguous uint8 tensor (num_blocks, h_kv, block_size * "
+                         "(2 * d_head + 2)) on the device of the others")
+    return cache.shape[2] // (2 * d_head + 2)
+
+
+def gqa_kv8_block_bytes(block_size: int, d_head: int) -> int:
+    """Bytes of one (block, head) of the 8-bit cache; 0 for a block size or d_head it does not have."""
+    return lib.gqa_kv8_block_bytes(int(block_size), int(d_head))
+
+
+def gqa_kv8_cache(num_blocks: int, block_size: int, h_kv: int, d_head: int, device=None) -> torch.Tensor:
+    """An empty 8-bit cache: uint8 (num_blocks, h_kv, block_size * (2 * d_head + 2))."""
+    n = gqa_kv8_block_bytes(block_size, d_head)
+    if n == 0:
+        raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_kv8_cache")
+    return torch.zeros(num_blocks, h_kv, n, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q: int, h_kv: int, slots: torch.Tensor,
+               k_cache: torch.Tensor, v_cache: Optional[torch.Tensor] = None, *,
+               positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
+               interleaved: bool = False, q_weight: Optional[torch.Tensor] = None,
+               k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+               workspace_tensor: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Put new tokens into a paged cache: per-head RMS norms of q and k (where ``q_weight`` / ``k_weight`` (D)
+    are given), their rotation (where ``cos_sin`` (max_position, rot_dim) float32 and ``positions`` (T) int32
+    are given: rot_dim/2 cosines then rot_dim/2 sines a row; ``interleaved``: pairs (2i, 2i+1) instead of
+    (i, i + rot_dim/2)), and the write of k and v into the cache rows ``slots`` (T) int64
+    (block * block_size + row; negative: not stored; no slot twice).
+
+    q (T, h_q*D) or None, k, v (T, h_kv*D) float16 or bfloat16, rows dense (views of a fused projection serve).
+    The cache: ``k_cache, v_cache`` of gqa_decode_paged (num_blocks, block_size, h_kv*D) or of
+    gqa_decode_paged_vllm, or one 8-bit cache (gqa_kv8_cache), quantised as it is written.
+    Returns the queries after norm and rotation (``q_out``, which may be q itself)."""
+    if stream is not None:
+        with _in_stream(stream):
+            return gqa_append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions=positions, cos_sin=cos_sin,
+                              interleaved=interleaved, q_weight=q_weight, k_weight=k_weight, eps=eps, q_out=q_out,
+                              workspace_tensor=workspace_tensor)
+    dt, dev = k.dtype, k.get_device()
+    if dt not in _HALVES or dev < 0 or k.dim() != 2 or k.shape[1] % h_kv:
+        raise ValueError("k must be a float16 or bfloat16 CUDA tensor (tokens, h_kv*d_head)")
+    raw = _here(dev)
+    T, kc = k.shape
+    D = kc // h_kv
+    kp, ks = _rows16(k, "k", dt, dev, T, kc)
+    vp, vs = _rows16(v, "v", dt, dev, T, kc)
+    qp = qs = op = os_ = 0
+    if q is None:
+        h_q, q_out = 0, None
+    else:
+        qp, qs = _rows16(q, "q", dt, dev, T, h_q * D)
+        if q_out is None:
+            q_out = torch.empty((T, h_q * D), dtype=dt, device=q.device)
+        op, os_ = _rows16(q_out, "q_out", dt, dev, T, h_q * D)
+    cp = pp = 0
+    rot = rows = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions is None:
+            raise ValueError("cos_sin must be (max_position, rot_dim) and comes with positions")
+        rows, rot = cos_sin.shape
+        cp = _index(cos_sin, "cos_sin", torch.float32, dev, (rows, rot))
+        pp = _index(positions, "positions", torch.int32, dev, (T,))
+    if k_cache.dtype == torch.uint8:
+        if v_cache is not None:
+            raise ValueError("an 8-bit cache holds K and V: pass no v_cache")
+        layout, bs, vcp = GQA_CACHE_KV8, _kv8_block_size(k_cache, h_kv, D, dev), 0
+    else:
+        shape = tuple(k_cache.shape)
+        if len(shape) == 5:
+            layout, bs = GQA_CACHE_VLLM, shape[3]
+            want, v_want = (shape[0], h_kv, D // 8, bs, 8), (shape[0], h_kv, D, bs)
+        else:
+            layout, bs = GQA_CACHE_ROWS, shape[1] if len(shape) == 3 else 0
+            want = v_want = (shape[0], bs, kc)
+        if v_cache is None:
+            raise ValueError("a 16-bit cache needs k_cache and v_cache")
+        _index(k_cache, "k_cache", dt, dev, want)
+        vcp = _index(v_cache, "v_cache", dt, dev, v_want)
+    ws = _status_workspace(dev, raw) if workspace_tensor is None else workspace_tensor
+    args = gqa_append_args(
+        qp, kp, vp, op, qs, ks, vs, os_, 0 if q_weight is None else _index(q_weight, "q_weight", dt, dev, (D,)),
+        0 if k_weight is None else _index(k_weight, "k_weight", dt, dev, (D,)), cp, pp,
+        _index(slots, "slots", torch.int64, dev, (T,)), k_cache.data_ptr(), vcp, T, h_q, h_kv, D, rows, rot,
+        1 if interleaved else 0, k_cache.shape[0], bs, layout, 1 if dt == torch.bfloat16 else 0, eps)
+    st = lib.gqa_append(args, ws.data_ptr(), ws.numel(), raw)
+    if st:
+        raise GQAError(st, "gqa_append")
+    return q_out
+
+
+_kv8_ws_bytes = {}
+
+
+def gqa_decode_kv8_workspace_size(num_seqs: int, T_q: int, h_q: int, h_kv: int, d_head: int) -> int:
+    """Workspace bytes of gqa_decode_kv8 on the current device (0: invalid shape)."""
+    return lib.gqa_decode_kv8_workspace_size(num_seqs, T_q, h_q, h_kv, d_head)
+
+
+def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, h_q: int,
+                   h_kv: int, scale: Optional[float] = None, *, causal: bool = False,
+                   out: Optional[torch.Tensor] = None, workspace_tensor: Optional[torch.Tensor] = None, stream=None,
+                   timeout_us: int = 0, test_stall_cta: int = -1) -> torch.Tensor:
+    """Decode attention over the 8-bit cache: q (N, h_q*D) or (N, T_q, h_q*D) float16 or bfloat16 (the output too),
+    cache (num_blocks, h_kv, block_size*(2D+2)) uint8, tables (N, max_blocks) and lens (N) int32; G*T_q <= 64.
+    ``causal``: query token t sees keys j <= len - T_q + t only."""
+    if stream is not None:
+        with _in_stream(stream):
+            return gqa_decode_kv8(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal=causal, out=out,
+                                  workspace_tensor=workspace_tensor, timeout_us=timeout_us,
+                                  test_stall_cta=test_stall_cta)
+    dt, dev, dim = q.dtype, q.get_device(), q.dim()
+    if dt not in _HALVES or dev < 0 or dim not in (2, 3) or not q.is_contiguous() or q.shape[-1] % h_q:
+        raise ValueError("q must be a contiguous float16 or bfloat16 CUDA tensor (N, h_q*d_head) or (N, T_q, h_q*d_head)")
+    raw = _here(dev)
+    N, T_q = q.shape[0], q.shape[1] if dim == 3 else 1
+    D = q.shape[-1] // h_q
+    bs = _kv8_block_size(cache, h_kv, D, dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (N, max_blocks)")
+    mb = block_tables.shape[1]
+    tp = _index(block_tables, "block_tables", torch.int32, dev, (N, mb))
+    lp = _index(seq_lens, "seq_lens", torch.int32, dev, (N,))
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != dt or out.get_device() != dev or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be like q")
+    if workspace_tensor is None:
+        key = (dev, N, T_q, h_q, h_kv, D)
+        n = _kv8_ws_bytes.get(key)
+        if n is None:
+            n = lib.gqa_decode_kv8_workspace_size(N, T_q, h_q, h_kv, D)
+            if n == 0:
+                raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_decode_kv8_workspace_size")
+            _kv8_ws_bytes[key] = n
+        ws = _ws_cache.get((dev, raw))
+        if torch.cuda.is_current_stream_capturing():
+            # a graph keeps its own partials: another graph or call may run beside its replays
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+            ws[:256].zero_()
+        elif ws is None or ws.numel() < n:
+            ws = workspace(n, q.device)
+    else:
+        ws = workspace_tensor
+    opt = gqa_options(0, 0, timeout_us, test_stall_cta, 0, 1 if causal else 0, 1 if dt == torch.bfloat16 else 0, 0)
+    st = lib.gqa_decode_kv8(q.data_ptr(), cache.data_ptr(), tp, lp, out.data_ptr(), N, T_q, mb, cache.shape[0], bs, h_q,
+                            h_kv, D, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), raw, opt)
+    if st:
+        raise GQAError(st, "gqa_decode_kv8")
+    return out
+
+
+def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, d_head: int,
+                 out_len: Optional[int] = None, *, begins: Optional[torch.Tensor] = None, dtype=None,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 workspace_tensor: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Tokens [begins[b], min(begins[b] + out_len, seq_lens[b])) of every sequence of an 8-bit cache as 16-bit
+    K and V (N, out_len, h_kv*D), the layout of gqa_decode.  Into ``k_out`` / ``v_out`` (the one left out is
+    not read; rows past a sequence's last token stay as they were), or, with neither, into zeros of ``dtype``
+    (float16) and ``out_len`` tokens.  begins (N) int32, default 0."""
+    if stream is not None:
+        with _in_stream(stream):
+            return gqa_kv8_read(cache, block_tables, seq_lens, d_head, out_len, begins=begins, dtype=dtype,
+                                k_out=k_out, v_out=v_out, workspace_tensor=workspace_tensor)
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError("cache must be a CUDA tensor")
+    raw = _here(dev)
+    bs = _kv8_block_size(cache, None, d_head, dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (N, max_blocks)")
+    N, mb = block_tables.shape
+    nb, h_kv, _ = cache.shape
+    tp = _index(block_tables, "block_tables", torch.int32, dev, (N, mb))
+    lp = _index(seq_lens, "seq_lens", torch.int32, dev, (N,))
+    bp = 0 if begins is None else _index(begins, "begins", torch.int32, dev, (N,))
+    given = k_out if k_out is not None else v_out
+    if given is None:
+        if out_len is None:
+            raise ValueError("pass out_len, or k_out / v_out")
+        dt = torch.float16 if dtype is None else dtype
+        k_out, v_out = (torch.zeros(N, out_len, h_kv * d_head, dtype=dt, device=cache.device) for _ in range(2))
+    else:
+        dt = given.dtype
+        if given.dim() != 3 or (out_len is not None and out_len != given.shape[1]) or (dtype is not None and dtype != dt):
+            raise ValueError("k_out and v_out must be (N, out_len, h_kv*d_head) of dtype")
+        out_len = given.shape[1]
+    if dt not in _HALVES:
+        raise ValueError("k_out and v_out must be float16 or bfloat16")
+    kp = 0 if k_out is None else _index(k_out, "k_out", dt, dev, (N, out_len, h_kv * d_head))
+    vp = 0 if v_out is None else _index(v_out, "v_out", dt, dev, (N, out_len, h_kv * d_head))
+    ws = _status_workspace(dev, raw) if workspace_tensor is None else workspace_tensor
+    opt = gqa_options(0, 0, 0, -1, 0, 0, 1 if dt == torch.bfloat16 else 0, 0)
+    st = lib.gqa_kv8_read(cache.data_ptr(), tp, lp, bp, kp, vp, N, out_len, mb, nb, bs, h_kv, d_head, ws.data_ptr(),
+                          ws.numel(), raw, opt)
+    if st:
+        raise GQAError(st, "gqa_kv8_read")
+    return k_out, v_out

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/gqa_decode.h"
+#include "gqa_host.cuh"
 #include "gqa_instances.cuh"
 #include "gqa_merge.cuh"
 #include "gqa_tc.cuh"
@@ -18,9 +19,7 @@ namespace gqa {
 namespace {
 
 constexpr int kVersion = 10000;            // 1.0.0
-constexpr size_t kHeaderBytes = 256;        // status word (+ reserved)
 constexpr int kMinTilesPerSplit = 1;        // a split streams at least one 64-key tile
-constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
 constexpr int kTcMinRows = 16;              // automatic MMA path: tcgen05 from this many rows per KV head
 // Automatic merge: the mma.sync split kernel folds 2 to kMaxClusterSplits splits in one cluster
@@ -69,8 +68,6 @@ constexpr int64_t kDeepMinTilesPerSplit = 48;
 // 306.5.)  So the automatic choice is v2; v1 is a partition_size of at least max_seq_len.
 constexpr int kV2Partition = 512;
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 int d_index(int d) { return d == 64 ? 0 : (d == 128 ? 1 : -1); }
 
 int row_class(int rows) {
@@ -80,8 +77,6 @@ int row_class(int rows) {
   if (rows <= 64) return 3;
   return -1;
 }
-
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---------------------------------------------------------------- per-device state
 struct DevState {
@@ -444,23 +439,6 @@ gqa_status plan_contig(int B, int T_q, int64_t S_kv, int64_t s_begin, int64_t s_
     }
   }
   return GQA_OK;
-}
-
-// Launch with programmatic stream serialisation: the kernel may begin launching while the
-// previous kernel in the stream finishes (it waits in griddepcontrol.wait before reading).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(block, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 // one warp per row while a warp's first chunk of loads covers every partial, else four

@@ -1,0 +1,216 @@
+// Host side of the cache operators: gqa_append, gqa_decode_kv8 and gqa_kv8_read.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gqa_decode.h"
+#include "gqa_host.cuh"
+#include "gqa_kv8.cuh"
+#include "gqa_kv8_decode.cuh"
+
+namespace gqa {
+namespace {
+
+bool block_size_ok(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64; }
+
+bool aligned_to(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
+
+// ---------------------------------------------------------------- append
+template <int D, bool BF16, int U>
+cudaError_t append_launch(AppendParams p, cudaStream_t st) {
+  constexpr int HPW = 32 / (D / 8);
+  p.sets = (p.h_q + 2 * p.h_kv + U * HPW - 1) / (U * HPW);
+  const int64_t warps = (int64_t)p.num_tokens * p.sets, per = kAppendThreads / 32;
+  const int64_t blocks = (warps + per - 1) / per;
+  if (blocks > 2147483647LL) return cudaErrorInvalidValue;
+  return launch_pdl(gqa_append_kernel<D, BF16, U>, (unsigned)blocks, kAppendThreads, st, p);
+}
+
+gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void* stream) {
+  if (a.num_tokens < 0 || a.h_q < 0 || a.h_kv < 1 || a.num_blocks < 0) return GQA_ERR_INVALID_ARG;
+  if (a.h_q > 65535 || a.h_kv > 65535 || a.h_q % a.h_kv != 0) return GQA_ERR_INVALID_ARG;
+  if (a.d_head != 64 && a.d_head != 128) return GQA_ERR_UNSUPPORTED;
+  if (!block_size_ok(a.block_size) || (int64_t)a.num_blocks * a.block_size >= (int64_t(1) << 31))
+    return GQA_ERR_INVALID_ARG;
+  if (a.cache_layout < GQA_CACHE_ROWS || a.cache_layout > GQA_CACHE_KV8) return GQA_ERR_INVALID_ARG;
+  if (!std::isfinite(a.eps) || a.eps < 0.f) return GQA_ERR_INVALID_ARG;
+  if (a.cos_sin != nullptr &&
+      (a.rot_dim < 8 || a.rot_dim > a.d_head || a.rot_dim % 8 != 0 || a.max_position < 1 || !aligned16(a.cos_sin) ||
+       !aligned_to(a.positions, 4)))
+    return GQA_ERR_INVALID_ARG;
+  const int64_t qn = (int64_t)a.h_q * a.d_head, kn = (int64_t)a.h_kv * a.d_head;
+  if (a.num_tokens > 0) {
+    if (a.k_stride < kn || a.v_stride < kn || a.k_stride % 8 || a.v_stride % 8) return GQA_ERR_INVALID_ARG;
+    if (a.h_q > 0 && (a.q_stride < qn || a.q_out_stride < qn || a.q_stride % 8 || a.q_out_stride % 8 ||
+                      !aligned16(a.q) || !aligned16(a.q_out)))
+      return GQA_ERR_INVALID_ARG;
+    if (!aligned16(a.k) || !aligned16(a.v) || !aligned_to(a.slots, 8) || !aligned16(a.k_cache) ||
+        (a.cache_layout != GQA_CACHE_KV8 && !aligned16(a.v_cache)))
+      return GQA_ERR_INVALID_ARG;
+    if ((a.q_weight != nullptr && !aligned16(a.q_weight)) || (a.k_weight != nullptr && !aligned16(a.k_weight)))
+      return GQA_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return GQA_ERR_INVALID_ARG;
+    if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
+  }
+  if (a.num_tokens == 0) return GQA_OK;
+  AppendParams p = {};
+  p.q = a.q; p.k = a.k; p.v = a.v; p.q_out = a.q_out;
+  p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride; p.q_out_stride = a.q_out_stride;
+  p.q_weight = a.q_weight; p.k_weight = a.k_weight;
+  p.cos_sin = a.cos_sin; p.positions = a.positions; p.slots = a.slots;
+  p.k_cache = a.k_cache; p.v_cache = a.v_cache;
+  p.status = static_cast<uint32_t*>(ws);
+  p.num_tokens = a.num_tokens; p.h_q = a.h_q; p.h_kv = a.h_kv;
+  p.max_position = a.max_position; p.rot_dim = a.rot_dim; p.interleaved = a.interleaved ? 1 : 0;
+  p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.layout = a.cache_layout;
+  p.eps = a.eps;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.d_head == 64)
+    return cuda_status(a.bf16 ? append_launch<64, true, 1>(p, st) : append_launch<64, false, 1>(p, st));
+  return cuda_status(a.bf16 ? append_launch<128, true, 1>(p, st) : append_launch<128, false, 1>(p, st));
+}
+
+// ---------------------------------------------------------------- shapes of the kv8 calls
+gqa_status check_kv8(int N, int h_kv, int D, int max_blocks, int num_blocks, int block_size) {
+  if (N < 0 || N > 65535 || h_kv < 1 || h_kv > 65535 || max_blocks < 1 || num_blocks < 0) return GQA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
+  if (!block_size_ok(block_size)) return GQA_ERR_INVALID_ARG;
+  if ((int64_t)max_blocks * block_size >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
+  if ((int64_t)num_blocks * block_size >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
+  return GQA_OK;
+}
+
+gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
+  if (N < 0 || N > 65535 || T_q < 1 || h_q < 1 || h_kv < 1 || h_kv > 65535 || h_q % h_kv != 0)
+    return GQA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
+  if ((int64_t)(h_q / h_kv) * T_q > 64) return GQA_ERR_UNSUPPORTED;
+  return GQA_OK;
+}
+
+// ---------------------------------------------------------------- decode
+template <int D, bool BF16>
+cudaError_t decode_launch(const Kv8Params& p, cudaStream_t st) {
+  return launch_pdl(gqa_decode_kv8_kernel<D, BF16>, (unsigned)((int64_t)p.N * p.T_q * p.h_q), kKv8Warps * 32, st, p);
+}
+
+gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* tables, const int32_t* lens,
+                           uint16_t* o, int N, int T_q, int max_blocks, int num_blocks, int block_size, int h_q,
+                           int h_kv, int D, float scale, void* ws, size_t ws_bytes, void* stream,
+                           const gqa_options* opt_in) {
+  const gqa_options opt = opt_in ? *opt_in : gqa_default_options();
+  gqa_status s = check_rows(N, T_q, h_q, h_kv, D);
+  if (s == GQA_OK) s = check_kv8(N, h_kv, D, max_blocks, num_blocks, block_size);
+  if (s != GQA_OK) return s;
+  if (!std::isfinite(scale)) return GQA_ERR_INVALID_ARG;
+  if (N == 0) return GQA_OK;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(ws) || !aligned_to(tables, 4) ||
+      !aligned_to(lens, 4))
+    return GQA_ERR_INVALID_ARG;
+  if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
+  Kv8Params p = {};
+  p.q = q; p.o = o; p.cache = static_cast<const uint8_t*>(cache);
+  p.block_tables = tables; p.seq_lens = lens; p.status = static_cast<uint32_t*>(ws);
+  p.N = N; p.T_q = T_q; p.h_q = h_q; p.h_kv = h_kv; p.G = h_q / h_kv; p.rows = p.G * T_q;
+  p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size;
+  p.causal = opt.causal ? 1 : 0;
+  p.scale_log2 = scale * kLog2e;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 64) return cuda_status(opt.bf16 ? decode_launch<64, true>(p, st) : decode_launch<64, false>(p, st));
+  return cuda_status(opt.bf16 ? decode_launch<128, true>(p, st) : decode_launch<128, false>(p, st));
+}
+
+// ---------------------------------------------------------------- read
+template <int D, bool BF16>
+cudaError_t read_launch(const Kv8ReadParams& p, cudaStream_t st) {
+  const int64_t warps = (int64_t)p.num_seqs * p.groups * p.h_kv, per = kReadThreads / 32;
+  const int64_t blocks = (warps + per - 1) / per;
+  if (blocks > 2147483647LL) return cudaErrorInvalidValue;
+  return launch_pdl(gqa_kv8_read_kernel<D, BF16>, (unsigned)blocks, kReadThreads, st, p);
+}
+
+gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* lens, const int32_t* begins,
+                     uint16_t* k_out, uint16_t* v_out, int N, int64_t out_len, int max_blocks, int num_blocks,
+                     int block_size, int h_kv, int D, void* ws, size_t ws_bytes, void* stream,
+                     const gqa_options* opt) {
+  gqa_status s = check_kv8(N, h_kv, D, max_blocks, num_blocks, block_size);
+  if (s != GQA_OK) return s;
+  if (out_len < 0 || out_len >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
+  if (N == 0 || out_len == 0) return GQA_OK;
+  if (k_out == nullptr && v_out == nullptr) return GQA_ERR_INVALID_ARG;
+  if (!aligned16(cache) || (k_out != nullptr && !aligned16(k_out)) || (v_out != nullptr && !aligned16(v_out)) ||
+      !aligned16(ws) || !aligned_to(tables, 4) || !aligned_to(lens, 4) || (begins != nullptr && !aligned_to(begins, 4)))
+    return GQA_ERR_INVALID_ARG;
+  if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
+  Kv8ReadParams p = {};
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.block_tables = tables; p.seq_lens = lens; p.begins = begins;
+  p.k_out = k_out; p.v_out = v_out; p.status = static_cast<uint32_t*>(ws);
+  p.out_len = out_len;
+  p.num_seqs = N; p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size; p.h_kv = h_kv;
+  // tokens past the table exist in no sequence: no warps for them
+  const int64_t most = out_len < (int64_t)max_blocks * block_size ? out_len : (int64_t)max_blocks * block_size;
+  p.groups = (most + kReadTokens - 1) / kReadTokens;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = opt != nullptr && opt->bf16;
+  if (D == 64) return cuda_status(bf16 ? read_launch<64, true>(p, st) : read_launch<64, false>(p, st));
+  return cuda_status(bf16 ? read_launch<128, true>(p, st) : read_launch<128, false>(p, st));
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+size_t gqa_kv8_block_bytes(int block_size, int d_head) {
+  if (!block_size_ok(block_size) || (d_head != 64 && d_head != 128)) return 0;
+  return (size_t)kv8_block_bytes(block_size, d_head);
+}
+
+gqa_status gqa_append(const gqa_append_args* args, void* workspace, size_t ws_bytes, void* stream) {
+  try {
+    if (args == nullptr) return GQA_ERR_INVALID_ARG;
+    return append_impl(*args, workspace, ws_bytes, stream);
+  } catch (...) {
+    return GQA_ERR_CUDA;
+  }
+}
+
+size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, int d_head) {
+  try {
+    return check_rows(num_seqs, T_q, h_q, h_kv, d_head) == GQA_OK ? kHeaderBytes : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
+                          uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
+                          int h_q, int h_kv, int d_head, float scale, void* workspace, size_t ws_bytes, void* stream,
+                          const gqa_options* opt) {
+  try {
+    return decode_kv8_impl(q, cache, block_tables, seq_lens, o, num_seqs, T_q, max_blocks_per_seq, num_blocks,
+                           block_size, h_q, h_kv, d_head, scale, workspace, ws_bytes, stream, opt);
+  } catch (...) {
+    return GQA_ERR_CUDA;
+  }
+}
+
+gqa_status gqa_kv8_read(const void* cache, const int32_t* block_tables, const int32_t* seq_lens, const int32_t* begins,
+                        uint16_t* k_out, uint16_t* v_out, int num_seqs, int64_t out_len, int max_blocks_per_seq,
+                        int num_blocks, int block_size, int h_kv, int d_head, void* workspace, size_t ws_bytes,
+                        void* stream, const gqa_options* opt) {
+  try {
+    return read_impl(cache, block_tables, seq_lens, begins, k_out, v_out, num_seqs, out_len, max_blocks_per_seq,
+                     num_blocks, block_size, h_kv, d_head, workspace, ws_bytes, stream, opt);
+  } catch (...) {
+    return GQA_ERR_CUDA;
+  }
+}
+
+}  // extern "C"

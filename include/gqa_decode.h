@@ -289,6 +289,98 @@ gqa_status gqa_decode_paged_vllm_ex(const uint16_t* q, const uint16_t* k_cache, 
                                     int max_seq_len, void* workspace, size_t ws_bytes, void* stream,
                                     const gqa_options* opt);
 
+/* ---------------------------------------------------------------- filling a cache; the 8-bit cache
+ * gqa_append puts new tokens into a paged cache: the norms and the position rotation of their query
+ * and key heads, then the write of K and V, in one pass.  It fills the caches of gqa_decode_paged and
+ * gqa_decode_paged_vllm, and the 8-bit cache "kv8", which gqa_decode_kv8 attends to and gqa_kv8_read
+ * gives back in 16 bits.  These calls have no counterpart on the pages.
+ *
+ * kv8: one byte array (num_blocks, h_kv, block_bytes), block_bytes = block_size * (2 * d_head + 2),
+ * block_size in {8, 16, 32, 64}.  A (block, head) holds
+ *   block_size rows of d_head K codes, block_size rows of d_head V codes  (e4m3 bytes),
+ *   block_size K exponents, block_size V exponents                        (bytes e: the scale 2^(e-127));
+ * the 16-byte chunk c of row r of K or V is stored at chunk c ^ (r % 8) of the row for d_head 128 and at
+ * chunk c ^ (r / 2 % 4) for d_head 64.  A row x (one token, one head) is stored as the codes
+ * e4m3(x * 2^-k), rounded to nearest even, k the smallest integer with max|x| <= 448 * 2^k, at least
+ * -126 (a row of zeros: -126), and the exponent byte k + 127.  NaN is stored as NaN; an infinity makes
+ * k = 120 and is stored as +-448. */
+#define GQA_CACHE_ROWS 0   /* k, v pools (num_blocks, block_size, h_kv*d_head) 16-bit: gqa_decode_paged */
+#define GQA_CACHE_VLLM 1   /* k (num_blocks, h_kv, d_head/8, block_size, 8), v (num_blocks, h_kv, d_head, block_size) */
+#define GQA_CACHE_KV8 2    /* the 8-bit cache above, K and V in one array */
+
+/* Bytes of one (block, head) of the 8-bit cache: block_size * (2 * d_head + 2); 0 for a block size or
+ * d_head that it does not have. */
+size_t gqa_kv8_block_bytes(int block_size, int d_head);
+
+/* Arguments of gqa_append.  Token t's heads are h*d_head .. (h+1)*d_head - 1 of row t of q, k and v; rows
+ * are q_stride, k_stride, v_stride elements apart (multiples of 8, so that views of one fused projection
+ * serve), pointers 16-byte aligned. */
+typedef struct {
+  const uint16_t* q;        /* (num_tokens, h_q*d_head), or NULL with h_q = 0 */
+  const uint16_t* k;        /* (num_tokens, h_kv*d_head) */
+  const uint16_t* v;        /* (num_tokens, h_kv*d_head) */
+  uint16_t* q_out;          /* the queries after norm and rotation; may be q itself */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const uint16_t* q_weight; /* (d_head) weight of the norm of every query head, NULL = no norm */
+  const uint16_t* k_weight; /* the same for the key heads */
+  const float* cos_sin;     /* (max_position, rot_dim): rot_dim/2 cosines, then rot_dim/2 sines; NULL = no rotation */
+  const int32_t* positions; /* (num_tokens) row of cos_sin of each token; not read without cos_sin */
+  const int64_t* slots;     /* (num_tokens) block * block_size + row; negative: the token's K and V are not stored */
+  void* k_cache;            /* the pool of cache_layout (kv8: the one array) */
+  void* v_cache;            /* NULL for kv8 */
+  int num_tokens;
+  int h_q, h_kv, d_head;
+  int max_position;         /* rows of cos_sin */
+  int rot_dim;              /* leading elements of a head that are rotated: a multiple of 8 up to d_head */
+  int interleaved;          /* 0: element i turns with i + rot_dim/2; 1: element 2i with 2i + 1 */
+  int num_blocks, block_size;
+  int cache_layout;         /* GQA_CACHE_* */
+  int bf16;                 /* q, k, v, the weights, q_out and a 16-bit cache hold bfloat16 instead of binary16 */
+  float eps;                /* of the norms, >= 0 */
+} gqa_append_args;
+
+/* For every token: y = x * (mean(x^2) + eps)^(-1/2) * weight for each query and key head (where its weight
+ * is given), the rotation (a, b) -> (a cos - b sin, b cos + a sin) of its pairs, both in fp32; the queries
+ * rounded once to q_out, the keys and the unchanged values rounded once into the cache row of the token's
+ * slot.  Slots of one call must be distinct (negative ones aside): two tokens with one slot leave a mix.
+ * Nothing else in the cache is written.  block_size in {8, 16, 32, 64}.
+ * A slot outside the cache is not stored, a token whose position is outside the table leaves neither
+ * q_out nor a cache row, and gqa_workspace_check reports both as GQA_ERR_INVALID_ARG.  The workspace is
+ * its status word: 256 zeroed bytes, or any workspace of this library.  num_tokens = 0 is a no-op. */
+gqa_status gqa_append(const gqa_append_args* args, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of gqa_decode_kv8 on the current device; 0 on invalid arguments or when no device is
+ * usable. */
+size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, int d_head);
+
+/* Decode step over the 8-bit cache.
+ *   q (num_seqs, T_q, h_q*d_head) 16-bit     cache (num_blocks, h_kv, block_bytes)
+ *   block_tables (num_seqs, max_blocks_per_seq) int32, seq_lens (num_seqs) int32 as gqa_decode_paged
+ *   o (num_seqs, T_q, h_q*d_head) 16-bit, written
+ * G * T_q <= 64.  seq_lens count the T_q new tokens when they are in the cache (gqa_append before this
+ * call).  gqa_options used: bf16, causal (token t sees the keys j <= len - T_q + t; a token that sees no
+ * key gets O = 0, as does a sequence of length 0), timeout_us, test_stall_cta (the index of one worker --
+ * a group of warps that streams one share of all keys -- whose second tile is never loaded).  Sequences are
+ * split over the workers evenly, whatever their lengths; results do not depend on other calls and are the
+ * same every time.  Block ids outside [0, num_blocks) are not loaded, lengths outside
+ * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check. */
+gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
+                          uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
+                          int h_q, int h_kv, int d_head, float scale, void* workspace, size_t ws_bytes, void* stream,
+                          const gqa_options* opt);
+
+/* Tokens [begins[b], min(begins[b] + out_len, seq_lens[b])) of every sequence b as 16-bit values (the codes
+ * times their scales, rounded to nearest even), in rows 0, 1, ... of
+ *   k_out, v_out (num_seqs, out_len, h_kv*d_head)
+ * (what gqa_decode takes); rows past a sequence's last token are left as they were.  begins NULL: 0.
+ * k_out or v_out may be NULL.  Block ids outside the cache (their rows are left as they were), negative
+ * begins and lengths outside the table are reported by gqa_workspace_check; the workspace is that status word
+ * (256 zeroed bytes, or any workspace of this library).  gqa_options used: bf16. */
+gqa_status gqa_kv8_read(const void* cache, const int32_t* block_tables, const int32_t* seq_lens, const int32_t* begins,
+                        uint16_t* k_out, uint16_t* v_out, int num_seqs, int64_t out_len, int max_blocks_per_seq,
+                        int num_blocks, int block_size, int h_kv, int d_head, void* workspace, size_t ws_bytes,
+                        void* stream, const gqa_options* opt);
+
 /* Size of the per-GPU device array used by gqa_decode_noalloc: 8 MiB. */
 #define GQA_NOALLOC_SCRATCH_BYTES (8u * 1024u * 1024u)
 
