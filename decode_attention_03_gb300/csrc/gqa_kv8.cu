@@ -3,6 +3,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/gqa_decode.h"
 #include "gqa_host.cuh"
@@ -92,9 +93,89 @@ gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
 }
 
 // ---------------------------------------------------------------- decode
+// Kernel shapes: up to 8 or 16 query rows for one warp, 32 or 64 for two or four warps that share a ring.
+int kv8_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 3)); }
+int kv8_groups(int cls) { return cls < 2 ? kKv8Warps : (cls == 2 ? kKv8Warps / 2 : kKv8Warps / 4); }
+
+struct Kv8Device {
+  int sms = 0;
+  bool ready[2][4][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
+};
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+Kv8Device g_kv8[kMaxDevices];
+
+template <int D, int NT, int RG, bool BF16>
+cudaError_t kv8_prepare() {
+  return cudaFuncSetAttribute(gqa_decode_kv8_kernel<D, NT, RG, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Kv8Cfg<D, RG>::SMEM);
+}
+
 template <int D, bool BF16>
-cudaError_t decode_launch(const Kv8Params& p, cudaStream_t st) {
-  return launch_pdl(gqa_decode_kv8_kernel<D, BF16>, (unsigned)((int64_t)p.N * p.T_q * p.h_q), kKv8Warps * 32, st, p);
+cudaError_t kv8_prepare_class(int cls) {
+  switch (cls) {
+    case 0: return kv8_prepare<D, 1, 1, BF16>();
+    case 1: return kv8_prepare<D, 2, 1, BF16>();
+    case 2: return kv8_prepare<D, 2, 2, BF16>();
+    default: return kv8_prepare<D, 2, 4, BF16>();
+  }
+}
+
+// SMs of the current device; the kernel of (D, cls, bf16) is ready to launch on it
+gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GQA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_mu);
+  Kv8Device& d = g_kv8[dev];
+  if (d.sms == 0 && cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    d.sms = 0;
+    return GQA_ERR_CUDA;
+  }
+  bool& ready = d.ready[D == 64 ? 0 : 1][cls][bf16];
+  if (!ready) {
+    const cudaError_t e = D == 64 ? (bf16 ? kv8_prepare_class<64, true>(cls) : kv8_prepare_class<64, false>(cls))
+                                  : (bf16 ? kv8_prepare_class<128, true>(cls) : kv8_prepare_class<128, false>(cls));
+    if (e != cudaSuccess) return GQA_ERR_CUDA;
+    ready = true;
+  }
+  *sms = d.sms;
+  return GQA_OK;
+}
+
+struct Kv8Layout {
+  size_t prefix, m, l, o, total;
+};
+
+// workspace: the status header, the tiles before each sequence of a launch, two partials for each worker
+Kv8Layout kv8_layout(int workers, int rows, int D) {
+  Kv8Layout L;
+  const size_t n = 2 * (size_t)workers * rows;
+  L.prefix = kHeaderBytes;
+  L.m = L.prefix + align256((kKv8Seqs + 1) * sizeof(int64_t));
+  L.l = L.m + align256(n * 4);
+  L.o = L.l + align256(n * 4);
+  L.total = L.o + align256(n * D * 4);
+  return L;
+}
+
+template <int D, int NT, int RG, bool BF16>
+cudaError_t kv8_launch(const Kv8Params& p, unsigned grid, cudaStream_t st) {
+  return launch_pdl_smem(gqa_decode_kv8_kernel<D, NT, RG, BF16>, grid, kKv8Threads, Kv8Cfg<D, RG>::SMEM, st, p);
+}
+
+template <int D, bool BF16>
+cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool many_pieces, cudaStream_t st) {
+  cudaError_t e;
+  switch (cls) {
+    case 0: e = kv8_launch<D, 1, 1, BF16>(p, grid, st); break;
+    case 1: e = kv8_launch<D, 2, 1, BF16>(p, grid, st); break;
+    case 2: e = kv8_launch<D, 2, 2, BF16>(p, grid, st); break;
+    default: e = kv8_launch<D, 2, 4, BF16>(p, grid, st); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)p.N * p.T_q * p.h_q, warps = kMergeThreads / 32;
+  if (many_pieces) return launch_pdl(gqa_kv8_merge_kernel<D, BF16, 8>, (unsigned)rows, kMergeThreads, st, p);
+  return launch_pdl(gqa_kv8_merge_kernel<D, BF16, 1>, (unsigned)((rows + warps - 1) / warps), kMergeThreads, st, p);
 }
 
 gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* tables, const int32_t* lens,
@@ -106,21 +187,53 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   if (s == GQA_OK) s = check_kv8(N, h_kv, D, max_blocks, num_blocks, block_size);
   if (s != GQA_OK) return s;
   if (!std::isfinite(scale)) return GQA_ERR_INVALID_ARG;
+  if ((int64_t)(N < kKv8Seqs ? N : kKv8Seqs) * T_q * h_q >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
   if (N == 0) return GQA_OK;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(ws) || !aligned_to(tables, 4) ||
       !aligned_to(lens, 4))
     return GQA_ERR_INVALID_ARG;
   if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
+  const int rows = h_q / h_kv * T_q, cls = kv8_class(rows), bf16 = opt.bf16 ? 1 : 0;
+  int sms = 0;
+  if ((s = kv8_device(D, cls, bf16, &sms)) != GQA_OK) return s;
+  const Kv8Layout lay = kv8_layout(sms * kv8_groups(cls), rows, D);
+  if (ws_bytes < lay.total) return GQA_ERR_WORKSPACE;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
   Kv8Params p = {};
-  p.q = q; p.o = o; p.cache = static_cast<const uint8_t*>(cache);
-  p.block_tables = tables; p.seq_lens = lens; p.status = static_cast<uint32_t*>(ws);
-  p.N = N; p.T_q = T_q; p.h_q = h_q; p.h_kv = h_kv; p.G = h_q / h_kv; p.rows = p.G * T_q;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.status = reinterpret_cast<uint32_t*>(wsb);
+  p.prefix = reinterpret_cast<int64_t*>(wsb + lay.prefix);
+  p.ws_m = reinterpret_cast<float*>(wsb + lay.m);
+  p.ws_l = reinterpret_cast<float*>(wsb + lay.l);
+  p.ws_o = reinterpret_cast<float*>(wsb + lay.o);
+  p.T_q = T_q; p.h_q = h_q; p.h_kv = h_kv; p.G = h_q / h_kv; p.rows = rows;
   p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size;
+  p.bs_log = block_size == 8 ? 3 : (block_size == 16 ? 4 : (block_size == 32 ? 5 : 6));
   p.causal = opt.causal ? 1 : 0;
+  p.stall = opt.test_stall_cta;
   p.scale_log2 = scale * kLog2e;
+  p.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 64) return cuda_status(opt.bf16 ? decode_launch<64, true>(p, st) : decode_launch<64, false>(p, st));
-  return cuda_status(opt.bf16 ? decode_launch<128, true>(p, st) : decode_launch<128, false>(p, st));
+  const int64_t seq_tiles = ((int64_t)max_blocks * block_size + kKv8Keys - 1) / kKv8Keys;
+  for (int b0 = 0; b0 < N; b0 += kKv8Seqs) {
+    p.N = N - b0 < kKv8Seqs ? N - b0 : kKv8Seqs;
+    p.q = q + (int64_t)b0 * T_q * h_q * D;
+    p.o = o + (int64_t)b0 * T_q * h_q * D;
+    p.block_tables = tables + (int64_t)b0 * max_blocks;
+    p.seq_lens = lens + b0;
+    // as many CTAs as there can be tiles, at most one on each SM
+    const int64_t units = (int64_t)p.N * h_kv;
+    const unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
+    p.workers = (int)grid * kv8_groups(cls);
+    // pieces of a unit: about workers / units + 1 when the sequences are alike
+    const bool many = p.workers / units >= kMergeChunk - 1;
+    const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, many, st)
+                                          : kv8_decode<64, false>(p, cls, grid, many, st))
+                                  : (bf16 ? kv8_decode<128, true>(p, cls, grid, many, st)
+                                          : kv8_decode<128, false>(p, cls, grid, many, st));
+    if (e != cudaSuccess) return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
 }
 
 // ---------------------------------------------------------------- read
@@ -183,7 +296,11 @@ gqa_status gqa_append(const gqa_append_args* args, void* workspace, size_t ws_by
 
 size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, int d_head) {
   try {
-    return check_rows(num_seqs, T_q, h_q, h_kv, d_head) == GQA_OK ? kHeaderBytes : 0;
+    if (check_rows(num_seqs, T_q, h_q, h_kv, d_head) != GQA_OK) return 0;
+    const int rows = h_q / h_kv * T_q, cls = kv8_class(rows);
+    int sms = 0;
+    if (kv8_device(d_head, cls, 0, &sms) != GQA_OK) return 0;
+    return kv8_layout(sms * kv8_groups(cls), rows, d_head).total;
   } catch (...) {
     return 0;
   }

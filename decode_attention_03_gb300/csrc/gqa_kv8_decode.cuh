@@ -1,8 +1,38 @@
 // Decode attention over the 8-bit cache.
+//
+// Work: every (sequence, KV head) is a row of 32-key tiles; all tiles of a launch lie on one axis, which is
+// cut into equal shares, one for each worker (a worker is RG warps, GROUPS of them on a CTA, one CTA on an
+// SM).  The cut does not look at sequences: a share may hold many short ones or a part of a long one, so
+// every worker streams the same bytes whatever the lengths are, and nothing is claimed or counted at run
+// time.  A (sequence, head) that lies inside one share is finished by its worker; the others leave partials
+// (m, l, O) that a merge kernel folds in the order of the keys.
+//
+// A worker streams its tiles through a ring of its own in shared memory: one plain bulk copy for each block
+// (32 keys are 32/block_size of them), K, V and scales together.  No warp waits for another worker's.
+//
+// Arithmetic of a warp, for its 8 NT query rows and 32 keys.  S^T = K Q^T with keys on the MMA's M side and
+// query rows on its N side (n = 8: with 4 query heads a KV head only half of the tile is idle).  K codes come
+// by ldmatrix -- a thread's 4 bytes are the elements 16j + 4c .. +3 of one key, and since the order of the
+// summed index is free, Q is laid out to match -- and become f16 by one conversion for two codes, exactly.
+// The K scale multiplies the fp32 score, the V scale multiplies the weight: P = p 2^(ev - e), e the largest V
+// exponent so far, so that P <= 2^8 stays in f16's range whatever the scales are (O is rescaled when e grows,
+// together with the running maximum).  V codes come by transposing ldmatrix as byte pairs of two d for each of
+// two keys, one byte permutation turns them into pairs of keys, the MMA's A operand of O^T += V^T P^T.
+// bfloat16 queries are brought into f16's range by a power of two for each row (8 bits of fraction fit into
+// 11: nothing is rounded that fp32 sums would keep); O, m and l are fp32.
+// The running maximum is only moved when a score exceeds it by 2^8: the weights stay below 2^8 and the
+// common tile needs no cross-lane maximum and no rescaling.
 #pragma once
 #include "gqa_kv8.cuh"
+#include "gqa_merge.cuh"   // kMergeThreads, kMergeChunk
 
 namespace gqa {
+
+constexpr int kKv8Keys = 32;                   // keys of a tile
+constexpr int kKv8Seqs = 1024;                 // sequences of a launch (the host splits larger batches)
+constexpr int kKv8Warps = 8;
+constexpr int kKv8Threads = 32 * kKv8Warps;
+constexpr float kKv8Slack = 8.f;               // log2 of the largest weight
 
 struct Kv8Params {
   const uint16_t* q;
@@ -10,90 +40,684 @@ struct Kv8Params {
   const uint8_t* cache;
   const int32_t *block_tables, *seq_lens;
   uint32_t* status;
-  int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, causal;
+  int64_t* prefix;       // [N + 1] tiles (of one head) before each sequence
+  float *ws_m, *ws_l;    // [2 * workers][rows]   m in log2 units
+  float* ws_o;           // [2 * workers][rows][D]
+  int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, bs_log, causal, workers, stall;
   float scale_log2;
+  uint64_t timeout_ns;
 };
 
-constexpr int kKv8Warps = 4;
+// The slots of partials: worker w's first piece 2w, a later piece that it does not finish 2w + 1.
+template <int D, int RG>
+struct Kv8Cfg {
+  static constexpr int GROUPS = kKv8Warps / RG;
+  static constexpr int TILE = kKv8Keys * (2 * D + 2);
+  static constexpr int PREFIX_OFF = 0;
+  static constexpr int LENS_OFF = (kKv8Seqs + 2) * 8;
+  static constexpr int SUMS_OFF = LENS_OFF + kKv8Seqs * 4;
+  static constexpr int FLAG_OFF = SUMS_OFF + kKv8Warps * 8;
+  static constexpr int BAR_OFF = FLAG_OFF + 16;
+  static constexpr int MAX_STAGES = (232448 - BAR_OFF - 256) / (GROUPS * (TILE + 16));
+  static constexpr int STAGES = MAX_STAGES > 12 ? 12 : MAX_STAGES;
+  static constexpr int RING_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
+  static constexpr int SMEM = RING_OFF + GROUPS * STAGES * TILE;
+  static_assert(STAGES >= 3 && SMEM <= 232448, "ring");
+};
 
-// One CTA per (sequence, query token, query head), its warps taking every fourth key: the running
-// maximum, sum and O of each warp in registers, folded through shared memory.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kKv8Warps * 32)
-gqa_decode_kv8_kernel(const Kv8Params a) {
-  constexpr int PER = D / 32;
-  __shared__ float sm[kKv8Warps][D + 2];
-  ptx::grid_dependency_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x;
-  const int h = (int)(r % a.h_q), t = (int)(r / a.h_q % a.T_q);
-  const int64_t b = r / ((int64_t)a.h_q * a.T_q);
-  const int g = h / a.G, cap = a.max_blocks * a.block_size, bb = kv8_block_bytes(a.block_size, D);
-  int len = a.seq_lens[b];
-  if (len < 0 || len > cap) {
-    if (threadIdx.x == 0) atomicOr(a.status, kDevBadInput);
-    len = len < 0 ? 0 : cap;
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// the four e4m3 codes of a word as two pairs of f16
+__device__ __forceinline__ void kv8_unpack(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// 2^(e - 127 + d) for d <= 0, 0 where that leaves the range
+__device__ __forceinline__ float kv8_ratio(int d) { return __uint_as_float((uint32_t)max(d + 127, 0) << 23); }
+
+// A place on the axis of tiles: tile t of the `tiles` tiles of head g of sequence b.
+struct Kv8Place {
+  int b, g, t, tiles;
+};
+
+__device__ __forceinline__ void kv8_next_unit(Kv8Place& p, const int64_t* prefix, int N, int h_kv) {
+  p.t = 0;
+  if (++p.g < h_kv) return;
+  p.g = 0;
+  do {
+    ++p.b;
+  } while (p.b < N && prefix[p.b + 1] == prefix[p.b]);
+  p.tiles = p.b < N ? (int)(prefix[p.b + 1] - prefix[p.b]) : 0;
+}
+
+__device__ __forceinline__ Kv8Place kv8_find(int64_t f, const int64_t* prefix, int N, int h_kv) {
+  int lo = 0, hi = N - 1;   // the first sequence that ends after f
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid + 1] * h_kv > f) hi = mid; else lo = mid + 1;
   }
-  const int end = a.causal ? len - a.T_q + t + 1 : len;
-  float q[PER], acc[PER], m = -CUDART_INF_F, l = 0.f;
+  Kv8Place p;
+  p.b = lo;
+  p.tiles = (int)(prefix[lo + 1] - prefix[lo]);
+  const int64_t rem = f - prefix[lo] * h_kv;
+  p.g = (int)(rem / p.tiles);
+  p.t = (int)(rem - (int64_t)p.g * p.tiles);
+  return p;
+}
+
+// Tiles before each sequence of the launch, in shared memory (and, by CTA 0, in the workspace for the merge).
+__device__ __forceinline__ void kv8_prefix(const Kv8Params& a, int64_t* prefix, int* lens, int64_t* sums) {
+  constexpr int PER = kKv8Seqs / kKv8Threads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t cap = (int64_t)a.max_blocks * a.block_size;
+  int64_t v[PER], run = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const uint16_t x = a.q[r * D + lane * PER + i];
-    q[i] = BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
-    acc[i] = 0.f;
-  }
-  for (int j = warp; j < end; j += kKv8Warps) {
-    const int id = a.block_tables[b * a.max_blocks + j / a.block_size], row = j % a.block_size;
-    if (id < 0 || id >= a.num_blocks) {
-      if (lane == 0) atomicOr(a.status, kDevBadInput);
-      continue;
+    const int b = threadIdx.x * PER + i;
+    int len = b < a.N ? a.seq_lens[b] : 0;
+    if (len < 0 || len > cap) {
+      if (blockIdx.x == 0) atomicOr(a.status, kDevBadInput);
+      len = len < 0 ? 0 : (int)cap;
     }
-    const uint8_t* at = a.cache + ((int64_t)id * a.h_kv + g) * bb;
-    const int off = kv8_chunk<D>(row, lane * PER / 16) + lane * PER % 16;
-    float s = 0.f, v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-      const float2 x = half2_floats(kv8_halves(*reinterpret_cast<const uint16_t*>(at + off + i)));
-      const float2 y = half2_floats(kv8_halves(*reinterpret_cast<const uint16_t*>(at + a.block_size * D + off + i)));
-      s += q[i] * x.x + q[i + 1] * x.y;
-      v[i] = y.x;
-      v[i + 1] = y.y;
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    s *= kv8_scale(at[2 * a.block_size * D + row]) * a.scale_log2;
-    const float m_new = fmaxf(m, s), m_use = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float alpha = ptx::ex2(m - m_use), p = ptx::ex2(s - m_use);
-    const float pv = p * kv8_scale(at[2 * a.block_size * D + a.block_size + row]);
-    m = m_new;
-    l = l * alpha + p;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = acc[i] * alpha + pv * v[i];
+    lens[b] = len;
+    run += ((int64_t)len + kKv8Keys - 1) / kKv8Keys;
+    v[i] = run;
   }
+  int64_t incl = run;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sm[warp][lane * PER + i] = acc[i];
-  if (lane == 0) {
-    sm[warp][D] = m;
-    sm[warp][D + 1] = l;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
   }
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  if (warp != 0) return;
-  float M = -CUDART_INF_F, L = 0.f;
+  int64_t before = incl - run;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  if (threadIdx.x == 0) prefix[0] = 0;
 #pragma unroll
-  for (int k = 0; k < kKv8Warps; ++k) M = fmaxf(M, sm[k][D]);
+  for (int i = 0; i < PER; ++i) {
+    const int b = threadIdx.x * PER + i;
+    if (b < a.N) {
+      prefix[b + 1] = before + v[i];
+      if (blockIdx.x == 0) a.prefix[b + 1] = before + v[i];
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[0] = 0;
+  __syncthreads();
+}
+
+// Block ids of the next tiles of a worker, one for each lane, and its copies.
+struct Kv8Stream {
+  Kv8Place at;       // next tile to copy
+  Kv8Place ahead;    // first tile after the current window
+  int id, id_next;   // this lane's block id in the current window and the one after it
+  int t_end;         // tile of at's unit where the current window ends
+  int j0;            // block index of lane 0 in the current window
+};
+
+// blocks of a sequence, the block that holds a tile's first key, and the tile where the window of 32 blocks
+// that starts at p ends
+__device__ __forceinline__ int kv8_blocks(const Kv8Params& a, int len) {
+  return (int)(((uint32_t)len + (uint32_t)a.block_size - 1) >> a.bs_log);
+}
+__device__ __forceinline__ int kv8_first_block(const Kv8Params& a, int t) {
+  return (int)(((uint32_t)t * (uint32_t)kKv8Keys) >> a.bs_log);
+}
+__device__ __forceinline__ int kv8_window_end(const Kv8Params& a, const Kv8Place& p) {
+  const int n = a.block_size > kKv8Keys ? a.block_size - (p.t & 1) : a.block_size;   // 32 blocks in tiles
+  return p.tiles - p.t < n ? p.tiles : p.t + n;
+}
+
+// this lane's block id of the window that starts at p; *end: the tile where the window ends
+__device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p, const int* lens, int lane, int* end) {
+  if (p.b >= a.N) return -1;
+  *end = kv8_window_end(a, p);
+  const int j = kv8_first_block(a, p.t) + lane;
+  const int used = kv8_blocks(a, lens[p.b]);
+  if (j >= used || !idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status)) return -1;
+  return __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + j);
+}
+
+__device__ __forceinline__ void kv8_ahead(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix) {
+  s.ahead = s.at;
+  s.ahead.t = s.t_end;
+  if (s.t_end >= s.at.tiles) kv8_next_unit(s.ahead, prefix, a.N, a.h_kv);
+}
+
+__device__ __forceinline__ void kv8_start(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
+                                          int lane) {
+  s.j0 = kv8_first_block(a, s.at.t);
+  s.id = kv8_window(a, s.at, lens, lane, &s.t_end);
+  kv8_ahead(s, a, prefix);
+  int end;
+  s.id_next = kv8_window(a, s.ahead, lens, lane, &end);
+}
+
+// Copies the stream's next tile to `dst` and moves on.  Every lane of the warp calls this.
+template <int D>
+__device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
+                                         uint32_t dst, uint32_t bar, uint64_t policy, int lane, const Win& ring) {
+  const int bs = a.block_size;
+  const int64_t bb = kv8_block_bytes(bs, D);
+  const bool half = bs > kKv8Keys;                  // 64: the tile is half a block, in four pieces
+  const int n = half ? 4 : kKv8Keys >> a.bs_log;
+  const int j = kv8_first_block(a, s.at.t) + (half ? 0 : lane);
+  const int src_lane = j - s.j0;
+  const int id = __shfl_sync(0xffffffffu, s.id, src_lane & 31);
+  const bool mine = lane < n && j < kv8_blocks(a, lens[s.at.b]);
+  const bool bad = mine && (id < 0 || id >= a.num_blocks);
+  if (bad) atomicOr(a.status, kDevBadInput);
+  const bool go = mine && !bad;
+  uint32_t size = (uint32_t)bb, to = (uint32_t)lane * (uint32_t)bb;
+  int64_t off = 0;
+  if (half) {
+    const int h = s.at.t & 1;
+    size = lane < 2 ? kKv8Keys * D : kKv8Keys;
+    off = lane < 2 ? (lane * bs + h * kKv8Keys) * D : 2 * bs * D + (lane - 2) * bs + h * kKv8Keys;
+    to = lane < 2 ? lane * kKv8Keys * D : 2 * kKv8Keys * D + (lane - 2) * kKv8Keys;
+  }
+  uint32_t total;
+  if (half) {
+    total = __ballot_sync(0xffffffffu, go) ? kKv8Keys * (2 * D + 2) : 0;
+  } else {
+    total = __popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)bb;
+  }
+  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
+  __syncwarp();
+  if (go) {
+    const int64_t src = ((int64_t)id * a.h_kv + s.at.g) * bb + off;
+    if (idx_ok(src + size - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status) &&
+        smem_ok(dst + to, size, ring.lo, ring.hi, ring.status))
+      bulk_load(dst + to, a.cache + src, size, bar, policy);
+  }
+  // ---- move on
+  if (++s.at.t < s.t_end) return;
+  s.at = s.ahead;
+  s.id = s.id_next;
+  if (s.at.b >= a.N) return;
+  s.j0 = kv8_first_block(a, s.at.t);
+  s.t_end = kv8_window_end(a, s.at);
+  int end;
+  kv8_ahead(s, a, prefix);
+  s.id_next = kv8_window(a, s.ahead, lens, lane, &end);
+}
+
+// RG warps of 16 query rows share a ring (RG > 1: more than 16 rows), NT n-tiles of 8 rows a warp.
+template <int D, int NT, int RG>
+struct Kv8Warp {
+  static constexpr int KD = D / 16;
+  uint32_t qf[NT][KD][2];
+  float acc[KD][NT][4];
+  float m[NT][2], l[NT][2], qs[NT][2];
+  int lim[NT][2];       // last key each of this lane's rows sees
+  int e;                // largest V exponent byte so far
+  // the same for every unit and tile
+  int64_t q_off[NT];    // element offset of this lane's query row from the unit's first (negative: no row)
+  int back[NT][2];      // causal: keys hidden from this lane's rows at the end
+  uint32_t rows[2];     // byte offset in a tile of this lane's ldmatrix row, keys 16p + lane % 16
+  uint32_t ex[4];       // and of the K exponent of key 8o + lane / 4
+  uint32_t turn;        // chunk swizzle of that row, and which of two chunks this lane addresses
+};
+
+template <int D, int NT, int RG>
+__device__ __forceinline__ void kv8_setup(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int rg, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+  const int eb = min(a.block_size, kKv8Keys), bb = kv8_block_bytes(eb, D);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = (rg * NT + nt) * 8 + r, t = row / a.G;
+    w.q_off[nt] = row < a.rows ? ((int64_t)t * a.h_q + (row - t * a.G)) * D + 4 * c : -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w.back[nt][i] = a.causal ? max(a.T_q - 1 - ((rg * NT + nt) * 8 + 2 * c + i) / a.G, 0) : 0;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int key = 16 * p + (lane & 15);
+    w.rows[p] = key / eb * bb + key % eb * D;
+  }
+#pragma unroll
+  for (int o = 0; o < 4; ++o) {
+    const int key = 8 * o + r;
+    w.ex[o] = key / eb * bb + 2 * eb * D + key % eb;
+  }
+  w.turn = (uint32_t)((lane >> 4) ^ (D == 128 ? (lane & 7) : ((lane >> 1) & 3))) << 4;
+}
+
+template <int D, int NT, int RG, bool BF16>
+__device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int len,
+                                          int lane) {
+  constexpr int KD = Kv8Warp<D, NT, RG>::KD;
+  const int c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    uint2 raw[KD];
+    const int64_t at = ((int64_t)b * a.T_q * a.h_q + (int64_t)g * a.G) * D + w.q_off[nt];
+    const bool ok = w.q_off[nt] >= 0 && idx_ok(at + D - 1 - 4 * c, (int64_t)a.N * a.T_q * a.h_q * D, a.status);
+#pragma unroll
+    for (int j = 0; j < KD; ++j)
+      raw[j] = ok ? __ldg(reinterpret_cast<const uint2*>(a.q + at + 16 * j)) : make_uint2(0u, 0u);
+    float qs = a.scale_log2;
+    if constexpr (BF16) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < KD; ++j)
+        top = max(max(top, max(raw[j].x & 0x7fffu, (raw[j].x >> 16) & 0x7fffu)),
+                  max(raw[j].y & 0x7fffu, (raw[j].y >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t e = max(top >> 7, 15u);                    // the row's largest value becomes 2^14 .. 2^15
+      const float up = __uint_as_float((268u - e) << 23);
+      qs *= __uint_as_float((e - 14u) << 23);
+#pragma unroll
+      for (int j = 0; j < KD; ++j) {
+        float x[4];
+        unpack4<true>(raw[j], x);
+        w.qf[nt][j][0] = ptx::pack_half2(x[0] * up, x[1] * up);
+        w.qf[nt][j][1] = ptx::pack_half2(x[2] * up, x[3] * up);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < KD; ++j) {
+        w.qf[nt][j][0] = raw[j].x;
+        w.qf[nt][j][1] = raw[j].y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w.qs[nt][i] = __shfl_sync(0xffffffffu, qs, (2 * c + i) * 4);
+      w.lim[nt][i] = len - 1 - w.back[nt][i];
+      w.m[nt][i] = -CUDART_INF_F;
+      w.l[nt][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < KD; ++j)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.acc[j][nt][i] = 0.f;
+  w.e = 1;
+}
+
+// One tile of `valid` keys (key0 the first), `st` its place in the ring; masked: some key of it is hidden
+// from some row.
+template <int D, int NT, int RG>
+__device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, uint32_t st, int eb, int valid, int key0, bool masked,
+                                         int lane, const Win& ring) {
+  constexpr int KD = Kv8Warp<D, NT, RG>::KD;
+  const int r = lane >> 2;
+  if (valid < kKv8Keys) {
+    // V rows that hold no key: zeros, so that a weight of 0 meets no NaN.  Then the writes are ordered before
+    // the next copy into this place.
+    for (int i = lane; i < (kKv8Keys - valid) * KD; i += 32) {
+      const int key = valid + i / KD;
+      const uint32_t to = st + key / eb * kv8_block_bytes(eb, D) + (eb + key % eb) * D + i % KD * 16;
+      if (smem_ok(to, 16, ring.lo, ring.hi, ring.status))
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+  }
+  // ---- exponents of this lane's keys 8o + r
+  int ek[4], ev[4], top = 1;
+#pragma unroll
+  for (int o = 0; o < 4; ++o) {
+    uint32_t x, y;
+    const uint32_t at = smem_clamp(st + w.ex[o], 1, ring.lo, ring.hi, ring.status);
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at));
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(smem_clamp(st + w.ex[o] + eb, 1, ring.lo, ring.hi, ring.status)));
+    ek[o] = (int)x;
+    ev[o] = 8 * o + r < valid ? (int)y : 1;
+    top = max(top, ev[o]);
+  }
+  // ---- S^T = K Q^T
+  float s[2][NT][4];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[p][nt][0] = s[p][nt][1] = s[p][nt][2] = s[p][nt][3] = 0.f;
+#pragma unroll
+  for (int j = 0; j < KD; j += 2)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t x[4], f[2][4];
+      ptx::ldmatrix_x4(x, smem_clamp(st + w.rows[p] + ((uint32_t)(j << 4) ^ w.turn), 16, ring.lo, ring.hi, ring.status));
+      kv8_unpack(x[0], f[0][0], f[0][2]);
+      kv8_unpack(x[1], f[0][1], f[0][3]);
+      kv8_unpack(x[2], f[1][0], f[1][2]);
+      kv8_unpack(x[3], f[1][1], f[1][3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        ptx::mma_16816(s[p][nt], f[0], w.qf[nt][j]);
+        ptx::mma_16816(s[p][nt], f[1], w.qf[nt][j + 1]);
+      }
+    }
+  // ---- scores in log2 units; s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
+  top = __reduce_max_sync(0xffffffffu, top);
+  bool over = false;
+  float mx[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        float& x = s[o >> 1][nt][(o & 1) * 2 + i];
+        x = x * w.qs[nt][i] * kv8_scale((uint32_t)ek[o]);
+        if (masked && 8 * o + r > w.lim[nt][i] - key0) x = -CUDART_INF_F;
+      }
+      mx[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i]));
+      over |= mx[nt][i] > w.m[nt][i] + kKv8Slack;
+    }
+  const bool grow = __any_sync(0xffffffffu, over);
+  if (grow || top > w.e) {
+    const int e = max(top, w.e);
+    const float fe = kv8_ratio(w.e - e);
+    w.e = e;
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[nt][i] = fe;
+        if (grow) {
+          float x = mx[nt][i];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, w.m[nt][i]);
+          const float alpha = ptx::ex2(w.m[nt][i] - (x == -CUDART_INF_F ? 0.f : x));
+          w.m[nt][i] = x;
+          w.l[nt][i] *= alpha;
+          f[nt][i] *= alpha;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < KD; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f[nt][i & 1];
+  }
+  // ---- weights, and P as the B operand
+  float fv[4];
+#pragma unroll
+  for (int o = 0; o < 4; ++o) fv[o] = kv8_ratio(ev[o] - w.e);
+  uint32_t pf[2][NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] = w.m[nt][i] == -CUDART_INF_F ? 0.f : w.m[nt][i];
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+      const float p0 = ptx::ex2(s[o >> 1][nt][(o & 1) * 2] - u[0]);
+      const float p1 = ptx::ex2(s[o >> 1][nt][(o & 1) * 2 + 1] - u[1]);
+      w.l[nt][0] += p0;
+      w.l[nt][1] += p1;
+      pf[o >> 1][nt][o & 1] = ptx::movmatrix_trans(ptx::pack_half2(p0 * fv[o], p1 * fv[o]));
+    }
+  }
+  // ---- O^T += V^T P^T; accumulator rows r, r + 8 of tile j: d = 16j + 2r, 16j + 2r + 1
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int j = 0; j < KD; j += 2) {
+      uint32_t x[4], f[2][4];
+      ptx::ldmatrix_x4_trans(x, smem_clamp(st + w.rows[p] + eb * D + ((uint32_t)(j << 4) ^ w.turn), 16, ring.lo, ring.hi,
+                                           ring.status));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kv8_unpack(__byte_perm(x[i], 0, 0x3120), f[i >> 1][(i & 1) * 2], f[i >> 1][(i & 1) * 2 + 1]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        ptx::mma_16816(w.acc[j][nt], f[0], pf[p][nt]);
+        ptx::mma_16816(w.acc[j + 1][nt], f[1], pf[p][nt]);
+      }
+    }
+}
+
+// The end of a piece: the whole unit's output, or the partial of slot >= 0.
+template <int D, int NT, int RG, bool BF16>
+__device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int64_t slot, int rg,
+                                        int lane) {
+  constexpr int KD = Kv8Warp<D, NT, RG>::KD;
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float l = w.l[nt][i];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int row = (rg * NT + nt) * 8 + 2 * c + i;
+      if (row >= a.rows) continue;
+      const float unit = kv8_scale((uint32_t)w.e);
+      if (slot < 0) {
+        const int t = row / a.G;
+        const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D;
+        if (!idx_ok(at + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) continue;
+        const float f = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int j = 0; j < KD; ++j)
+          Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at + 16 * j + 2 * r, w.acc[j][nt][i] * f * unit,
+                             w.acc[j][nt][2 + i] * f * unit);
+      } else {
+        const int64_t at = slot * a.rows + row;
+        if (!idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status)) continue;
+#pragma unroll
+        for (int j = 0; j < KD; ++j)
+          *reinterpret_cast<float2*>(a.ws_o + at * D + 16 * j + 2 * r) =
+              make_float2(w.acc[j][nt][i] * unit, w.acc[j][nt][2 + i] * unit);
+        if (r == 0) {
+          a.ws_m[at] = w.m[nt][i];
+          a.ws_l[at] = l;
+        }
+      }
+    }
+}
+
+template <int D, int NT, int RG, bool BF16>
+__global__ void __launch_bounds__(kKv8Threads, 1)
+gqa_decode_kv8_kernel(const Kv8Params a) {
+  using C = Kv8Cfg<D, RG>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::PREFIX_OFF);
+  int* lens = reinterpret_cast<int*>(smem + C::LENS_OFF);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp / RG, rg = warp % RG;
+  const uint32_t full = ptx::smem_u32(smem + C::BAR_OFF) + grp * STAGES * 16, empty = full + STAGES * 8;
+  if (threadIdx.x < C::GROUPS * STAGES) {
+    const uint32_t f = ptx::smem_u32(smem + C::BAR_OFF) + threadIdx.x / STAGES * STAGES * 16 + threadIdx.x % STAGES * 8;
+    ptx::mbar_init(f, 1);
+    ptx::mbar_init(f + STAGES * 8, RG);
+  }
+  if (threadIdx.x == 0) *abort = 0;
+  ptx::fence_mbar_init();
+  ptx::grid_dependency_wait();
+  kv8_prefix(a, prefix, lens, reinterpret_cast<int64_t*>(smem + C::SUMS_OFF));
+  if (threadIdx.x == 0) ptx::grid_launch_dependents();
+
+  const int64_t total = prefix[a.N] * a.h_kv;
+  const int64_t share = (total + a.workers - 1) / a.workers;
+  const int64_t wk = (int64_t)grp * gridDim.x + blockIdx.x;
+  const int64_t f0 = wk * share, f1 = f0 + share < total ? f0 + share : total;
+  if (f0 >= f1) return;
+  const int n = (int)(f1 - f0);
+  Kv8Place at = kv8_find(f0, prefix, a.N, a.h_kv);
+  const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
+  const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
+  const uint64_t policy = ptx::policy_evict_first();
+  const int eb = min(a.block_size, kKv8Keys);
+  Kv8Stream str;
+  int issued = 0;
+  if (rg == 0) {
+    str.at = at;
+    kv8_start(str, a, prefix, lens, lane);
+    for (; issued < n && issued < STAGES; ++issued)
+      if (!(issued == 1 && wk == a.stall))
+        kv8_copy<D>(str, a, prefix, lens, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
+  }
+  Kv8Warp<D, NT, RG> w;
+  kv8_setup(w, a, rg, lane);
+  int len = lens[at.b];
+  kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, lane);
+  bool fresh = at.t == 0;        // this piece begins with its unit
+  int64_t slot = 2 * wk;         // where it goes when it is not the whole unit
+  int i = 0, stage = 0, phase = 0;
+  for (; i < n; ++i) {
+    if (!ptx::mbar_wait_bounded(full + stage * 8, phase, a.timeout_ns, abort)) break;
+    const int key0 = at.t * kKv8Keys;
+    const int valid = min(len - key0, kKv8Keys);
+    const int sees = a.causal ? len - a.T_q : len - 1;       // the fewest keys that a row sees
+    kv8_tile<D, NT, RG>(w, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, lane, ring);
+    __syncwarp();
+    if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
+    if (rg == 0 && i + STAGES < n) {
+      if (RG > 1 && !ptx::mbar_wait_bounded(empty + stage * 8, phase, a.timeout_ns, abort)) {
+        ++i;
+        break;
+      }
+      kv8_copy<D>(str, a, prefix, lens, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
+      ++issued;
+    }
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (++at.t == at.tiles || i + 1 == n) {
+      const bool whole = fresh && at.t == at.tiles;
+      kv8_end<D, NT, RG, BF16>(w, a, at.b, at.g, whole ? -1 : slot, rg, lane);
+      if (i + 1 < n) {
+        kv8_next_unit(at, prefix, a.N, a.h_kv);
+        len = lens[at.b];
+        kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, lane);
+        fresh = true;
+        slot = 2 * wk + 1;
+      }
+    }
+  }
+  if (i < n) {
+    // a wait gave up: tell the others and wait (bounded) for this worker's copies in flight
+    if (lane == 0) {
+      atomicOr(a.status, kDevTimeout);
+      *abort = 1;
+    }
+    if (rg == 0)
+      for (int k = i; k < issued; ++k)
+        ptx::mbar_wait_bounded(full + k % STAGES * 8, k / STAGES & 1, a.timeout_ns, nullptr);
+  }
+}
+
+// Folds the pieces of every unit that more than one worker streamed, in the order of its keys, and writes the
+// rows of empty sequences.  W warps a row.
+template <int D, bool BF16, int W>
+__global__ void __launch_bounds__(kMergeThreads)
+gqa_kv8_merge_kernel(const Kv8Params a) {
+  constexpr int PER = D / 32, RPB = kMergeThreads / (32 * W);
+  __shared__ float sm[RPB][W * (D + 2)];
+  if (threadIdx.x == 0) ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = warp / W, w = warp % W;
+  const int64_t R = (int64_t)a.N * a.T_q * a.h_q, r = (int64_t)blockIdx.x * RPB + rr;
+  int n = 0, row = 0, first = 0;
+  int64_t w0 = 0, tiles = -1;
+  if (r < R) {
+    const int h = (int)(r % a.h_q);
+    const int64_t bt = r / a.h_q;
+    const int t = (int)(bt % a.T_q), b = (int)(bt / a.T_q), g = h / a.G;
+    row = t * a.G + h - g * a.G;
+    const int64_t p0 = __ldcg(a.prefix + b);
+    tiles = __ldcg(a.prefix + b + 1) - p0;
+    if (tiles > 0) {
+      const int64_t total = __ldcg(a.prefix + a.N) * a.h_kv, share = (total + a.workers - 1) / a.workers;
+      const int64_t start = p0 * a.h_kv + g * tiles;
+      w0 = start / share;
+      n = (int)((start + tiles - 1) / share - w0) + 1;
+      first = start > w0 * share ? 1 : 0;
+    }
+  }
+  if (n == 1) n = 0;            // written by its worker
+  else if (tiles == 0) n = -1;  // nothing to attend to: zeros
+  float M = -CUDART_INF_F, L = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  for (int s0 = w; s0 < n; s0 += W * kMergeChunk) {
+    float mj[kMergeChunk], lj[kMergeChunk], oj[kMergeChunk][PER];
 #pragma unroll
-  for (int k = 0; k < kKv8Warps; ++k) {
-    const float f = M == -CUDART_INF_F ? 0.f : ptx::ex2(sm[k][D] - M);
-    L += f * sm[k][D + 1];
+    for (int j = 0; j < kMergeChunk; ++j) {
+      const int s = s0 + j * W;
+      const int64_t at = (2 * (w0 + s) + (s == 0 ? first : 0)) * a.rows + row;
+      const bool have = s < n && idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status);
+      mj[j] = have ? __ldcg(a.ws_m + at) : -CUDART_INF_F;
+      lj[j] = have ? __ldcg(a.ws_l + at) : 0.f;
+      const float* src = a.ws_o + at * D + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 v = have ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        oj[j][0] = v.x; oj[j][1] = v.y; oj[j][2] = v.z; oj[j][3] = v.w;
+      } else {
+        const float2 v = have ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+        oj[j][0] = v.x; oj[j][1] = v.y;
+      }
+    }
+    float Mc = M;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += f * sm[k][lane * PER + i];
+    for (int j = 0; j < kMergeChunk; ++j) Mc = fmaxf(Mc, mj[j]);
+    if (Mc == -CUDART_INF_F) continue;
+    const float so = ptx::ex2(M - Mc);
+    L *= so;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] *= so;
+#pragma unroll
+    for (int j = 0; j < kMergeChunk; ++j) {
+      const float f = ptx::ex2(mj[j] - Mc);
+      L += f * lj[j];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += f * oj[j][i];
+    }
+    M = Mc;
   }
+  if constexpr (W > 1) {
+    float* mine = sm[rr] + w * (D + 2);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[lane * PER + i] = acc[i];
+    if (lane == 0) {
+      mine[D] = M;
+      mine[D + 1] = L;
+    }
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int k = 0; k < W; ++k) M = fmaxf(M, sm[rr][k * (D + 2) + D]);
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    if (M != -CUDART_INF_F)
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float* wk = sm[rr] + k * (D + 2);
+        const float f = ptx::ex2(wk[D] - M);
+        L += f * wk[D + 1];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += f * wk[lane * PER + i];
+      }
+  }
+  if (n == 0) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    Elem<BF16>::store(reinterpret_cast<__half*>(a.o), r * D + lane * PER + i, acc[i] * inv);
+  for (int i = 0; i < PER; i += 2)
+    Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), r * D + lane * PER + i, acc[i] * inv, acc[i + 1] * inv);
 }
 
 }  // namespace gqa

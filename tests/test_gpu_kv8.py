@@ -481,6 +481,21 @@ def test_decode_reports_bad_blocks_and_lengths(gqa):
     assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
 
 
+@pytest.mark.parametrize("hq,worker", [(16, 3), (64, 1), (256, 0)])
+def test_decode_timeout_is_reported_not_hung(gqa, hq, worker):
+    """A worker whose second tile never comes (one warp, two and four warps on a ring)."""
+    D, hk, bs = 128, 4, 16
+    lens = [4000] * 8
+    cache, tab = make_cache(lens, D, hk, bs, 105)
+    q = torch.randn(8, hq * D, generator=gen(15)).half()
+    ws = torch.zeros(gqa.gqa_decode_kv8_workspace_size(8, 1, hq, hk, D), dtype=torch.uint8, device="cuda")
+    run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws, timeout_us=20000, test_stall_cta=worker)
+    assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_TIMEOUT
+    o = run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws)
+    assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+    check_decode(o[:2], cache, tab[:2], lens[:2], q[:2], hq, hk, D, D ** -0.5, bs, False, "f16", "after a timeout")
+
+
 def test_offsets_past_32_bits(gqa):
     """Blocks behind the first 4 GiB of a cache, written, attended to and read back."""
     D, hk, bs, hq = 128, 8, 64, 32
