@@ -19,15 +19,64 @@ bool aligned_to(const void* p, uintptr_t n) { return p != nullptr && (reinterpre
 
 gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
 
+// ---------------------------------------------------------------- per-device state
+struct Kv8Device {
+  int sms = 0;
+  bool ready[2][4][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
+};
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+Kv8Device g_kv8[kMaxDevices];
+
+// SMs of the current device, with g_mu held by the caller
+gqa_status device_locked(Kv8Device** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GQA_ERR_CUDA;
+  Kv8Device& d = g_kv8[dev];
+  if (d.sms == 0 && cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    d.sms = 0;
+    return GQA_ERR_CUDA;
+  }
+  *out = &d;
+  return GQA_OK;
+}
+
 // ---------------------------------------------------------------- append
-template <int D, bool BF16, int U>
-cudaError_t append_launch(AppendParams p, cudaStream_t st) {
-  constexpr int HPW = 32 / (D / 8);
-  p.sets = (p.h_q + 2 * p.h_kv + U * HPW - 1) / (U * HPW);
+// Heads of a warp, in groups of HPW: as many as four where the tokens then still fill the GPU's resident warps,
+// so that a token's cosines, sines and weights are loaded once for them; else one, the shortest chain.
+// Measured (us, groups 1 / 2 / 4 / 8): 16384 tokens, 64 + 8 + 8 heads of 128: 173.7 / 125.9 / 120.1 / 125.7;
+// 64 tokens, 32 + 8 + 8 heads, with the read-back of what was stored: 4.5 / 4.8 / 5.6 / 6.8.
+template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
+cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
+  constexpr int HPW = 32 / (D / (2 * CW));
+  const int qg = (p.h_q + HPW - 1) / HPW, kg = (p.h_kv + HPW - 1) / HPW;
+  for (p.iters = 4;; p.iters /= 2) {
+    p.q_sets = (qg + p.iters - 1) / p.iters;
+    p.k_sets = (kg + p.iters - 1) / p.iters;
+    p.sets = p.q_sets + 2 * p.k_sets;
+    if (p.iters == 1 || (int64_t)p.num_tokens * p.sets >= (int64_t)sms * 4 * (kAppendThreads / 32)) break;
+  }
   const int64_t warps = (int64_t)p.num_tokens * p.sets, per = kAppendThreads / 32;
   const int64_t blocks = (warps + per - 1) / per;
   if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-  return launch_pdl(gqa_append_kernel<D, BF16, U>, (unsigned)blocks, kAppendThreads, st, p);
+  return launch_pdl(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, (unsigned)blocks, kAppendThreads, st, p);
+}
+
+template <int D, bool BF16, int CW, bool PAIRS>
+cudaError_t append_layout(const AppendParams& p, int layout, int sms, cudaStream_t st) {
+  switch (layout) {
+    case GQA_CACHE_ROWS: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_ROWS>(p, sms, st);
+    case GQA_CACHE_VLLM: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_VLLM>(p, sms, st);
+    default: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_KV8>(p, sms, st);
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t append_run(const AppendParams& p, int layout, int sms, cudaStream_t st) {
+  const bool pairs = p.cos_sin != nullptr && p.interleaved;
+  if (p.cos_sin != nullptr && p.rot_dim % 16 != 0)
+    return pairs ? append_layout<D, BF16, 4, true>(p, layout, sms, st) : append_layout<D, BF16, 4, false>(p, layout, sms, st);
+  return pairs ? append_layout<D, BF16, 8, true>(p, layout, sms, st) : append_layout<D, BF16, 8, false>(p, layout, sms, st);
 }
 
 gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void* stream) {
@@ -57,6 +106,14 @@ gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void
     if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
   }
   if (a.num_tokens == 0) return GQA_OK;
+  int sms = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    Kv8Device* dev = nullptr;
+    const gqa_status s = device_locked(&dev);
+    if (s != GQA_OK) return s;
+    sms = dev->sms;
+  }
   AppendParams p = {};
   p.q = a.q; p.k = a.k; p.v = a.v; p.q_out = a.q_out;
   p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride; p.q_out_stride = a.q_out_stride;
@@ -66,12 +123,12 @@ gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void
   p.status = static_cast<uint32_t*>(ws);
   p.num_tokens = a.num_tokens; p.h_q = a.h_q; p.h_kv = a.h_kv;
   p.max_position = a.max_position; p.rot_dim = a.rot_dim; p.interleaved = a.interleaved ? 1 : 0;
-  p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.layout = a.cache_layout;
+  p.num_blocks = a.num_blocks; p.block_size = a.block_size;
   p.eps = a.eps;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.d_head == 64)
-    return cuda_status(a.bf16 ? append_launch<64, true, 1>(p, st) : append_launch<64, false, 1>(p, st));
-  return cuda_status(a.bf16 ? append_launch<128, true, 1>(p, st) : append_launch<128, false, 1>(p, st));
+    return cuda_status(a.bf16 ? append_run<64, true>(p, a.cache_layout, sms, st) : append_run<64, false>(p, a.cache_layout, sms, st));
+  return cuda_status(a.bf16 ? append_run<128, true>(p, a.cache_layout, sms, st) : append_run<128, false>(p, a.cache_layout, sms, st));
 }
 
 // ---------------------------------------------------------------- shapes of the kv8 calls
@@ -97,14 +154,6 @@ gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
 int kv8_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 3)); }
 int kv8_groups(int cls) { return cls < 2 ? kKv8Warps : (cls == 2 ? kKv8Warps / 2 : kKv8Warps / 4); }
 
-struct Kv8Device {
-  int sms = 0;
-  bool ready[2][4][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
-};
-constexpr int kMaxDevices = 64;
-std::mutex g_mu;
-Kv8Device g_kv8[kMaxDevices];
-
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_prepare() {
   return cudaFuncSetAttribute(gqa_decode_kv8_kernel<D, NT, RG, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -123,22 +172,18 @@ cudaError_t kv8_prepare_class(int cls) {
 
 // SMs of the current device; the kernel of (D, cls, bf16) is ready to launch on it
 gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return GQA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_mu);
-  Kv8Device& d = g_kv8[dev];
-  if (d.sms == 0 && cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    d.sms = 0;
-    return GQA_ERR_CUDA;
-  }
-  bool& ready = d.ready[D == 64 ? 0 : 1][cls][bf16];
+  Kv8Device* dev = nullptr;
+  const gqa_status s = device_locked(&dev);
+  if (s != GQA_OK) return s;
+  bool& ready = dev->ready[D == 64 ? 0 : 1][cls][bf16];
   if (!ready) {
     const cudaError_t e = D == 64 ? (bf16 ? kv8_prepare_class<64, true>(cls) : kv8_prepare_class<64, false>(cls))
                                   : (bf16 ? kv8_prepare_class<128, true>(cls) : kv8_prepare_class<128, false>(cls));
     if (e != cudaSuccess) return GQA_ERR_CUDA;
     ready = true;
   }
-  *sms = d.sms;
+  *sms = dev->sms;
   return GQA_OK;
 }
 
@@ -266,7 +311,8 @@ gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* le
   p.num_seqs = N; p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size; p.h_kv = h_kv;
   // tokens past the table exist in no sequence: no warps for them
   const int64_t most = out_len < (int64_t)max_blocks * block_size ? out_len : (int64_t)max_blocks * block_size;
-  p.groups = (most + kReadTokens - 1) / kReadTokens;
+  const int tokens = D == 64 ? ReadCfg<64>::TOKENS : ReadCfg<128>::TOKENS;
+  p.groups = (most + tokens - 1) / tokens;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = opt != nullptr && opt->bf16;
   if (D == 64) return cuda_status(bf16 ? read_launch<64, true>(p, st) : read_launch<64, false>(p, st));

@@ -15,7 +15,6 @@ namespace gqa {
 
 constexpr int kAppendThreads = 256;
 constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 16;   // tokens of one warp of the read kernel
 
 __host__ __device__ constexpr int kv8_block_bytes(int block_size, int D) { return block_size * (2 * D + 2); }
 
@@ -37,7 +36,7 @@ __device__ __forceinline__ int kv8_exponent(float amax) {
 }
 
 // four codes of x[0..3] * inv, nearest even (|x| * inv <= 448; infinities become 448, NaN stays)
-__device__ __forceinline__ uint32_t kv8_codes(const float (&x)[4], float inv) {
+__device__ __forceinline__ uint32_t kv8_codes(const float* x, float inv) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
@@ -79,166 +78,221 @@ struct AppendParams {
   const int64_t* slots;
   void *k_cache, *v_cache;
   uint32_t* status;
-  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, layout, sets;
+  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, sets, q_sets, k_sets, iters;
   float eps;
 };
 
-// A head's D elements lie on D/8 lanes, each with two groups of four: elements 4s.. and rot/2 + 4s.. for
-// the lanes s < rot/8 that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
-// thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes U
-// times 32/(D/8) heads of one token and issues all their loads before it uses one.  Bound by its bytes:
-// the heads read and written once; the sums of squares and maxima go through log2(D/8) shuffles.
-template <int D, bool BF16, int U>
-__global__ void __launch_bounds__(kAppendThreads)
+// CW neighbouring 16-bit elements: one 8- or 16-byte access
+template <int CW>
+struct Chunk {
+  uint32_t w[CW / 2];
+};
+
+template <int CW>
+__device__ __forceinline__ Chunk<CW> load_chunk(const uint16_t* p) {
+  Chunk<CW> c;
+  if constexpr (CW == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    c.w[0] = v.x; c.w[1] = v.y; c.w[2] = v.z; c.w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    c.w[0] = v.x; c.w[1] = v.y;
+  }
+  return c;
+}
+
+template <int CW>
+__device__ __forceinline__ void store_chunk(uint16_t* p, const Chunk<CW>& c) {
+  if constexpr (CW == 8) *reinterpret_cast<uint4*>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
+}
+
+template <bool BF16, int CW>
+__device__ __forceinline__ void unpack_chunk(const Chunk<CW>& c, float* x) {
+#pragma unroll
+  for (int i = 0; i < CW / 2; i += 2) unpack4<BF16>(make_uint2(c.w[i], c.w[i + 1]), x + 2 * i);
+}
+
+template <bool BF16, int CW>
+__device__ __forceinline__ Chunk<CW> pack_chunk(const float* x) {
+  Chunk<CW> c;
+#pragma unroll
+  for (int i = 0; i < CW / 2; ++i) c.w[i] = Elem<BF16>::pack(x[2 * i], x[2 * i + 1]);
+  return c;
+}
+
+// n consecutive floats, 4 n bytes aligned to 8
+template <int n>
+__device__ __forceinline__ void load_floats(float* x, const float* p) {
+  if constexpr (n % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < n; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(p + i));
+      x[i] = v.x; x[i + 1] = v.y;
+    }
+  }
+}
+
+// A head's D elements lie on D/(2 CW) lanes, each with two chunks of CW: elements CW s.. and rot/2 + CW s.. for
+// the lanes s < rot/(2 CW) that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
+// thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes
+// heads of one kind (queries, keys or values) of one token: 32/(D/(2 CW)) at a time, up to a.iters times, the next
+// ones' loads in flight; cosines, sines and norm weights stay in registers over its heads.  Bound by its bytes, the
+// heads read and written once, when there are many tokens; the sums of squares and maxima go through log2 of
+// the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
+// Four CTAs an SM (64 registers, a few spilled): 16384 tokens of 64 + 8 + 8 heads of 128 took 120.1 us with four,
+// 133.2 with three (76 registers), 176.5 with two; 146 with CW = 4, whose lanes hold half as much and shuffle more.
+template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
+__global__ void __launch_bounds__(kAppendThreads, 4)
 gqa_append_kernel(const AppendParams a) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH;
+  constexpr int LPH = D / (2 * CW), HPW = 32 / LPH;
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31, sub = lane % LPH;
   const int64_t w = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
   const int64_t t = w / a.sets;
   if (t >= a.num_tokens) return;
-  const int h0 = (int)(w - t * a.sets) * (U * HPW) + lane / LPH;
-  const int heads = a.h_q + 2 * a.h_kv;
-  const bool turns = a.cos_sin != nullptr && sub < a.rot_dim / 8;
+  int set = (int)(w - t * a.sets);
+  const int kind = set < a.q_sets ? 0 : (set < a.q_sets + a.k_sets ? 1 : 2);
+  set -= kind == 0 ? 0 : (kind == 1 ? a.q_sets : a.q_sets + a.k_sets);
+  const int heads = kind == 0 ? a.h_q : a.h_kv;
+  int h = set * (a.iters * HPW) + lane / LPH;
   const int rot = a.cos_sin != nullptr ? a.rot_dim : 0;
+  const bool turns = 2 * CW * sub < rot;
   int off[2];
-  off[0] = turns ? 4 * sub : rot + 4 * (sub - rot / 8);
-  off[1] = turns ? rot / 2 + 4 * sub : rot + (D - rot) / 2 + 4 * (sub - rot / 8);
+  off[0] = turns ? CW * sub : rot + CW * (sub - rot / (2 * CW));
+  off[1] = off[0] + (turns ? rot / 2 : (D - rot) / 2);
 
-  uint2 raw[U][2];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPW;
-    const uint16_t* src = nullptr;
-    if (h < a.h_q) src = a.q + t * a.q_stride + h * D;
-    else if (h < a.h_q + a.h_kv) src = a.k + t * a.k_stride + (h - a.h_q) * D;
-    else if (h < heads) src = a.v + t * a.v_stride + (h - a.h_q - a.h_kv) * D;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      raw[u][j] = src != nullptr ? *reinterpret_cast<const uint2*>(src + off[j]) : make_uint2(0u, 0u);
+  const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+  Chunk<CW> next[2] = {};
+  if (h < heads) {
+    next[0] = load_chunk<CW>(src + h * D + off[0]);
+    next[1] = load_chunk<CW>(src + h * D + off[1]);
   }
-  const int64_t slot = a.slots[t];
-  const int64_t n_slots = (int64_t)a.num_blocks * a.block_size;
-  if (slot >= n_slots && lane == 0) atomicOr(a.status, kDevBadInput);
-  const bool stored = slot >= 0 && slot < n_slots;
-  const int64_t blk = stored ? slot / a.block_size : 0;
-  const int row = stored ? (int)(slot - blk * a.block_size) : 0;
-  float cs[8];   // cosines and sines of this lane's four pairs
+  int64_t slot = -1, blk = 0;
+  int row = 0;
+  if (kind != 0) {
+    slot = a.slots[t];
+    if (slot >= (int64_t)a.num_blocks * a.block_size) {
+      if (lane == 0) atomicOr(a.status, kDevBadInput);
+      slot = -1;
+    }
+    blk = (uint32_t)slot / (uint32_t)a.block_size;
+    row = (int)((uint32_t)slot % (uint32_t)a.block_size);
+  }
+  float cs[2][CW];          // cosines and sines of this lane's pairs
   if (a.cos_sin != nullptr) {
-    const int p = a.positions[t];
-    if (p < 0 || p >= a.max_position) {
+    const int pos = a.positions[t];
+    if (pos < 0 || pos >= a.max_position) {
       if (lane == 0) atomicOr(a.status, kDevBadInput);
       return;
     }
-    if (turns) {
-      const float* c = a.cos_sin + (int64_t)p * a.rot_dim;
-      if (a.interleaved) {
+    if (turns && kind < 2) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 x = *reinterpret_cast<const float2*>(c + off[j] / 2);
-          const float2 y = *reinterpret_cast<const float2*>(c + rot / 2 + off[j] / 2);
-          cs[2 * j] = x.x; cs[2 * j + 1] = x.y; cs[4 + 2 * j] = y.x; cs[5 + 2 * j] = y.y;
+      for (int k = 0; k < 2; ++k) {
+        const float* c = a.cos_sin + (int64_t)pos * a.rot_dim + k * (rot / 2);
+        if constexpr (PAIRS) {
+          load_floats<CW / 2>(cs[k], c + off[0] / 2);
+          load_floats<CW / 2>(cs[k] + CW / 2, c + off[1] / 2);
+        } else {
+          load_floats<CW>(cs[k], c + off[0]);
         }
-      } else {
-        const float4 x = *reinterpret_cast<const float4*>(c + 4 * sub);
-        const float4 y = *reinterpret_cast<const float4*>(c + rot / 2 + 4 * sub);
-        cs[0] = x.x; cs[1] = x.y; cs[2] = x.z; cs[3] = x.w;
-        cs[4] = y.x; cs[5] = y.y; cs[6] = y.z; cs[7] = y.w;
       }
     }
   }
+  if (kind != 0 && slot < 0) return;
+  const uint16_t* weight = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
+  Chunk<CW> wt[2] = {};
+  if (weight != nullptr) {
+    wt[0] = load_chunk<CW>(weight + off[0]);
+    wt[1] = load_chunk<CW>(weight + off[1]);
+  }
+#pragma unroll 1
+  for (int it = 0; it < a.iters; ++it, h += HPW) {
+    float x[2][CW];
+    unpack_chunk<BF16, CW>(next[0], x[0]);
+    unpack_chunk<BF16, CW>(next[1], x[1]);
+    if (it + 1 < a.iters && h + HPW < heads) {
+      next[0] = load_chunk<CW>(src + (h + HPW) * D + off[0]);
+      next[1] = load_chunk<CW>(src + (h + HPW) * D + off[1]);
+    }
+    if (weight != nullptr) {
+      float ss = 0.f;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPW;
-    float x[2][4];
-    unpack4<BF16>(raw[u][0], x[0]);
-    unpack4<BF16>(raw[u][1], x[1]);
-    const bool is_q = h < a.h_q, is_k = !is_q && h < a.h_q + a.h_kv;
-    // ---- norm of the head
-    float ss = 0.f;
+      for (int i = 0; i < CW; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
-#pragma unroll
-    for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const uint16_t* wt = is_q ? a.q_weight : (is_k ? a.k_weight : nullptr);
-    if (wt != nullptr) {
-      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float g[4];
-        unpack4<BF16>(*reinterpret_cast<const uint2*>(wt + off[j]), g);
+        float g[CW];
+        // (unpacked anew for every head: kept as floats they would cost 2 CW registers and a third of the warps)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[j][i] = x[j][i] * r * g[i];
+        for (int i = 0; i < CW / 2; ++i) asm volatile("" : "+r"(wt[j].w[i]));
+        unpack_chunk<BF16, CW>(wt[j], g);
+#pragma unroll
+        for (int i = 0; i < CW; ++i) x[j][i] = x[j][i] * r * g[i];
       }
     }
-    // ---- rotation of its pairs
-    if (turns && (is_q || is_k)) {
-      if (a.interleaved) {
+    if (turns && kind < 2) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const float c = cs[2 * j + i / 2], s = cs[4 + 2 * j + i / 2], p = x[j][i], n = x[j][i + 1];
-            x[j][i] = p * c - n * s;
-            x[j][i + 1] = n * c + p * s;
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float c = cs[i], s = cs[4 + i], p = x[0][i], n = x[1][i];
-          x[0][i] = p * c - n * s;
-          x[1][i] = n * c + p * s;
-        }
+      for (int i = 0; i < CW; ++i) {
+        // pair i of the lane: (x[0][i], x[1][i]), or neighbours of chunk i / (CW/2)
+        float& p = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2))] : x[0][i];
+        float& n = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2)) + 1] : x[1][i];
+        const float y = p * cs[0][i] - n * cs[1][i];
+        n = n * cs[0][i] + p * cs[1][i];
+        p = y;
       }
     }
-    // ---- the row's exponent (kv8)
-    int e = 0;
-    if (a.layout == 2) {
+    if (kind == 0) {
+      if (h < heads) {
+        uint16_t* to = a.q_out + t * a.q_out_stride + h * D;
+        store_chunk<CW>(to + off[0], pack_chunk<BF16, CW>(x[0]));
+        store_chunk<CW>(to + off[1], pack_chunk<BF16, CW>(x[1]));
+      }
+    } else if constexpr (LAYOUT == 2) {
       float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(x[0][i]), fabsf(x[1][i])));
+      for (int i = 0; i < CW; ++i) top = fmaxf(top, fmaxf(fabsf(x[0][i]), fabsf(x[1][i])));
 #pragma unroll
       for (int m = LPH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      e = kv8_exponent(top);
-    }
-    if (h >= heads) continue;
-    if (is_q) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<uint2*>(a.q_out + t * a.q_out_stride + h * D + off[j]) =
-            make_uint2(Elem<BF16>::pack(x[j][0], x[j][1]), Elem<BF16>::pack(x[j][2], x[j][3]));
-      continue;
-    }
-    if (!stored) continue;
-    const int g = is_k ? h - a.h_q : h - a.h_q - a.h_kv;
-    if (a.layout == 2) {
+      const int e = kv8_exponent(top);
       const int bb = kv8_block_bytes(a.block_size, D);
-      const int64_t at = (blk * a.h_kv + g) * bb;
-      if (!idx_ok(at + bb - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status)) continue;
-      uint8_t* base = reinterpret_cast<uint8_t*>(a.k_cache) + at;
-      uint8_t* codes = base + (is_k ? 0 : a.block_size * D);
-      const float inv = kv8_scale(254 - e);   // 2^-k
+      const int64_t at = (blk * a.h_kv + h) * bb;
+      if (h < heads && idx_ok(at + bb - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status)) {
+        uint8_t* base = reinterpret_cast<uint8_t*>(a.k_cache) + at;
+        uint8_t* codes = base + (kind - 1) * a.block_size * D;
+        const float inv = kv8_scale(254 - e);   // 2^-k
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<uint32_t*>(codes + kv8_chunk<D>(row, off[j] >> 4) + (off[j] & 15)) = kv8_codes(x[j], inv);
-      if (sub == 0) base[2 * a.block_size * D + (is_k ? 0 : a.block_size) + row] = (uint8_t)e;
-    } else {
-      uint16_t* pool = reinterpret_cast<uint16_t*>(is_k ? a.k_cache : a.v_cache);
+        for (int j = 0; j < 2; ++j) {
+          uint8_t* to = codes + kv8_chunk<D>(row, off[j] >> 4) + (off[j] & 15);
+          if constexpr (CW == 8) *reinterpret_cast<uint2*>(to) = make_uint2(kv8_codes(x[j], inv), kv8_codes(x[j] + 4, inv));
+          else *reinterpret_cast<uint32_t*>(to) = kv8_codes(x[j], inv);
+        }
+        if (sub == 0) base[2 * a.block_size * D + (kind - 1) * a.block_size + row] = (uint8_t)e;
+      }
+    } else if (h < heads) {
+      uint16_t* pool = reinterpret_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache);
+      const int64_t size = (int64_t)a.num_blocks * a.block_size * a.h_kv * D;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint2 y = make_uint2(Elem<BF16>::pack(x[j][0], x[j][1]), Elem<BF16>::pack(x[j][2], x[j][3]));
-        if (a.layout == 0 || is_k) {
+        const Chunk<CW> y = pack_chunk<BF16, CW>(x[j]);
+        if (LAYOUT == 0 || kind == 1) {
           const int64_t at =
-              a.layout == 0 ? ((blk * a.block_size + row) * a.h_kv + g) * D + off[j]
-                            : (((blk * a.h_kv + g) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
-          if (idx_ok(at + 3, n_slots * a.h_kv * D, a.status)) *reinterpret_cast<uint2*>(pool + at) = y;
+              LAYOUT == 0 ? (slot * a.h_kv + h) * D + off[j]
+                            : (((blk * a.h_kv + h) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
+          if (idx_ok(at + CW - 1, size, a.status)) store_chunk<CW>(pool + at, y);
         } else {
-          const int64_t at = ((blk * a.h_kv + g) * D + off[j]) * a.block_size + row;
-          if (!idx_ok(at + 3 * a.block_size, n_slots * a.h_kv * D, a.status)) continue;
-          pool[at] = (uint16_t)y.x;
-          pool[at + a.block_size] = (uint16_t)(y.x >> 16);
-          pool[at + 2 * a.block_size] = (uint16_t)y.y;
-          pool[at + 3 * a.block_size] = (uint16_t)(y.y >> 16);
+          const int64_t at = ((blk * a.h_kv + h) * D + off[j]) * a.block_size + row;
+          if (!idx_ok(at + (CW - 1) * a.block_size, size, a.status)) continue;
+#pragma unroll
+          for (int i = 0; i < CW; ++i) pool[at + i * a.block_size] = (uint16_t)(y.w[i / 2] >> (16 * (i & 1)));
         }
       }
     }
@@ -257,20 +311,25 @@ struct Kv8ReadParams {
   int num_seqs, max_blocks, num_blocks, block_size, h_kv;
 };
 
-// One warp for kReadTokens tokens of one head: D/8 lanes a row, 8 codes a lane, all loads of the warp's
-// rows first.  Warps of a CTA take the heads of the same tokens, whose blocks lie side by side in the
+// One warp for 4 * RPP tokens of one head: D/16 lanes a row, 16 codes a lane, the loads of K and V of all
+// its rows first.  Warps of a CTA take the heads of the same tokens, whose blocks lie side by side in the
 // cache and whose output rows touch.  Bound by its bytes.
+template <int D>
+struct ReadCfg {
+  static constexpr int LPR = D / 16, RPP = 32 / LPR, P = 4, TOKENS = P * RPP;
+};
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kReadThreads)
 gqa_kv8_read_kernel(const Kv8ReadParams a) {
-  constexpr int LPR = D / 8, RPP = 32 / LPR, P = kReadTokens / RPP;
+  constexpr int LPR = ReadCfg<D>::LPR, RPP = ReadCfg<D>::RPP, P = ReadCfg<D>::P;
   ptx::grid_dependency_wait();
-  const int lane = threadIdx.x & 31, c8 = lane % LPR;
+  const int lane = threadIdx.x & 31, c = lane % LPR;
   int64_t w = ((int64_t)blockIdx.x * kReadThreads + threadIdx.x) >> 5;
   if (w >= (int64_t)a.num_seqs * a.groups * a.h_kv) return;
   const int g = (int)(w % a.h_kv);
   w /= a.h_kv;
-  const int64_t b = w / a.groups, i0 = (w - b * a.groups) * kReadTokens;
+  const int64_t b = w / a.groups, i0 = (w - b * a.groups) * ReadCfg<D>::TOKENS;
   const int cap = a.max_blocks * a.block_size;
   int len = a.seq_lens[b];
   const int begin = a.begins != nullptr ? a.begins[b] : 0;
@@ -279,53 +338,53 @@ gqa_kv8_read_kernel(const Kv8ReadParams a) {
     len = len > cap ? cap : len;
   }
   if (begin < 0 || begin + i0 >= len) return;
-  const int bb = kv8_block_bytes(a.block_size, D);
-  int64_t base[P];
-  int rows[P];
+  const int bb = kv8_block_bytes(a.block_size, D), v_off = a.block_size * D;
+  uint4 codes[2][P];
+  uint32_t e[2][P];
+  bool have[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int64_t i = i0 + p * RPP + lane / LPR, tok = begin + i;
-    base[p] = -1;
-    rows[p] = 0;
+    have[p] = false;
     if (i < a.out_len && tok < len) {
-      const int64_t j = tok / a.block_size;
-      const int id = a.block_tables[b * a.max_blocks + j];
-      rows[p] = (int)(tok - j * a.block_size);
-      if (id >= 0 && id < a.num_blocks) base[p] = ((int64_t)id * a.h_kv + g) * bb;
-      else atomicOr(a.status, kDevBadInput);
+      const int j = (int)((uint32_t)tok / (uint32_t)a.block_size), row = (int)tok - j * a.block_size;
+      const int id = __ldg(a.block_tables + b * a.max_blocks + j);
+      have[p] = id >= 0 && id < a.num_blocks;
+      if (!have[p]) atomicOr(a.status, kDevBadInput);
+      const uint8_t* at = a.cache + ((int64_t)id * a.h_kv + g) * bb;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+        if (have[p] && (kv ? a.v_out : a.k_out) != nullptr) {
+          codes[kv][p] = __ldcs(reinterpret_cast<const uint4*>(at + kv * v_off + kv8_chunk<D>(row, c)));
+          e[kv][p] = __ldg(at + 2 * v_off + kv * a.block_size + row);
+        }
     }
   }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     uint16_t* out = kv ? a.v_out : a.k_out;
     if (out == nullptr) continue;
-    uint2 codes[P];
-    uint32_t e[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      codes[p] = make_uint2(0u, 0u);
-      e[p] = 127;
-      if (base[p] >= 0) {
-        const uint8_t* at = a.cache + base[p];
-        codes[p] = __ldcs(reinterpret_cast<const uint2*>(at + kv * a.block_size * D + kv8_chunk<D>(rows[p], c8 >> 1) +
-                                                         (c8 & 1) * 8));
-        e[p] = at[2 * a.block_size * D + kv * a.block_size + rows[p]];
-      }
-    }
+      if (!have[p]) continue;
+      const float s = kv8_scale(e[kv][p]);
+      const uint32_t word[4] = {codes[kv][p].x, codes[kv][p].y, codes[kv][p].z, codes[kv][p].w};
+      uint32_t y[8];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (base[p] < 0) continue;
-      const float s = kv8_scale(e[p]);
-      uint4 y;
-      uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t word = q < 2 ? codes[p].x : codes[p].y;
-        const float2 f = half2_floats(kv8_halves((uint16_t)(word >> (16 * (q & 1)))));
-        yw[q] = Elem<BF16>::pack(f.x * s, f.y * s);
+      for (int q = 0; q < 8; ++q) {
+        const float2 f = half2_floats(kv8_halves((uint16_t)(word[q >> 1] >> (16 * (q & 1)))));
+        y[q] = Elem<BF16>::pack(f.x * s, f.y * s);
       }
-      const int64_t at = ((b * a.out_len + i0 + p * RPP + lane / LPR) * a.h_kv + g) * D + c8 * 8;
-      if (idx_ok(at + 7, a.num_seqs * a.out_len * a.h_kv * D, a.status)) *reinterpret_cast<uint4*>(out + at) = y;
+      const int64_t at = ((b * a.out_len + i0 + p * RPP + lane / LPR) * a.h_kv + g) * D + c * 16;
+      if (!idx_ok(at + 15, a.num_seqs * a.out_len * a.h_kv * D, a.status)) continue;
+      if (reinterpret_cast<uintptr_t>(out) & 31) {
+        *reinterpret_cast<uint4*>(out + at) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(out + at + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+      } else {   // a lane's 32 bytes in one store: whole sectors
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + at), "r"(y[0]), "r"(y[1]),
+                     "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+      }
     }
   }
 }
