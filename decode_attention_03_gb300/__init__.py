@@ -33,5 +33,6 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         mod = importlib.import_module("._binding", __name__)
-        return getattr(mod, name)
+        value = globals()[name] = getattr(mod, name)   # found without this function from now on
+        return value
     raise AttributeError(name)
