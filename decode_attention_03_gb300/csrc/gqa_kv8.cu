@@ -150,14 +150,14 @@ gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
 }
 
 // ---------------------------------------------------------------- decode
-// Kernel shapes: up to 8 or 16 query rows for one warp, 32 or 64 for two or four warps that share a ring.
+// Kernel shapes: up to 8, 16 or 32 query rows for one warp, 64 for two warps that share a ring.
 int kv8_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 3)); }
-int kv8_groups(int cls) { return cls < 2 ? kKv8Warps : (cls == 2 ? kKv8Warps / 2 : kKv8Warps / 4); }
+int kv8_groups(int cls) { return cls < 3 ? kKv8Warps : kKv8Warps / 2; }
 
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_prepare() {
   return cudaFuncSetAttribute(gqa_decode_kv8_kernel<D, NT, RG, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Kv8Cfg<D, RG>::SMEM);
+                              Kv8Cfg<D, NT, RG>::SMEM);
 }
 
 template <int D, bool BF16>
@@ -165,8 +165,8 @@ cudaError_t kv8_prepare_class(int cls) {
   switch (cls) {
     case 0: return kv8_prepare<D, 1, 1, BF16>();
     case 1: return kv8_prepare<D, 2, 1, BF16>();
-    case 2: return kv8_prepare<D, 2, 2, BF16>();
-    default: return kv8_prepare<D, 2, 4, BF16>();
+    case 2: return kv8_prepare<D, 4, 1, BF16>();
+    default: return kv8_prepare<D, 4, 2, BF16>();
   }
 }
 
@@ -188,15 +188,17 @@ gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
 }
 
 struct Kv8Layout {
-  size_t prefix, m, l, o, total;
+  size_t prefix, splits, m, l, o, total;
 };
 
-// workspace: the status header, the tiles before each sequence of a launch, two partials for each worker
+// workspace: the status header, the tiles before each sequence of a launch, the unit each worker cuts and two
+// partials for each worker
 Kv8Layout kv8_layout(int workers, int rows, int D) {
   Kv8Layout L;
   const size_t n = 2 * (size_t)workers * rows;
   L.prefix = kHeaderBytes;
-  L.m = L.prefix + align256((kKv8Seqs + 1) * sizeof(int64_t));
+  L.splits = L.prefix + align256((kKv8Seqs + 1) * sizeof(int64_t));
+  L.m = L.splits + align256((size_t)workers * sizeof(int4));
   L.l = L.m + align256(n * 4);
   L.o = L.l + align256(n * 4);
   L.total = L.o + align256(n * D * 4);
@@ -205,7 +207,7 @@ Kv8Layout kv8_layout(int workers, int rows, int D) {
 
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_launch(const Kv8Params& p, unsigned grid, cudaStream_t st) {
-  return launch_pdl_smem(gqa_decode_kv8_kernel<D, NT, RG, BF16>, grid, kKv8Threads, Kv8Cfg<D, RG>::SMEM, st, p);
+  return launch_pdl_smem(gqa_decode_kv8_kernel<D, NT, RG, BF16>, grid, kKv8Threads, Kv8Cfg<D, NT, RG>::SMEM, st, p);
 }
 
 template <int D, bool BF16>
@@ -214,13 +216,15 @@ cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool many_pie
   switch (cls) {
     case 0: e = kv8_launch<D, 1, 1, BF16>(p, grid, st); break;
     case 1: e = kv8_launch<D, 2, 1, BF16>(p, grid, st); break;
-    case 2: e = kv8_launch<D, 2, 2, BF16>(p, grid, st); break;
-    default: e = kv8_launch<D, 2, 4, BF16>(p, grid, st); break;
+    case 2: e = kv8_launch<D, 4, 1, BF16>(p, grid, st); break;
+    default: e = kv8_launch<D, 4, 2, BF16>(p, grid, st); break;
   }
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)p.N * p.T_q * p.h_q, warps = kMergeThreads / 32;
-  if (many_pieces) return launch_pdl(gqa_kv8_merge_kernel<D, BF16, 8>, (unsigned)rows, kMergeThreads, st, p);
-  return launch_pdl(gqa_kv8_merge_kernel<D, BF16, 1>, (unsigned)((rows + warps - 1) / warps), kMergeThreads, st, p);
+  if (many_pieces)
+    return launch_pdl(gqa_kv8_merge_kernel<D, BF16, true>, (unsigned)((int64_t)p.N * p.T_q * p.h_q * (D / 32)),
+                      kMergeThreads, st, p);
+  const int64_t tasks = (int64_t)p.workers * p.rows, warps = kMergeThreads / 32;
+  return launch_pdl(gqa_kv8_merge_kernel<D, BF16, false>, (unsigned)((tasks + warps - 1) / warps), kMergeThreads, st, p);
 }
 
 gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* tables, const int32_t* lens,
@@ -248,6 +252,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   p.cache = static_cast<const uint8_t*>(cache);
   p.status = reinterpret_cast<uint32_t*>(wsb);
   p.prefix = reinterpret_cast<int64_t*>(wsb + lay.prefix);
+  p.splits = reinterpret_cast<int4*>(wsb + lay.splits);
   p.ws_m = reinterpret_cast<float*>(wsb + lay.m);
   p.ws_l = reinterpret_cast<float*>(wsb + lay.l);
   p.ws_o = reinterpret_cast<float*>(wsb + lay.o);
@@ -271,7 +276,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     const unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
     p.workers = (int)grid * kv8_groups(cls);
     // pieces of a unit: about workers / units + 1 when the sequences are alike
-    const bool many = p.workers / units >= kMergeChunk - 1;
+    const bool many = p.workers / units >= 7;
     const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, many, st)
                                           : kv8_decode<64, false>(p, cls, grid, many, st))
                                   : (bf16 ? kv8_decode<128, true>(p, cls, grid, many, st)

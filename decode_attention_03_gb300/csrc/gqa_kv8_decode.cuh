@@ -5,7 +5,7 @@
 // SM).  The cut does not look at sequences: a share may hold many short ones or a part of a long one, so
 // every worker streams the same bytes whatever the lengths are, and nothing is claimed or counted at run
 // time.  A (sequence, head) that lies inside one share is finished by its worker; the others leave partials
-// (m, l, O) that a merge kernel folds in the order of the keys.
+// (m, l, O) that a merge kernel folds in the order of the keys: the same bits every time.
 //
 // A worker streams its tiles through a ring of its own in shared memory: one plain bulk copy for each block
 // (32 keys are 32/block_size of them), K, V and scales together.  No warp waits for another worker's.
@@ -41,6 +41,7 @@ struct Kv8Params {
   const int32_t *block_tables, *seq_lens;
   uint32_t* status;
   int64_t* prefix;       // [N + 1] tiles (of one head) before each sequence
+  int4* splits;          // [workers] the unit that a worker's range cuts first: sequence, head, pieces, first slot
   float *ws_m, *ws_l;    // [2 * workers][rows]   m in log2 units
   float* ws_o;           // [2 * workers][rows][D]
   int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, bs_log, causal, workers, stall;
@@ -49,20 +50,25 @@ struct Kv8Params {
 };
 
 // The slots of partials: worker w's first piece 2w, a later piece that it does not finish 2w + 1.
-template <int D, int RG>
+template <int D, int NT, int RG>
 struct Kv8Cfg {
   static constexpr int GROUPS = kKv8Warps / RG;
   static constexpr int TILE = kKv8Keys * (2 * D + 2);
+  static constexpr bool Q_SMEM = NT > 2;                    // query fragments in shared memory, else in registers
+  static constexpr int QUERIES = Q_SMEM ? 8 * NT * (D * 2 + 4) : 0;   // of a warp, and its rows' factors
   static constexpr int PREFIX_OFF = 0;
   static constexpr int LENS_OFF = (kKv8Seqs + 2) * 8;
   static constexpr int SUMS_OFF = LENS_OFF + kKv8Seqs * 4;
   static constexpr int FLAG_OFF = SUMS_OFF + kKv8Warps * 8;
   static constexpr int BAR_OFF = FLAG_OFF + 16;
-  static constexpr int MAX_STAGES = (232448 - BAR_OFF - 256) / (GROUPS * (TILE + 16));
-  static constexpr int STAGES = MAX_STAGES > 12 ? 12 : MAX_STAGES;
-  static constexpr int RING_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
+  // 2 x 8.25 KB in flight for each warp.  Three entries at d_head 128: 64 sequences of 1K-16K keys 168 us instead of
+  // 157, 2^20 keys 340 instead of 320: the fuller the memory's queues, the more unevenly it serves the SMs, and the
+  // shares are equal (last worker done 22 us after the median instead of 10).
+  static constexpr int STAGES = (D == 128 ? 2 : 4) * RG;
+  static constexpr int Q_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
+  static constexpr int RING_OFF = (Q_OFF + kKv8Warps * QUERIES + 127) & ~127;
   static constexpr int SMEM = RING_OFF + GROUPS * STAGES * TILE;
-  static_assert(STAGES >= 3 && SMEM <= 232448, "ring");
+  static_assert(GROUPS * STAGES <= kKv8Threads && SMEM <= 232448, "ring");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
@@ -151,6 +157,16 @@ __device__ __forceinline__ void kv8_prefix(const Kv8Params& a, int64_t* prefix, 
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[0] = 0;
   __syncthreads();
+}
+
+// Rows of sequences without keys: zeros, each sequence by one CTA.
+template <int D>
+__device__ __forceinline__ void kv8_empty_rows(const Kv8Params& a, const int* lens) {
+  const int64_t words = (int64_t)a.T_q * a.h_q * D / 8;
+  for (int b = blockIdx.x; b < a.N; b += gridDim.x)
+    if (lens[b] == 0)
+      for (int64_t i = threadIdx.x; i < words; i += kKv8Threads)
+        reinterpret_cast<uint4*>(a.o)[b * words + i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Block ids of the next tiles of a worker, one for each lane, and its copies.
@@ -249,35 +265,29 @@ __device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const
   s.id_next = kv8_window(a, s.ahead, lens, lane, &end);
 }
 
-// RG warps of 16 query rows share a ring (RG > 1: more than 16 rows), NT n-tiles of 8 rows a warp.
+// RG warps share a ring (RG = 2: more than 32 rows), each with NT n-tiles of 8 query rows.
 template <int D, int NT, int RG>
 struct Kv8Warp {
   static constexpr int KD = D / 16;
-  uint32_t qf[NT][KD][2];
+  static constexpr bool Q_SMEM = NT > 2;
+  uint32_t qf[Q_SMEM ? 1 : NT][Q_SMEM ? 1 : KD][2];   // Q^T fragments, or, in shared memory at q_at, [KD][NT][lane] ...
+  float qs[Q_SMEM ? 1 : NT][2];                       // ... followed by the rows' factors
+  uint32_t q_at;
   float acc[KD][NT][4];
-  float m[NT][2], l[NT][2], qs[NT][2];
-  int lim[NT][2];       // last key each of this lane's rows sees
+  float m[NT][2], l[NT][2];
+  int last;             // last key of the sequence
   int e;                // largest V exponent byte so far
   // the same for every unit and tile
-  int64_t q_off[NT];    // element offset of this lane's query row from the unit's first (negative: no row)
-  int back[NT][2];      // causal: keys hidden from this lane's rows at the end
   uint32_t rows[2];     // byte offset in a tile of this lane's ldmatrix row, keys 16p + lane % 16
   uint32_t ex[4];       // and of the K exponent of key 8o + lane / 4
   uint32_t turn;        // chunk swizzle of that row, and which of two chunks this lane addresses
 };
 
 template <int D, int NT, int RG>
-__device__ __forceinline__ void kv8_setup(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int rg, int lane) {
-  const int r = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void kv8_setup(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, uint32_t q_at, int lane) {
+  w.q_at = q_at;
+  const int r = lane >> 2;
   const int eb = min(a.block_size, kKv8Keys), bb = kv8_block_bytes(eb, D);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int row = (rg * NT + nt) * 8 + r, t = row / a.G;
-    w.q_off[nt] = row < a.rows ? ((int64_t)t * a.h_q + (row - t * a.G)) * D + 4 * c : -1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w.back[nt][i] = a.causal ? max(a.T_q - 1 - ((rg * NT + nt) * 8 + 2 * c + i) / a.G, 0) : 0;
-  }
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int key = 16 * p + (lane & 15);
@@ -292,15 +302,17 @@ __device__ __forceinline__ void kv8_setup(Kv8Warp<D, NT, RG>& w, const Kv8Params
 }
 
 template <int D, int NT, int RG, bool BF16>
-__device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int len,
+__device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int len, int rg,
                                           int lane) {
-  constexpr int KD = Kv8Warp<D, NT, RG>::KD;
-  const int c = lane & 3;
+  using W = Kv8Warp<D, NT, RG>;
+  constexpr int KD = W::KD;
+  const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    const int row = (rg * NT + nt) * 8 + r, t = row / a.G;
+    const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D + 4 * c;
+    const bool ok = row < a.rows && idx_ok(at + D - 1 - 4 * c, (int64_t)a.N * a.T_q * a.h_q * D, a.status);
     uint2 raw[KD];
-    const int64_t at = ((int64_t)b * a.T_q * a.h_q + (int64_t)g * a.G) * D + w.q_off[nt];
-    const bool ok = w.q_off[nt] >= 0 && idx_ok(at + D - 1 - 4 * c, (int64_t)a.N * a.T_q * a.h_q * D, a.status);
 #pragma unroll
     for (int j = 0; j < KD; ++j)
       raw[j] = ok ? __ldg(reinterpret_cast<const uint2*>(a.q + at + 16 * j)) : make_uint2(0u, 0u);
@@ -320,24 +332,32 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params
       for (int j = 0; j < KD; ++j) {
         float x[4];
         unpack4<true>(raw[j], x);
-        w.qf[nt][j][0] = ptx::pack_half2(x[0] * up, x[1] * up);
-        w.qf[nt][j][1] = ptx::pack_half2(x[2] * up, x[3] * up);
+        raw[j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
       }
+    }
+    if constexpr (W::Q_SMEM) {
+#pragma unroll
+      for (int j = 0; j < KD; ++j)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(w.q_at + ((j * NT + nt) * 32 + lane) * 8), "r"(raw[j].x),
+                     "r"(raw[j].y)
+                     : "memory");
+      if (c == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.q_at + KD * NT * 256 + (nt * 8 + r) * 4), "f"(qs) : "memory");
     } else {
 #pragma unroll
       for (int j = 0; j < KD; ++j) {
         w.qf[nt][j][0] = raw[j].x;
         w.qf[nt][j][1] = raw[j].y;
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w.qs[nt][i] = __shfl_sync(0xffffffffu, qs, (2 * c + i) * 4);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      w.qs[nt][i] = __shfl_sync(0xffffffffu, qs, (2 * c + i) * 4);
-      w.lim[nt][i] = len - 1 - w.back[nt][i];
       w.m[nt][i] = -CUDART_INF_F;
       w.l[nt][i] = 0.f;
     }
   }
+  w.last = len - 1;
 #pragma unroll
   for (int j = 0; j < KD; ++j)
 #pragma unroll
@@ -345,13 +365,15 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params
 #pragma unroll
       for (int i = 0; i < 4; ++i) w.acc[j][nt][i] = 0.f;
   w.e = 1;
+  if constexpr (W::Q_SMEM) __syncwarp();
 }
 
 // One tile of `valid` keys (key0 the first), `st` its place in the ring; masked: some key of it is hidden
 // from some row.
 template <int D, int NT, int RG>
-__device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, uint32_t st, int eb, int valid, int key0, bool masked,
-                                         int lane, const Win& ring) {
+__device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, uint32_t st, int eb, int valid,
+                                         int key0, bool masked, int rg, int lane, const Win& ring) {
+  using W = Kv8Warp<D, NT, RG>;
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2;
   if (valid < kKv8Keys) {
@@ -385,7 +407,21 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, uint32_t st, int
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[p][nt][0] = s[p][nt][1] = s[p][nt][2] = s[p][nt][3] = 0.f;
 #pragma unroll
-  for (int j = 0; j < KD; j += 2)
+  for (int j = 0; j < KD; j += 2) {
+    uint32_t q[2][NT][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (W::Q_SMEM) {
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(q[k][nt][0]), "=r"(q[k][nt][1])
+                       : "r"(w.q_at + (((j + k) * NT + nt) * 32 + lane) * 8));
+        } else {
+          q[k][nt][0] = w.qf[nt][j + k][0];
+          q[k][nt][1] = w.qf[nt][j + k][1];
+        }
+      }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       uint32_t x[4], f[2][4];
@@ -396,27 +432,45 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, uint32_t st, int
       kv8_unpack(x[3], f[1][1], f[1][3]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        ptx::mma_16816(s[p][nt], f[0], w.qf[nt][j]);
-        ptx::mma_16816(s[p][nt], f[1], w.qf[nt][j + 1]);
+        ptx::mma_16816(s[p][nt], f[0], q[0][nt]);
+        ptx::mma_16816(s[p][nt], f[1], q[1][nt]);
       }
     }
+  }
   // ---- scores in log2 units; s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
   top = __reduce_max_sync(0xffffffffu, top);
   bool over = false;
   float mx[NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    float qs[2];
+    if constexpr (W::Q_SMEM) {
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(qs[0]), "=f"(qs[1])
+                   : "r"(w.q_at + KD * NT * 256 + (nt * 8 + 2 * (lane & 3)) * 4));
+    } else {
+      qs[0] = w.qs[nt][0];
+      qs[1] = w.qs[nt][1];
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
         float& x = s[o >> 1][nt][(o & 1) * 2 + i];
-        x = x * w.qs[nt][i] * kv8_scale((uint32_t)ek[o]);
-        if (masked && 8 * o + r > w.lim[nt][i] - key0) x = -CUDART_INF_F;
+        x = x * qs[i] * kv8_scale((uint32_t)ek[o]);
+      }
+      if (masked) {
+        // the last key that the row sees: token row / G of T_q
+        const int row = (rg * NT + nt) * 8 + 2 * (lane & 3) + i;
+        const int lim = w.last - key0 - (a.causal ? max(a.T_q - 1 - row / a.G, 0) : 0);
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+          if (8 * o + r > lim) s[o >> 1][nt][(o & 1) * 2 + i] = -CUDART_INF_F;
       }
       mx[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i]));
       over |= mx[nt][i] > w.m[nt][i] + kKv8Slack;
     }
+  }
   const bool grow = __any_sync(0xffffffffu, over);
   if (grow || top > w.e) {
     const int e = max(top, w.e);
@@ -528,7 +582,7 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
 template <int D, int NT, int RG, bool BF16>
 __global__ void __launch_bounds__(kKv8Threads, 1)
 gqa_decode_kv8_kernel(const Kv8Params a) {
-  using C = Kv8Cfg<D, RG>;
+  using C = Kv8Cfg<D, NT, RG>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::PREFIX_OFF);
@@ -547,14 +601,25 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   ptx::grid_dependency_wait();
   kv8_prefix(a, prefix, lens, reinterpret_cast<int64_t*>(smem + C::SUMS_OFF));
   if (threadIdx.x == 0) ptx::grid_launch_dependents();
+  kv8_empty_rows<D>(a, lens);
 
   const int64_t total = prefix[a.N] * a.h_kv;
   const int64_t share = (total + a.workers - 1) / a.workers;
   const int64_t wk = (int64_t)grp * gridDim.x + blockIdx.x;
   const int64_t f0 = wk * share, f1 = f0 + share < total ? f0 + share : total;
-  if (f0 >= f1) return;
+  if (f0 >= f1) {
+    if (lane == 0 && rg == 0) a.splits[wk] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int n = (int)(f1 - f0);
   Kv8Place at = kv8_find(f0, prefix, a.N, a.h_kv);
+  if (lane == 0 && rg == 0) {
+    // this range begins inside a unit, and it is the first that does: the unit's pieces are those of the range
+    // before (its slot 0 if the unit begins with that range, else 1), this one and as many more as the unit has tiles
+    const bool first_cut = at.t > 0 && at.t <= share;
+    const int64_t pieces = first_cut ? 1 + (at.tiles - at.t + share - 1) / share : 0;
+    a.splits[wk] = make_int4(at.b, at.g, (int)pieces, at.t < share ? 1 : 0);
+  }
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
   const uint64_t policy = ptx::policy_evict_first();
@@ -569,9 +634,9 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
         kv8_copy<D>(str, a, prefix, lens, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
   }
   Kv8Warp<D, NT, RG> w;
-  kv8_setup(w, a, rg, lane);
+  kv8_setup(w, a, ptx::smem_u32(smem + C::Q_OFF) + warp * C::QUERIES, lane);
   int len = lens[at.b];
-  kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, lane);
+  kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, rg, lane);
   bool fresh = at.t == 0;        // this piece begins with its unit
   int64_t slot = 2 * wk;         // where it goes when it is not the whole unit
   int i = 0, stage = 0, phase = 0;
@@ -580,7 +645,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
     const int key0 = at.t * kKv8Keys;
     const int valid = min(len - key0, kKv8Keys);
     const int sees = a.causal ? len - a.T_q : len - 1;       // the fewest keys that a row sees
-    kv8_tile<D, NT, RG>(w, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, lane, ring);
+    kv8_tile<D, NT, RG>(w, a, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, rg, lane, ring);
     __syncwarp();
     if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
     if (rg == 0 && i + STAGES < n) {
@@ -601,7 +666,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
       if (i + 1 < n) {
         kv8_next_unit(at, prefix, a.N, a.h_kv);
         len = lens[at.b];
-        kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, lane);
+        kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, rg, lane);
         fresh = true;
         slot = 2 * wk + 1;
       }
@@ -619,50 +684,82 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   }
 }
 
-// Folds the pieces of every unit that more than one worker streamed, in the order of its keys, and writes the
-// rows of empty sequences.  W warps a row.
-template <int D, bool BF16, int W>
+// The pieces of a unit that more than one worker streamed: n >= 2 of them, of workers w0, w0 + 1, ...; the first
+// one's slot is 2 w0 + first.
+struct Kv8Pieces {
+  int64_t w0;
+  int n, first, row;
+};
+
+// of output row r, for few units: from the lengths
+__device__ __forceinline__ Kv8Pieces kv8_pieces(const Kv8Params& a, int64_t r) {
+  Kv8Pieces p = {0, 0, 0, 0};
+  const int h = (int)(r % a.h_q);
+  const int64_t bt = r / a.h_q;
+  const int t = (int)(bt % a.T_q), b = (int)(bt / a.T_q), g = h / a.G;
+  p.row = t * a.G + h - g * a.G;
+  const int64_t p0 = __ldcg(a.prefix + b), tiles = __ldcg(a.prefix + b + 1) - p0;
+  const int64_t total = __ldcg(a.prefix + a.N) * a.h_kv;
+  if (tiles == 0) return p;
+  const int64_t share = (total + a.workers - 1) / a.workers, start = p0 * a.h_kv + g * tiles;
+  p.w0 = start / share;
+  p.n = (int)((start + tiles - 1) / share - p.w0) + 1;
+  p.first = start > p.w0 * share ? 1 : 0;
+  return p;
+}
+
+__device__ __forceinline__ int64_t kv8_slot_row(const Kv8Params& a, const Kv8Pieces& p, int s) {
+  return (2 * (p.w0 + s) + (s == 0 ? p.first : 0)) * a.rows + p.row;
+}
+
+// Folds the pieces of every unit that more than one worker streamed, in the order of its keys.
+// SLICED = false, for batches whose units have a few pieces each: a warp for each worker's range (whose first cut
+// unit the worker has noted: no search, no division) and row, all D columns.
+// SLICED = true, for few units of many pieces: a CTA for 32 columns of an output row, 8 lanes for each piece.
+template <int D, bool BF16, bool SLICED>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_kv8_merge_kernel(const Kv8Params a) {
-  constexpr int PER = D / 32, RPB = kMergeThreads / (32 * W);
-  __shared__ float sm[RPB][W * (D + 2)];
+  constexpr int WARPS = kMergeThreads / 32;
+  constexpr int LANES = SLICED ? 8 : 32;                 // lanes of a piece
+  constexpr int PER = (SLICED ? 32 : D) / LANES;         // columns of a lane
+  constexpr int SUBS = 32 / LANES, STEP = SLICED ? WARPS * SUBS : 1;
+  constexpr int LOADS = 4;
   if (threadIdx.x == 0) ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = warp / W, w = warp % W;
-  const int64_t R = (int64_t)a.N * a.T_q * a.h_q, r = (int64_t)blockIdx.x * RPB + rr;
-  int n = 0, row = 0, first = 0;
-  int64_t w0 = 0, tiles = -1;
-  if (r < R) {
-    const int h = (int)(r % a.h_q);
-    const int64_t bt = r / a.h_q;
-    const int t = (int)(bt % a.T_q), b = (int)(bt / a.T_q), g = h / a.G;
-    row = t * a.G + h - g * a.G;
-    const int64_t p0 = __ldcg(a.prefix + b);
-    tiles = __ldcg(a.prefix + b + 1) - p0;
-    if (tiles > 0) {
-      const int64_t total = __ldcg(a.prefix + a.N) * a.h_kv, share = (total + a.workers - 1) / a.workers;
-      const int64_t start = p0 * a.h_kv + g * tiles;
-      w0 = start / share;
-      n = (int)((start + tiles - 1) / share - w0) + 1;
-      first = start > w0 * share ? 1 : 0;
-    }
+  Kv8Pieces pc;
+  int64_t out;   // element offset of the output row
+  int col = lane % LANES * PER;
+  if constexpr (SLICED) {
+    const int64_t r = blockIdx.x / (D / 32);
+    col += (int)(blockIdx.x % (D / 32)) * 32;
+    pc = kv8_pieces(a, r);
+    out = r * D;
+  } else {
+    const uint32_t i = blockIdx.x * WARPS + warp, w = i / (uint32_t)a.rows;
+    if (w >= (uint32_t)a.workers) return;
+    const int4 unit = __ldcg(a.splits + w);
+    pc.w0 = (int64_t)w - 1;
+    pc.n = unit.z;
+    pc.first = unit.w;
+    pc.row = (int)(i - w * (uint32_t)a.rows);
+    const int t = pc.row / a.G;
+    out = (((int64_t)unit.x * a.T_q + t) * a.h_q + (int64_t)unit.y * a.G + (pc.row - t * a.G)) * D;
   }
-  if (n == 1) n = 0;            // written by its worker
-  else if (tiles == 0) n = -1;  // nothing to attend to: zeros
+  if (pc.n < 2 || !idx_ok(out + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
   float M = -CUDART_INF_F, L = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  for (int s0 = w; s0 < n; s0 += W * kMergeChunk) {
-    float mj[kMergeChunk], lj[kMergeChunk], oj[kMergeChunk][PER];
+  for (int s0 = SLICED ? warp * SUBS + lane / LANES : 0; s0 < pc.n; s0 += LOADS * STEP) {
+    float mj[LOADS], lj[LOADS], oj[LOADS][PER];
 #pragma unroll
-    for (int j = 0; j < kMergeChunk; ++j) {
-      const int s = s0 + j * W;
-      const int64_t at = (2 * (w0 + s) + (s == 0 ? first : 0)) * a.rows + row;
-      const bool have = s < n && idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status);
+    for (int j = 0; j < LOADS; ++j) {
+      const int s = s0 + j * STEP;
+      const int64_t at = kv8_slot_row(a, pc, s);
+      const bool have = s < pc.n && idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status);
       mj[j] = have ? __ldcg(a.ws_m + at) : -CUDART_INF_F;
       lj[j] = have ? __ldcg(a.ws_l + at) : 0.f;
-      const float* src = a.ws_o + at * D + lane * PER;
+      const float* src = a.ws_o + at * D + col;
       if constexpr (PER == 4) {
         const float4 v = have ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
         oj[j][0] = v.x; oj[j][1] = v.y; oj[j][2] = v.z; oj[j][3] = v.w;
@@ -673,14 +770,14 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
     }
     float Mc = M;
 #pragma unroll
-    for (int j = 0; j < kMergeChunk; ++j) Mc = fmaxf(Mc, mj[j]);
+    for (int j = 0; j < LOADS; ++j) Mc = fmaxf(Mc, mj[j]);
     if (Mc == -CUDART_INF_F) continue;
     const float so = ptx::ex2(M - Mc);
     L *= so;
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] *= so;
 #pragma unroll
-    for (int j = 0; j < kMergeChunk; ++j) {
+    for (int j = 0; j < LOADS; ++j) {
       const float f = ptx::ex2(mj[j] - Mc);
       L += f * lj[j];
 #pragma unroll
@@ -688,36 +785,46 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
     }
     M = Mc;
   }
-  if constexpr (W > 1) {
-    float* mine = sm[rr] + w * (D + 2);
+  if constexpr (SLICED) {
+    // the groups of a warp, then the warps
+    __shared__ float sm[WARPS][32 + 2];
+    float Mt = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+    Mt = fmaxf(Mt, __shfl_xor_sync(0xffffffffu, Mt, 16));
+    const float f = M == -CUDART_INF_F ? 0.f : ptx::ex2(M - Mt);
+    L *= f;
+    L += __shfl_xor_sync(0xffffffffu, L, 8);
+    L += __shfl_xor_sync(0xffffffffu, L, 16);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mine[lane * PER + i] = acc[i];
+    for (int i = 0; i < PER; ++i) {
+      acc[i] *= f;
+      acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 8);
+      acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+      if (lane < LANES) sm[warp][lane * PER + i] = acc[i];
+    }
     if (lane == 0) {
-      mine[D] = M;
-      mine[D + 1] = L;
+      sm[warp][32] = Mt;
+      sm[warp][33] = L;
     }
     __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int k = 0; k < W; ++k) M = fmaxf(M, sm[rr][k * (D + 2) + D]);
+    if (threadIdx.x >= LANES) return;
+    M = -CUDART_INF_F;
     L = 0.f;
 #pragma unroll
+    for (int k = 0; k < WARPS; ++k) M = fmaxf(M, sm[k][32]);
+#pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    if (M != -CUDART_INF_F)
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        const float* wk = sm[rr] + k * (D + 2);
-        const float f = ptx::ex2(wk[D] - M);
-        L += f * wk[D + 1];
+    for (int k = 0; k < WARPS; ++k) {
+      const float g = sm[k][32] == -CUDART_INF_F ? 0.f : ptx::ex2(sm[k][32] - M);
+      L += g * sm[k][33];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] += f * wk[lane * PER + i];
-      }
+      for (int i = 0; i < PER; ++i) acc[i] += g * sm[k][lane * PER + i];
+    }
   }
-  if (n == 0) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
-    Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), r * D + lane * PER + i, acc[i] * inv, acc[i + 1] * inv);
+    Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), out + col + i, acc[i] * inv, acc[i + 1] * inv);
 }
 
 }  // namespace gqa
