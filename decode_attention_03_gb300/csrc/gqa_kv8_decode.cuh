@@ -85,6 +85,50 @@ __device__ __forceinline__ void kv8_unpack(uint32_t w, uint32_t& lo, uint32_t& h
       : "r"(w));
 }
 
+// The MMA and the 8x8 transpose as ptx:: has them, but free to be scheduled among the shared-memory reads.
+__device__ __forceinline__ void kv8_mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ uint32_t kv8_transpose(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// two fp32 operations in one instruction
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two t;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(lo), "f"(hi));
+  return t;
+}
+__device__ __forceinline__ float2 split(Two t) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t.v));
+  return f;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
 // 2^(e - 127 + d) for d <= 0, 0 where that leaves the range
 __device__ __forceinline__ float kv8_ratio(int d) { return __uint_as_float((uint32_t)max(d + 127, 0) << 23); }
 
@@ -316,7 +360,11 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params
 #pragma unroll
     for (int j = 0; j < KD; ++j)
       raw[j] = ok ? __ldg(reinterpret_cast<const uint2*>(a.q + at + 16 * j)) : make_uint2(0u, 0u);
-    float qs = a.scale_log2;
+    float qs = fabsf(a.scale_log2);
+    if (a.scale_log2 < 0.f) {    // the factor of a row is kept >= 0, so that the largest y is the largest logit
+#pragma unroll
+      for (int j = 0; j < KD; ++j) raw[j] = make_uint2(raw[j].x ^ 0x80008000u, raw[j].y ^ 0x80008000u);
+    }
     if constexpr (BF16) {
       uint32_t top = 0;
 #pragma unroll
@@ -335,6 +383,7 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params
         raw[j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
       }
     }
+    qs = fmaxf(qs, 1.2e-38f);      // not 0: a hidden key's y is -inf
     if constexpr (W::Q_SMEM) {
 #pragma unroll
       for (int j = 0; j < KD; ++j)
@@ -408,7 +457,10 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     for (int nt = 0; nt < NT; ++nt) s[p][nt][0] = s[p][nt][1] = s[p][nt][2] = s[p][nt][3] = 0.f;
 #pragma unroll
   for (int j = 0; j < KD; j += 2) {
-    uint32_t q[2][NT][2];
+    uint32_t q[2][NT][2], x[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      ptx::ldmatrix_x4(x[p], smem_clamp(st + w.rows[p] + ((uint32_t)(j << 4) ^ w.turn), 16, ring.lo, ring.hi, ring.status));
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -424,52 +476,66 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      uint32_t x[4], f[2][4];
-      ptx::ldmatrix_x4(x, smem_clamp(st + w.rows[p] + ((uint32_t)(j << 4) ^ w.turn), 16, ring.lo, ring.hi, ring.status));
-      kv8_unpack(x[0], f[0][0], f[0][2]);
-      kv8_unpack(x[1], f[0][1], f[0][3]);
-      kv8_unpack(x[2], f[1][0], f[1][2]);
-      kv8_unpack(x[3], f[1][1], f[1][3]);
+      uint32_t f[2][4];
+      kv8_unpack(x[p][0], f[0][0], f[0][2]);
+      kv8_unpack(x[p][1], f[0][1], f[0][3]);
+      kv8_unpack(x[p][2], f[1][0], f[1][2]);
+      kv8_unpack(x[p][3], f[1][1], f[1][3]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        ptx::mma_16816(s[p][nt], f[0], q[0][nt]);
-        ptx::mma_16816(s[p][nt], f[1], q[1][nt]);
-      }
+      for (int nt = 0; nt < NT; ++nt) kv8_mma(s[p][nt], f[0], q[0][nt]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) kv8_mma(s[p][nt], f[1], q[1][nt]);
     }
   }
-  // ---- scores in log2 units; s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
+  // ---- y = the scores by the K scales; the logit in log2 units is y qs, qs >= 0 of the row.
+  // s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
   top = __reduce_max_sync(0xffffffffu, top);
   bool over = false;
   float mx[NT][2];
+  Two y[4][NT], qs[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float qs[2];
     if constexpr (W::Q_SMEM) {
+      float2 f;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(qs[0]), "=f"(qs[1])
+                   : "=f"(f.x), "=f"(f.y)
                    : "r"(w.q_at + KD * NT * 256 + (nt * 8 + 2 * (lane & 3)) * 4));
+      qs[nt] = two(f.x, f.y);
     } else {
-      qs[0] = w.qs[nt][0];
-      qs[1] = w.qs[nt][1];
+      qs[nt] = two(w.qs[nt][0], w.qs[nt][1]);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+  for (int o = 0; o < 4; ++o) {
+    const float k = kv8_scale((uint32_t)ek[o]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) y[o][nt] = mul2(two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]), two(k, k));
+  }
+  if (masked) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // the last key that each row sees: token row / G of T_q
+      int lim[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = (rg * NT + nt) * 8 + 2 * (lane & 3) + i;
+        lim[i] = w.last - key0 - (a.causal ? max(a.T_q - 1 - row / a.G, 0) : 0);
+      }
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-        float& x = s[o >> 1][nt][(o & 1) * 2 + i];
-        x = x * qs[i] * kv8_scale((uint32_t)ek[o]);
+        const float2 f = split(y[o][nt]);
+        y[o][nt] = two(8 * o + r > lim[0] ? -CUDART_INF_F : f.x, 8 * o + r > lim[1] ? -CUDART_INF_F : f.y);
       }
-      if (masked) {
-        // the last key that the row sees: token row / G of T_q
-        const int row = (rg * NT + nt) * 8 + 2 * (lane & 3) + i;
-        const int lim = w.last - key0 - (a.causal ? max(a.T_q - 1 - row / a.G, 0) : 0);
-#pragma unroll
-        for (int o = 0; o < 4; ++o)
-          if (8 * o + r > lim) s[o >> 1][nt][(o & 1) * 2 + i] = -CUDART_INF_F;
-      }
-      mx[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i]));
-      over |= mx[nt][i] > w.m[nt][i] + kKv8Slack;
     }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 f0 = split(y[0][nt]), f1 = split(y[1][nt]), f2 = split(y[2][nt]), f3 = split(y[3][nt]);
+    const float2 t = split(mul2(two(fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x)), fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y))),
+                                qs[nt]));
+    mx[nt][0] = t.x;
+    mx[nt][1] = t.y;
+    over |= t.x > w.m[nt][0] + kKv8Slack || t.y > w.m[nt][1] + kKv8Slack;
   }
   const bool grow = __any_sync(0xffffffffu, over);
   if (grow || top > w.e) {
@@ -502,23 +568,30 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
         for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f[nt][i & 1];
   }
   // ---- weights, and P as the B operand
-  float fv[4];
-#pragma unroll
-  for (int o = 0; o < 4; ++o) fv[o] = kv8_ratio(ev[o] - w.e);
   uint32_t pf[2][NT][2];
+  Two off[NT], sum[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float u[2];
+    off[nt] = two(w.m[nt][0] == -CUDART_INF_F ? 0.f : -w.m[nt][0], w.m[nt][1] == -CUDART_INF_F ? 0.f : -w.m[nt][1]);
+    sum[nt] = two(w.l[nt][0], w.l[nt][1]);
+  }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) u[i] = w.m[nt][i] == -CUDART_INF_F ? 0.f : w.m[nt][i];
+  for (int o = 0; o < 4; ++o) {
+    const float v = kv8_ratio(ev[o] - w.e);
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      const float p0 = ptx::ex2(s[o >> 1][nt][(o & 1) * 2] - u[0]);
-      const float p1 = ptx::ex2(s[o >> 1][nt][(o & 1) * 2 + 1] - u[1]);
-      w.l[nt][0] += p0;
-      w.l[nt][1] += p1;
-      pf[o >> 1][nt][o & 1] = ptx::movmatrix_trans(ptx::pack_half2(p0 * fv[o], p1 * fv[o]));
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = split(fma2(y[o][nt], qs[nt], off[nt]));
+      const Two p = two(ptx::ex2(x.x), ptx::ex2(x.y));
+      sum[nt] = add2(sum[nt], p);
+      const float2 pv = split(mul2(p, two(v, v)));
+      pf[o >> 1][nt][o & 1] = kv8_transpose(ptx::pack_half2(pv.x, pv.y));
     }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 f = split(sum[nt]);
+    w.l[nt][0] = f.x;
+    w.l[nt][1] = f.y;
   }
   // ---- O^T += V^T P^T; accumulator rows r, r + 8 of tile j: d = 16j + 2r, 16j + 2r + 1
 #pragma unroll
@@ -532,8 +605,8 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       for (int i = 0; i < 4; ++i) kv8_unpack(__byte_perm(x[i], 0, 0x3120), f[i >> 1][(i & 1) * 2], f[i >> 1][(i & 1) * 2 + 1]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        ptx::mma_16816(w.acc[j][nt], f[0], pf[p][nt]);
-        ptx::mma_16816(w.acc[j + 1][nt], f[1], pf[p][nt]);
+        kv8_mma(w.acc[j][nt], f[0], pf[p][nt]);
+        kv8_mma(w.acc[j + 1][nt], f[1], pf[p][nt]);
       }
     }
 }
