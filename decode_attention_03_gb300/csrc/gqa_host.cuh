@@ -17,10 +17,10 @@ inline bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<
 // Launch with programmatic stream serialisation: the kernel may begin launching while the
 // previous kernel in the stream finishes (it waits in griddepcontrol.wait before reading).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
                             Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -34,7 +34,7 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned bl
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
-  return launch_pdl_smem(kernel, grid, block, 0, st, args...);
+  return launch_pdl_smem(kernel, dim3(grid, 1, 1), block, 0, st, args...);
 }
 
 }  // namespace gqa

@@ -15,6 +15,8 @@ namespace {
 
 bool block_size_ok(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64; }
 
+int log2_of(int block_size) { return block_size == 8 ? 3 : (block_size == 16 ? 4 : (block_size == 32 ? 5 : 6)); }
+
 bool aligned_to(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
@@ -50,16 +52,16 @@ template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
 cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
   constexpr int HPW = 32 / (D / (2 * CW));
   const int qg = (p.h_q + HPW - 1) / HPW, kg = (p.h_kv + HPW - 1) / HPW;
-  for (p.iters = 4;; p.iters /= 2) {
+  int sets = 0;
+  for (p.iters = kAppendIters;; p.iters /= 2) {
     p.q_sets = (qg + p.iters - 1) / p.iters;
     p.k_sets = (kg + p.iters - 1) / p.iters;
-    p.sets = p.q_sets + 2 * p.k_sets;
-    if (p.iters == 1 || (int64_t)p.num_tokens * p.sets >= (int64_t)sms * 4 * (kAppendThreads / 32)) break;
+    sets = p.q_sets + 2 * p.k_sets;
+    if (p.iters == 1 || (int64_t)p.num_tokens * sets >= (int64_t)sms * 4 * (kAppendThreads / 32)) break;
   }
-  const int64_t warps = (int64_t)p.num_tokens * p.sets, per = kAppendThreads / 32;
-  const int64_t blocks = (warps + per - 1) / per;
-  if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-  return launch_pdl(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, (unsigned)blocks, kAppendThreads, st, p);
+  const unsigned per = kAppendThreads / 32;
+  const dim3 grid(((unsigned)p.num_tokens + per - 1) / per, (unsigned)sets);
+  return launch_pdl_smem(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, grid, kAppendThreads, 0, st, p);
 }
 
 template <int D, bool BF16, int CW, bool PAIRS>
@@ -81,7 +83,7 @@ cudaError_t append_run(const AppendParams& p, int layout, int sms, cudaStream_t 
 
 gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void* stream) {
   if (a.num_tokens < 0 || a.h_q < 0 || a.h_kv < 1 || a.num_blocks < 0) return GQA_ERR_INVALID_ARG;
-  if (a.h_q > 65535 || a.h_kv > 65535 || a.h_q % a.h_kv != 0) return GQA_ERR_INVALID_ARG;
+  if (a.h_q > 32767 || a.h_kv > 16383 || a.h_q % a.h_kv != 0) return GQA_ERR_INVALID_ARG;   // sets fit a grid's y
   if (a.d_head != 64 && a.d_head != 128) return GQA_ERR_UNSUPPORTED;
   if (!block_size_ok(a.block_size) || (int64_t)a.num_blocks * a.block_size >= (int64_t(1) << 31))
     return GQA_ERR_INVALID_ARG;
@@ -123,7 +125,7 @@ gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void
   p.status = static_cast<uint32_t*>(ws);
   p.num_tokens = a.num_tokens; p.h_q = a.h_q; p.h_kv = a.h_kv;
   p.max_position = a.max_position; p.rot_dim = a.rot_dim; p.interleaved = a.interleaved ? 1 : 0;
-  p.num_blocks = a.num_blocks; p.block_size = a.block_size;
+  p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.bs_log = log2_of(a.block_size);
   p.eps = a.eps;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.d_head == 64)
@@ -258,7 +260,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   p.ws_o = reinterpret_cast<float*>(wsb + lay.o);
   p.T_q = T_q; p.h_q = h_q; p.h_kv = h_kv; p.G = h_q / h_kv; p.rows = rows;
   p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size;
-  p.bs_log = block_size == 8 ? 3 : (block_size == 16 ? 4 : (block_size == 32 ? 5 : 6));
+  p.bs_log = log2_of(block_size);
   p.causal = opt.causal ? 1 : 0;
   p.stall = opt.test_stall_cta;
   p.scale_log2 = scale * kLog2e;
@@ -289,10 +291,10 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
 // ---------------------------------------------------------------- read
 template <int D, bool BF16>
 cudaError_t read_launch(const Kv8ReadParams& p, cudaStream_t st) {
-  const int64_t warps = (int64_t)p.num_seqs * p.groups * p.h_kv, per = kReadThreads / 32;
-  const int64_t blocks = (warps + per - 1) / per;
-  if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-  return launch_pdl(gqa_kv8_read_kernel<D, BF16>, (unsigned)blocks, kReadThreads, st, p);
+  const int64_t groups = (p.most + ReadCfg<D>::TOKENS - 1) / ReadCfg<D>::TOKENS, per = kReadThreads / 32;
+  const int64_t blocks = (groups * p.h_kv + per - 1) / per;
+  return launch_pdl_smem(gqa_kv8_read_kernel<D, BF16>, dim3((unsigned)blocks, (unsigned)p.num_seqs), kReadThreads, 0, st,
+                         p);
 }
 
 gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* lens, const int32_t* begins,
@@ -302,6 +304,8 @@ gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* le
   gqa_status s = check_kv8(N, h_kv, D, max_blocks, num_blocks, block_size);
   if (s != GQA_OK) return s;
   if (out_len < 0 || out_len >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
+  const int64_t most = out_len < (int64_t)max_blocks * block_size ? out_len : (int64_t)max_blocks * block_size;
+  if ((most / 16 + 1) * h_kv >= (int64_t(1) << 30)) return GQA_ERR_INVALID_ARG;   // warps of a sequence
   if (N == 0 || out_len == 0) return GQA_OK;
   if (k_out == nullptr && v_out == nullptr) return GQA_ERR_INVALID_ARG;
   if (!aligned16(cache) || (k_out != nullptr && !aligned16(k_out)) || (v_out != nullptr && !aligned16(v_out)) ||
@@ -313,11 +317,10 @@ gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* le
   p.block_tables = tables; p.seq_lens = lens; p.begins = begins;
   p.k_out = k_out; p.v_out = v_out; p.status = static_cast<uint32_t*>(ws);
   p.out_len = out_len;
-  p.num_seqs = N; p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size; p.h_kv = h_kv;
+  p.num_seqs = N; p.max_blocks = max_blocks; p.num_blocks = num_blocks; p.block_size = block_size;
+  p.bs_log = log2_of(block_size); p.h_kv = h_kv;
   // tokens past the table exist in no sequence: no warps for them
-  const int64_t most = out_len < (int64_t)max_blocks * block_size ? out_len : (int64_t)max_blocks * block_size;
-  const int tokens = D == 64 ? ReadCfg<64>::TOKENS : ReadCfg<128>::TOKENS;
-  p.groups = (most + tokens - 1) / tokens;
+  p.most = most;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = opt != nullptr && opt->bf16;
   if (D == 64) return cuda_status(bf16 ? read_launch<64, true>(p, st) : read_launch<64, false>(p, st));

@@ -14,6 +14,7 @@
 namespace gqa {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendIters = 4;   // groups of heads of a warp at most
 constexpr int kReadThreads = 256;
 
 __host__ __device__ constexpr int kv8_block_bytes(int block_size, int D) { return block_size * (2 * D + 2); }
@@ -52,6 +53,36 @@ __device__ __forceinline__ uint32_t kv8_halves(uint16_t codes) {
 
 __device__ __forceinline__ float2 half2_floats(uint32_t h) { return __half22float2(*reinterpret_cast<__half2*>(&h)); }
 
+// two fp32 operations in one instruction
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two t;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(lo), "f"(hi));
+  return t;
+}
+__device__ __forceinline__ float2 split(Two t) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t.v));
+  return f;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
 template <bool BF16>
 __device__ __forceinline__ void unpack4(uint2 r, float* x) {
   if constexpr (BF16) {
@@ -78,7 +109,7 @@ struct AppendParams {
   const int64_t* slots;
   void *k_cache, *v_cache;
   uint32_t* status;
-  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, sets, q_sets, k_sets, iters;
+  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, bs_log, q_sets, k_sets, iters;
   float eps;
 };
 
@@ -99,6 +130,27 @@ __device__ __forceinline__ Chunk<CW> load_chunk(const uint16_t* p) {
     c.w[0] = v.x; c.w[1] = v.y;
   }
   return c;
+}
+
+// the same into shared memory, asynchronously
+template <int CW>
+__device__ __forceinline__ void copy_chunk(Chunk<CW>* to, const uint16_t* from) {
+  if constexpr (CW == 8)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+}
+
+// of N groups of copies, groups 0 .. i are there
+template <int N>
+__device__ __forceinline__ void wait_copies(int i) {
+  static_assert(N == 4, "groups");
+  switch (i) {
+    case 0: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+  }
 }
 
 template <int CW>
@@ -142,8 +194,8 @@ __device__ __forceinline__ void load_floats(float* x, const float* p) {
 // A head's D elements lie on D/(2 CW) lanes, each with two chunks of CW: elements CW s.. and rot/2 + CW s.. for
 // the lanes s < rot/(2 CW) that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
 // thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes
-// heads of one kind (queries, keys or values) of one token: 32/(D/(2 CW)) at a time, up to a.iters times, the next
-// ones' loads in flight; cosines, sines and norm weights stay in registers over its heads.  Bound by its bytes, the
+// heads of one kind (queries, keys or values) of one token: 32/(D/(2 CW)) at a time, up to a.iters times, all
+// of them copied to the threads' own places in shared memory at the start; cosines, sines and norm weights stay in registers over its heads.  Bound by its bytes, the
 // heads read and written once, when there are many tokens; the sums of squares and maxima go through log2 of
 // the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
 // Four CTAs an SM (64 registers, a few spilled): 16384 tokens of 64 + 8 + 8 heads of 128 took 120.1 us with four,
@@ -154,10 +206,10 @@ gqa_append_kernel(const AppendParams a) {
   constexpr int LPH = D / (2 * CW), HPW = 32 / LPH;
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31, sub = lane % LPH;
-  const int64_t w = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
-  const int64_t t = w / a.sets;
+  // a CTA has one set of heads of kAppendThreads / 32 tokens
+  const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   if (t >= a.num_tokens) return;
-  int set = (int)(w - t * a.sets);
+  int set = blockIdx.y;
   const int kind = set < a.q_sets ? 0 : (set < a.q_sets + a.k_sets ? 1 : 2);
   set -= kind == 0 ? 0 : (kind == 1 ? a.q_sets : a.q_sets + a.k_sets);
   const int heads = kind == 0 ? a.h_q : a.h_kv;
@@ -168,11 +220,17 @@ gqa_append_kernel(const AppendParams a) {
   off[0] = turns ? CW * sub : rot + CW * (sub - rot / (2 * CW));
   off[1] = off[0] + (turns ? rot / 2 : (D - rot) / 2);
 
-  const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
-  Chunk<CW> next[2] = {};
-  if (h < heads) {
-    next[0] = load_chunk<CW>(src + h * D + off[0]);
-    next[1] = load_chunk<CW>(src + h * D + off[1]);
+  __shared__ __align__(16) Chunk<CW> stage[kAppendIters][2][kAppendThreads];   // a thread's own places
+  {
+    const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+#pragma unroll
+    for (int it = 0; it < kAppendIters; ++it) {
+      if (it < a.iters && h + it * HPW < heads) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) copy_chunk<CW>(&stage[it][j][threadIdx.x], src + (h + it * HPW) * D + off[j]);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
   }
   int64_t slot = -1, blk = 0;
   int row = 0;
@@ -182,8 +240,8 @@ gqa_append_kernel(const AppendParams a) {
       if (lane == 0) atomicOr(a.status, kDevBadInput);
       slot = -1;
     }
-    blk = (uint32_t)slot / (uint32_t)a.block_size;
-    row = (int)((uint32_t)slot % (uint32_t)a.block_size);
+    blk = (uint32_t)slot >> a.bs_log;
+    row = (int)slot & (a.block_size - 1);
   }
   float cs[2][CW];          // cosines and sines of this lane's pairs
   if (a.cos_sin != nullptr) {
@@ -215,16 +273,20 @@ gqa_append_kernel(const AppendParams a) {
 #pragma unroll 1
   for (int it = 0; it < a.iters; ++it, h += HPW) {
     float x[2][CW];
-    unpack_chunk<BF16, CW>(next[0], x[0]);
-    unpack_chunk<BF16, CW>(next[1], x[1]);
-    if (it + 1 < a.iters && h + HPW < heads) {
-      next[0] = load_chunk<CW>(src + (h + HPW) * D + off[0]);
-      next[1] = load_chunk<CW>(src + (h + HPW) * D + off[1]);
-    }
+    wait_copies<kAppendIters>(it);
+    unpack_chunk<BF16, CW>(stage[it][0][threadIdx.x], x[0]);
+    unpack_chunk<BF16, CW>(stage[it][1][threadIdx.x], x[1]);
     if (weight != nullptr) {
-      float ss = 0.f;
+      Two sq[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < CW; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) {
+          const Two v = two(x[j][i], x[j][i + 1]);
+          sq[j] = fma2(v, v, sq[j]);
+        }
+      const float2 sums = split(add2(sq[0], sq[1]));
+      float ss = sums.x + sums.y;
 #pragma unroll
       for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
@@ -236,7 +298,11 @@ gqa_append_kernel(const AppendParams a) {
         for (int i = 0; i < CW / 2; ++i) asm volatile("" : "+r"(wt[j].w[i]));
         unpack_chunk<BF16, CW>(wt[j], g);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) x[j][i] = x[j][i] * r * g[i];
+        for (int i = 0; i < CW; i += 2) {
+          const float2 v = split(mul2(mul2(two(x[j][i], x[j][i + 1]), two(r, r)), two(g[i], g[i + 1])));
+          x[j][i] = v.x;
+          x[j][i + 1] = v.y;
+        }
       }
     }
     if (turns && kind < 2) {
@@ -307,8 +373,8 @@ struct Kv8ReadParams {
   const int32_t *block_tables, *seq_lens, *begins;
   uint16_t *k_out, *v_out;
   uint32_t* status;
-  int64_t out_len, groups;   // token groups of a sequence
-  int num_seqs, max_blocks, num_blocks, block_size, h_kv;
+  int64_t out_len, most;   // rows of an output sequence, and how many of them there can be tokens for
+  int num_seqs, max_blocks, num_blocks, block_size, bs_log, h_kv;
 };
 
 // One warp for 4 * RPP tokens of one head: D/16 lanes a row, 16 codes a lane, the loads of K and V of all
@@ -325,11 +391,10 @@ gqa_kv8_read_kernel(const Kv8ReadParams a) {
   constexpr int LPR = ReadCfg<D>::LPR, RPP = ReadCfg<D>::RPP, P = ReadCfg<D>::P;
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31, c = lane % LPR;
-  int64_t w = ((int64_t)blockIdx.x * kReadThreads + threadIdx.x) >> 5;
-  if (w >= (int64_t)a.num_seqs * a.groups * a.h_kv) return;
-  const int g = (int)(w % a.h_kv);
-  w /= a.h_kv;
-  const int64_t b = w / a.groups, i0 = (w - b * a.groups) * ReadCfg<D>::TOKENS;
+  const uint32_t w = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5), group = w / (uint32_t)a.h_kv;
+  const int g = (int)(w - group * (uint32_t)a.h_kv);
+  const int64_t b = blockIdx.y, i0 = (int64_t)group * ReadCfg<D>::TOKENS;
+  if (i0 >= a.most) return;
   const int cap = a.max_blocks * a.block_size;
   int len = a.seq_lens[b];
   const int begin = a.begins != nullptr ? a.begins[b] : 0;
@@ -347,7 +412,7 @@ gqa_kv8_read_kernel(const Kv8ReadParams a) {
     const int64_t i = i0 + p * RPP + lane / LPR, tok = begin + i;
     have[p] = false;
     if (i < a.out_len && tok < len) {
-      const int j = (int)((uint32_t)tok / (uint32_t)a.block_size), row = (int)tok - j * a.block_size;
+      const int j = (int)((uint32_t)tok >> a.bs_log), row = (int)tok & (a.block_size - 1);
       const int id = __ldg(a.block_tables + b * a.max_blocks + j);
       have[p] = id >= 0 && id < a.num_blocks;
       if (!have[p]) atomicOr(a.status, kDevBadInput);

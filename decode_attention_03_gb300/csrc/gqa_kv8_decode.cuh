@@ -99,36 +99,6 @@ __device__ __forceinline__ uint32_t kv8_transpose(uint32_t x) {
   return y;
 }
 
-// two fp32 operations in one instruction
-struct Two {
-  uint64_t v;
-};
-__device__ __forceinline__ Two two(float lo, float hi) {
-  Two t;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(lo), "f"(hi));
-  return t;
-}
-__device__ __forceinline__ float2 split(Two t) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t.v));
-  return f;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  Two d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return d;
-}
-
 // 2^(e - 127 + d) for d <= 0, 0 where that leaves the range
 __device__ __forceinline__ float kv8_ratio(int d) { return __uint_as_float((uint32_t)max(d + 127, 0) << 23); }
 
