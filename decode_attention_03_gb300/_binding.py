@@ -182,13 +182,14 @@ _ws_lock = threading.Lock()
 _ws_cache = {}
 
 
-def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
-    """A zero-initialised workspace of at least ``nbytes``, cached per (device, stream).
+def workspace(nbytes: int, device=None, stream=None, use: Optional[str] = None) -> torch.Tensor:
+    """A zero-initialised workspace of at least ``nbytes``, cached per (device, stream), and per ``use`` for
+    calls whose partials may lie where others expect zeroed counters.
 
     Calls that share a workspace must not overlap on the GPU: keep one per stream."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     sid = _stream(stream).value or 0
-    key = (dev.index, sid)
+    key = (dev.index, sid) if use is None else (dev.index, sid, use)
     with _ws_lock:
         t = _ws_cache.get(key)
         if t is None or t.numel() < nbytes:
@@ -679,9 +680,9 @@ def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Ten
             ws = torch.empty(n, dtype=_U8, device=q.device)
             ws[:256].zero_()
         else:
-            ws = _ws_cache.get((dev, raw))
+            ws = _ws_cache.get((dev, raw, "kv8"))
             if ws is None or ws.numel() < n:
-                ws = workspace(n, q.device)
+                ws = workspace(n, q.device, use="kv8")
     st = _decode_kv8_c(q.data_ptr(), cache.data_ptr(), tp, lp, out.data_ptr(), N, T_q, mb, cache.shape[0], bs, h_q,
                        h_kv, D, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), raw,
                        _pack_opts(0, 0, timeout_us, test_stall_cta, 0, 1 if causal else 0, 1 if dt is _BF16 else 0, 0))

@@ -213,7 +213,7 @@ cudaError_t kv8_launch(const Kv8Params& p, unsigned grid, cudaStream_t st) {
 }
 
 template <int D, bool BF16>
-cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool many_pieces, cudaStream_t st) {
+cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool cut, bool many_pieces, cudaStream_t st) {
   cudaError_t e;
   switch (cls) {
     case 0: e = kv8_launch<D, 1, 1, BF16>(p, grid, st); break;
@@ -221,7 +221,7 @@ cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool many_pie
     case 2: e = kv8_launch<D, 4, 1, BF16>(p, grid, st); break;
     default: e = kv8_launch<D, 4, 2, BF16>(p, grid, st); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !cut) return e;
   if (many_pieces)
     return launch_pdl(gqa_kv8_merge_kernel<D, BF16, true>, (unsigned)((int64_t)p.N * p.T_q * p.h_q * (D / 32)),
                       kMergeThreads, st, p);
@@ -278,11 +278,11 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     const unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
     p.workers = (int)grid * kv8_groups(cls);
     // pieces of a unit: about workers / units + 1 when the sequences are alike
-    const bool many = p.workers / units >= 7;
-    const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, many, st)
-                                          : kv8_decode<64, false>(p, cls, grid, many, st))
-                                  : (bf16 ? kv8_decode<128, true>(p, cls, grid, many, st)
-                                          : kv8_decode<128, false>(p, cls, grid, many, st));
+    const bool many = p.workers / units >= 7, cut = seq_tiles > 1;   // (a unit of one tile is never cut)
+    const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, cut, many, st)
+                                          : kv8_decode<64, false>(p, cls, grid, cut, many, st))
+                                  : (bf16 ? kv8_decode<128, true>(p, cls, grid, cut, many, st)
+                                          : kv8_decode<128, false>(p, cls, grid, cut, many, st));
     if (e != cudaSuccess) return GQA_ERR_CUDA;
   }
   return GQA_OK;

@@ -183,14 +183,38 @@ __device__ __forceinline__ void kv8_empty_rows(const Kv8Params& a, const int* le
         reinterpret_cast<uint4*>(a.o)[b * words + i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Block ids of the next tiles of a worker, one for each lane, and its copies.
+// The copying side of a worker: block ids of the next tiles, one for each lane (-1: no block, or a bad id), and what
+// this lane copies of a tile.
 struct Kv8Stream {
   Kv8Place at;       // next tile to copy
   Kv8Place ahead;    // first tile after the current window
   int id, id_next;   // this lane's block id in the current window and the one after it
   int t_end;         // tile of at's unit where the current window ends
-  int j0;            // block index of lane 0 in the current window
+  int k;             // lane of the window that holds at's first block
+  const uint8_t* head;     // head at.g of block 0
+  // the same for every tile: lanes 0 .. n - 1 copy `size` bytes from `off` of a (block, head) to `to` of the tile,
+  // + step in the second half of a block of 64
+  int n;
+  uint32_t size, to, off, step, stride;   // stride: bytes of a block
 };
+
+template <int D>
+__device__ __forceinline__ void kv8_stream_setup(Kv8Stream& s, const Kv8Params& a, int lane) {
+  const int bs = a.block_size, bb = kv8_block_bytes(bs, D);
+  s.stride = (uint32_t)a.h_kv * (uint32_t)bb;
+  if (bs <= kKv8Keys) {        // whole blocks
+    s.n = kKv8Keys >> a.bs_log;
+    s.size = bb;
+    s.to = lane * bb;
+    s.off = s.step = 0;
+  } else {                     // half a block: K, V, K exponents, V exponents
+    s.n = 4;
+    s.size = lane < 2 ? kKv8Keys * D : kKv8Keys;
+    s.to = lane < 2 ? lane * kKv8Keys * D : 2 * kKv8Keys * D + (lane - 2) * kKv8Keys;
+    s.off = lane < 2 ? lane * bs * D : 2 * bs * D + (lane - 2) * bs;
+    s.step = lane < 2 ? kKv8Keys * D : kKv8Keys;
+  }
+}
 
 // blocks of a sequence, the block that holds a tile's first key, and the tile where the window of 32 blocks
 // that starts at p ends
@@ -205,78 +229,67 @@ __device__ __forceinline__ int kv8_window_end(const Kv8Params& a, const Kv8Place
   return p.tiles - p.t < n ? p.tiles : p.t + n;
 }
 
-// this lane's block id of the window that starts at p; *end: the tile where the window ends
-__device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p, const int* lens, int lane, int* end) {
+// this lane's block id of the window that starts at p
+__device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p, const int* lens, int lane) {
   if (p.b >= a.N) return -1;
-  *end = kv8_window_end(a, p);
   const int j = kv8_first_block(a, p.t) + lane;
-  const int used = kv8_blocks(a, lens[p.b]);
-  if (j >= used || !idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status)) return -1;
+  if (j >= kv8_blocks(a, lens[p.b]) || !idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status))
+    return -1;
   return __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + j);
 }
 
-__device__ __forceinline__ void kv8_ahead(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix) {
+// Enters the window at s.at, whose ids are in s.id: reports bad ids, finds where the next window begins and starts
+// loading its ids.
+template <int D>
+__device__ __forceinline__ void kv8_enter(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
+                                          int lane) {
+  const int j = kv8_first_block(a, s.at.t) + lane;
+  if (j < kv8_blocks(a, lens[s.at.b]) && (s.id < 0 || s.id >= a.num_blocks)) {
+    atomicOr(a.status, kDevBadInput);
+    s.id = -1;
+  }
+  s.k = 0;
+  s.head = a.cache + (int64_t)s.at.g * kv8_block_bytes(a.block_size, D);
+  s.t_end = kv8_window_end(a, s.at);
   s.ahead = s.at;
   s.ahead.t = s.t_end;
-  if (s.t_end >= s.at.tiles) kv8_next_unit(s.ahead, prefix, a.N, a.h_kv);
-}
-
-__device__ __forceinline__ void kv8_start(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
-                                          int lane) {
-  s.j0 = kv8_first_block(a, s.at.t);
-  s.id = kv8_window(a, s.at, lens, lane, &s.t_end);
-  kv8_ahead(s, a, prefix);
-  int end;
-  s.id_next = kv8_window(a, s.ahead, lens, lane, &end);
+  if (s.t_end >= s.at.tiles) {
+    kv8_next_unit(s.ahead, prefix, a.N, a.h_kv);
+    // the next unit's queries into L2 (its rows lie together for each token)
+    const uint32_t bytes = (uint32_t)a.G * D * 2;
+    if (s.ahead.b < a.N)
+      for (uint32_t i = lane * 128; i < bytes; i += 32 * 128)
+        for (int t = 0; t < a.T_q; ++t)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(
+              a.q + (((int64_t)s.ahead.b * a.T_q + t) * a.h_q + (int64_t)s.ahead.g * a.G) * D) + i));
+  }
+  s.id_next = kv8_window(a, s.ahead, lens, lane);
 }
 
 // Copies the stream's next tile to `dst` and moves on.  Every lane of the warp calls this.
 template <int D>
 __device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
                                          uint32_t dst, uint32_t bar, uint64_t policy, int lane, const Win& ring) {
-  const int bs = a.block_size;
-  const int64_t bb = kv8_block_bytes(bs, D);
-  const bool half = bs > kKv8Keys;                  // 64: the tile is half a block, in four pieces
-  const int n = half ? 4 : kKv8Keys >> a.bs_log;
-  const int j = kv8_first_block(a, s.at.t) + (half ? 0 : lane);
-  const int src_lane = j - s.j0;
-  const int id = __shfl_sync(0xffffffffu, s.id, src_lane & 31);
-  const bool mine = lane < n && j < kv8_blocks(a, lens[s.at.b]);
-  const bool bad = mine && (id < 0 || id >= a.num_blocks);
-  if (bad) atomicOr(a.status, kDevBadInput);
-  const bool go = mine && !bad;
-  uint32_t size = (uint32_t)bb, to = (uint32_t)lane * (uint32_t)bb;
-  int64_t off = 0;
-  if (half) {
-    const int h = s.at.t & 1;
-    size = lane < 2 ? kKv8Keys * D : kKv8Keys;
-    off = lane < 2 ? (lane * bs + h * kKv8Keys) * D : 2 * bs * D + (lane - 2) * bs + h * kKv8Keys;
-    to = lane < 2 ? lane * kKv8Keys * D : 2 * kKv8Keys * D + (lane - 2) * kKv8Keys;
-  }
-  uint32_t total;
-  if (half) {
-    total = __ballot_sync(0xffffffffu, go) ? kKv8Keys * (2 * D + 2) : 0;
-  } else {
-    total = __popc(__ballot_sync(0xffffffffu, go)) * (uint32_t)bb;
-  }
-  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, total);
-  __syncwarp();
+  const bool half = a.block_size > kKv8Keys;
+  const int id = __shfl_sync(0xffffffffu, s.id, (s.k + (half ? 0 : lane)) & 31);
+  const bool go = lane < s.n && id >= 0;
+  const uint32_t went = __popc(__ballot_sync(0xffffffffu, go));
+  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, half ? (went ? kKv8Keys * (2 * D + 2) : 0) : went * s.size);
   if (go) {
-    const int64_t src = ((int64_t)id * a.h_kv + s.at.g) * bb + off;
-    if (idx_ok(src + size - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status) &&
-        smem_ok(dst + to, size, ring.lo, ring.hi, ring.status))
-      bulk_load(dst + to, a.cache + src, size, bar, policy);
+    const uint32_t off = s.off + (s.at.t & 1) * s.step;
+    const uint8_t* src = s.head + (uint64_t)(uint32_t)id * s.stride + off;
+    if (idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status) &&
+        smem_ok(dst + s.to, s.size, ring.lo, ring.hi, ring.status))
+      bulk_load(dst + s.to, src, s.size, bar, policy);
   }
   // ---- move on
-  if (++s.at.t < s.t_end) return;
+  if (++s.at.t < s.t_end) {
+    s.k += half ? 1 - (s.at.t & 1) : s.n;
+    return;
+  }
   s.at = s.ahead;
   s.id = s.id_next;
-  if (s.at.b >= a.N) return;
-  s.j0 = kv8_first_block(a, s.at.t);
-  s.t_end = kv8_window_end(a, s.at);
-  int end;
-  kv8_ahead(s, a, prefix);
-  s.id_next = kv8_window(a, s.ahead, lens, lane, &end);
+  if (s.at.b < a.N) kv8_enter<D>(s, a, prefix, lens, lane);
 }
 
 // RG warps share a ring (RG = 2: more than 32 rows), each with NT n-tiles of 8 query rows.
@@ -315,32 +328,41 @@ __device__ __forceinline__ void kv8_setup(Kv8Warp<D, NT, RG>& w, const Kv8Params
   w.turn = (uint32_t)((lane >> 4) ^ (D == 128 ? (lane & 7) : ((lane >> 1) & 3))) << 4;
 }
 
-template <int D, int NT, int RG, bool BF16>
-__device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int len, int rg,
-                                          int lane) {
-  using W = Kv8Warp<D, NT, RG>;
-  constexpr int KD = W::KD;
+// A piece begins: its queries are loaded, ...
+template <int D, int NT, int RG>
+__device__ __forceinline__ void kv8_load_q(uint2 (&raw)[NT][D / 16], const Kv8Params& a, int b, int g, int rg, int lane) {
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = (rg * NT + nt) * 8 + r, t = row / a.G;
     const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D + 4 * c;
     const bool ok = row < a.rows && idx_ok(at + D - 1 - 4 * c, (int64_t)a.N * a.T_q * a.h_q * D, a.status);
-    uint2 raw[KD];
 #pragma unroll
-    for (int j = 0; j < KD; ++j)
-      raw[j] = ok ? __ldg(reinterpret_cast<const uint2*>(a.q + at + 16 * j)) : make_uint2(0u, 0u);
+    for (int j = 0; j < D / 16; ++j)
+      raw[nt][j] = ok ? __ldg(reinterpret_cast<const uint2*>(a.q + at + 16 * j)) : make_uint2(0u, 0u);
+  }
+}
+
+// ... brought into the MMA's form, and the state is emptied.
+template <int D, int NT, int RG, bool BF16>
+__device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT][D / 16], const Kv8Params& a, int len,
+                                          int lane) {
+  using W = Kv8Warp<D, NT, RG>;
+  constexpr int KD = W::KD;
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     float qs = fabsf(a.scale_log2);
     if (a.scale_log2 < 0.f) {    // the factor of a row is kept >= 0, so that the largest y is the largest logit
 #pragma unroll
-      for (int j = 0; j < KD; ++j) raw[j] = make_uint2(raw[j].x ^ 0x80008000u, raw[j].y ^ 0x80008000u);
+      for (int j = 0; j < KD; ++j) raw[nt][j] = make_uint2(raw[nt][j].x ^ 0x80008000u, raw[nt][j].y ^ 0x80008000u);
     }
     if constexpr (BF16) {
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < KD; ++j)
-        top = max(max(top, max(raw[j].x & 0x7fffu, (raw[j].x >> 16) & 0x7fffu)),
-                  max(raw[j].y & 0x7fffu, (raw[j].y >> 16) & 0x7fffu));
+        top = max(max(top, max(raw[nt][j].x & 0x7fffu, (raw[nt][j].x >> 16) & 0x7fffu)),
+                  max(raw[nt][j].y & 0x7fffu, (raw[nt][j].y >> 16) & 0x7fffu));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const uint32_t e = max(top >> 7, 15u);                    // the row's largest value becomes 2^14 .. 2^15
@@ -349,23 +371,23 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, const Kv8Params
 #pragma unroll
       for (int j = 0; j < KD; ++j) {
         float x[4];
-        unpack4<true>(raw[j], x);
-        raw[j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
+        unpack4<true>(raw[nt][j], x);
+        raw[nt][j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
       }
     }
     qs = fmaxf(qs, 1.2e-38f);      // not 0: a hidden key's y is -inf
     if constexpr (W::Q_SMEM) {
 #pragma unroll
       for (int j = 0; j < KD; ++j)
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(w.q_at + ((j * NT + nt) * 32 + lane) * 8), "r"(raw[j].x),
-                     "r"(raw[j].y)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(w.q_at + ((j * NT + nt) * 32 + lane) * 8), "r"(raw[nt][j].x),
+                     "r"(raw[nt][j].y)
                      : "memory");
       if (c == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.q_at + KD * NT * 256 + (nt * 8 + r) * 4), "f"(qs) : "memory");
     } else {
 #pragma unroll
       for (int j = 0; j < KD; ++j) {
-        w.qf[nt][j][0] = raw[j].x;
-        w.qf[nt][j][1] = raw[j].y;
+        w.qf[nt][j][0] = raw[nt][j].x;
+        w.qf[nt][j][1] = raw[nt][j].y;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) w.qs[nt][i] = __shfl_sync(0xffffffffu, qs, (2 * c + i) * 4);
@@ -667,11 +689,15 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
   const uint64_t policy = ptx::policy_evict_first();
   const int eb = min(a.block_size, kKv8Keys);
+  uint2 raw[NT][D / 16];
+  kv8_load_q<D, NT, RG>(raw, a, at.b, at.g, rg, lane);
   Kv8Stream str;
   int issued = 0;
   if (rg == 0) {
     str.at = at;
-    kv8_start(str, a, prefix, lens, lane);
+    kv8_stream_setup<D>(str, a, lane);
+    str.id = kv8_window(a, at, lens, lane);
+    kv8_enter<D>(str, a, prefix, lens, lane);
     for (; issued < n && issued < STAGES; ++issued)
       if (!(issued == 1 && wk == a.stall))
         kv8_copy<D>(str, a, prefix, lens, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
@@ -679,7 +705,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   Kv8Warp<D, NT, RG> w;
   kv8_setup(w, a, ptx::smem_u32(smem + C::Q_OFF) + warp * C::QUERIES, lane);
   int len = lens[at.b];
-  kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, rg, lane);
+  kv8_begin<D, NT, RG, BF16>(w, raw, a, len, lane);
   bool fresh = at.t == 0;        // this piece begins with its unit
   int64_t slot = 2 * wk;         // where it goes when it is not the whole unit
   int i = 0, stage = 0, phase = 0;
@@ -709,7 +735,8 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
       if (i + 1 < n) {
         kv8_next_unit(at, prefix, a.N, a.h_kv);
         len = lens[at.b];
-        kv8_begin<D, NT, RG, BF16>(w, a, at.b, at.g, len, rg, lane);
+        kv8_load_q<D, NT, RG>(raw, a, at.b, at.g, rg, lane);
+        kv8_begin<D, NT, RG, BF16>(w, raw, a, len, lane);
         fresh = true;
         slot = 2 * wk + 1;
       }

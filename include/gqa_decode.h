@@ -360,10 +360,12 @@ size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, i
  * G * T_q <= 64.  seq_lens count the T_q new tokens when they are in the cache (gqa_append before this
  * call).  gqa_options used: bf16, causal (token t sees the keys j <= len - T_q + t; a token that sees no
  * key gets O = 0, as does a sequence of length 0), timeout_us, test_stall_cta (the index of one worker --
- * a group of warps that streams one share of all keys -- whose second tile is never loaded).  Sequences are
- * split over the workers evenly, whatever their lengths; results do not depend on other calls and are the
- * same every time.  Block ids outside [0, num_blocks) are not loaded, lengths outside
- * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check. */
+ * one or two warps that stream an equal share of all keys -- whose second tile is never loaded).  The keys of
+ * all sequences are split evenly over the workers, whatever the lengths, and joined in the order of the
+ * keys: the same call gives the same bits.  Block ids outside [0, num_blocks) are not loaded, lengths outside
+ * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check.
+ * Only the first 256 bytes of the workspace have to be zero; the rest is left dirty, so that a workspace of this
+ * call needs gqa_workspace_init before it serves gqa_decode or gqa_decode_paged. */
 gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
                           uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
                           int h_q, int h_kv, int d_head, float scale, void* workspace, size_t ws_bytes, void* stream,

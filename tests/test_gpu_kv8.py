@@ -663,6 +663,27 @@ def test_other_streams(gqa):
         assert torch.equal(o, want[i]) if i is not None else torch.equal(o[0], wk) and torch.equal(o[1], wv)
 
 
+def test_other_calls_on_the_same_stream_keep_their_counters(gqa):
+    """gqa_decode folding in its last CTA counts arrivals in its workspace: a gqa_decode_kv8 in between
+    must not leave anything there."""
+    D, hq, hk, bs = 128, 8, 2, 16
+    lens = [3000, 50, 700]
+    cache, tab = make_cache(lens, D, hk, bs, 140)
+    q = torch.randn(3, hq * D, generator=gen(60)).half().cuda()
+    k = torch.randn(3, 4000, hk * D, generator=gen(61)).half().cuda()
+    v = torch.randn(3, 4000, hk * D, generator=gen(62)).half().cuda()
+    want = gqa.gqa_decode(q[:, None], k, v, hq, hk, n_splits=9, merge_mode=1)
+    x = dev(cache), dev(tab), dev(np.array(lens, np.int32))
+    first = gqa.gqa_decode_kv8(q, *x, hq, hk)
+    for _ in range(3):
+        assert torch.equal(gqa.gqa_decode_kv8(q, *x, hq, hk), first)
+        o = gqa.gqa_decode(q[:, None], k, v, hq, hk, n_splits=9, merge_mode=2)
+        torch.testing.assert_close(o, want, rtol=2e-3, atol=1e-4)
+    o = gqa.gqa_decode_kv8(q, *x, hq, hk)
+    assert torch.equal(o, first)
+    check_decode(o, cache, tab, lens, q.cpu(), hq, hk, D, D ** -0.5, bs, False, "f16", "after gqa_decode")
+
+
 def test_binding_checks(gqa):
     D, hq, hk, bs = 64, 8, 2, 16
     cache = gqa.gqa_kv8_cache(4, bs, hk, D)
