@@ -411,7 +411,10 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT
 
 // One tile of `valid` keys (key0 the first), `st` its place in the ring; masked: some key of it is hidden
 // from some row.
-template <int D, int NT, int RG>
+// FINE: the weights as two f16 numbers, the rounded one and what was lost.  A weight rounded to f16 is off by as much as
+// an f16 output is (64 sequences, against 64 bits: 2.9e-4 instead of 2.1e-4, 1.41 times), so f16 calls take the
+// second product; the rounding of a bf16 output is eight times as coarse.
+template <int D, int NT, int RG, bool FINE>
 __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, uint32_t st, int eb, int valid,
                                          int key0, bool masked, int rg, int lane, const Win& ring) {
   using W = Kv8Warp<D, NT, RG>;
@@ -560,7 +563,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
         for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f[nt][i & 1];
   }
   // ---- weights, and P as the B operand
-  uint32_t pf[2][NT][2];
+  uint32_t pf[2][NT][2], pl[2][NT][2];
   Two off[NT], sum[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -576,7 +579,12 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       const Two p = two(ptx::ex2(x.x), ptx::ex2(x.y));
       sum[nt] = add2(sum[nt], p);
       const float2 pv = split(mul2(p, two(v, v)));
-      pf[o >> 1][nt][o & 1] = kv8_transpose(ptx::pack_half2(pv.x, pv.y));
+      const uint32_t h = ptx::pack_half2(pv.x, pv.y);
+      pf[o >> 1][nt][o & 1] = kv8_transpose(h);
+      if constexpr (FINE) {
+        const float2 f = half2_floats(h);
+        pl[o >> 1][nt][o & 1] = kv8_transpose(ptx::pack_half2(pv.x - f.x, pv.y - f.y));
+      }
     }
   }
 #pragma unroll
@@ -599,6 +607,10 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       for (int nt = 0; nt < NT; ++nt) {
         kv8_mma(w.acc[j][nt], f[0], pf[p][nt]);
         kv8_mma(w.acc[j + 1][nt], f[1], pf[p][nt]);
+        if constexpr (FINE) {
+          kv8_mma(w.acc[j][nt], f[0], pl[p][nt]);
+          kv8_mma(w.acc[j + 1][nt], f[1], pl[p][nt]);
+        }
       }
     }
 }
@@ -714,7 +726,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
     const int key0 = at.t * kKv8Keys;
     const int valid = min(len - key0, kKv8Keys);
     const int sees = a.causal ? len - a.T_q : len - 1;       // the fewest keys that a row sees
-    kv8_tile<D, NT, RG>(w, a, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, rg, lane, ring);
+    kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, rg, lane, ring);
     __syncwarp();
     if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
     if (rg == 0 && i + STAGES < n) {
