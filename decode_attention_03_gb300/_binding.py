@@ -1,4 +1,5 @@
-"""ctypes binding of ``libgqa_decode.so`` -- argument marshalling only.
+"""Binding of ``libgqa_decode.so`` -- argument marshalling only, by ctypes, and by the extension module
+``_calls`` for the calls of every layer.
 
 Every function here has the name of the C entry point it calls (see
 ``include/gqa_decode.h``), takes torch tensors where the C call takes device
@@ -12,7 +13,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 import threading
 from typing import Optional, Tuple
 
@@ -458,31 +458,14 @@ def gqa_decode_noalloc_check(stream=None) -> int:
 
 
 # ---------------------------------------------------------------- filling a cache; the 8-bit cache
-# These calls are made for every layer of every decode step, where the host's time is what counts: their
-# checks are written out, arguments travel as packed bytes, and device and stream come from torch's own
-# C-level queries where it has them.
-_HALVES = (torch.float16, torch.bfloat16)
-_F32, _U8, _I32, _I64 = torch.float32, torch.uint8, torch.int32, torch.int64
-_BF16 = torch.bfloat16
+# These calls are made for every layer of every decode step, where the host's time is what counts: their checks
+# are in ``_calls`` (csrc/torch_calls.cpp), which reads the tensors' fields directly.
+from . import _calls  # noqa: E402
+
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
-_pack_args = struct.Struct("@15q11if").pack        # gqa_append_args
-_pack_opts = struct.Struct("@2iI5i").pack            # gqa_options
-assert struct.calcsize("@15q11if") == ctypes.sizeof(gqa_append_args)
-assert struct.calcsize("@2iI5i") == ctypes.sizeof(gqa_options)
-
-
-def _packed(name):
-    """The entry point once more, taking its structs as packed bytes."""
-    fn = lib[name]
-    args, fn.restype = _SIGS[name]
-    fn.argtypes = [ctypes.c_char_p if a in (_opt, ctypes.POINTER(gqa_append_args)) else a for a in args]
-    return fn
-
-
-_append_c, _decode_kv8_c, _read_c = _packed("gqa_append"), _packed("gqa_decode_kv8"), _packed("gqa_kv8_read")
 
 
 def _in_stream(stream):
@@ -490,37 +473,24 @@ def _in_stream(stream):
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
-def _status_workspace(dev: int, raw: int) -> torch.Tensor:
+def _place(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """Device of a tensor and its current stream."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev, _raw_stream(dev)
+
+
+def _status_workspace(t: torch.Tensor, name: str) -> torch.Tensor:
     """A workspace for calls that need its status word alone: the cached one of the stream, which graphs may
     share with other calls (the kernels only set bits in it)."""
-    t = _ws_cache.get((dev, raw))
-    if t is not None:
-        return t
+    key = _place(t, name)
+    ws = _ws_cache.get(key)
+    if ws is not None:
+        return ws
     if _capturing():
-        return torch.zeros(256, dtype=_U8, device=torch.device("cuda", dev))
-    return workspace(256, torch.device("cuda", dev))
-
-
-def _elsewhere(dev: int) -> ValueError:
-    return ValueError(f"the tensors are on device {dev}, the current device is {_device()}")
-
-
-def _bad(name: str, what: str) -> ValueError:
-    return ValueError(f"{name} must be {what}, on the device of the others")
-
-
-def _index(t: torch.Tensor, name: str, dtype, dev: int, shape) -> int:
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        raise _bad(name, f"a contiguous {dtype} tensor of shape {shape}")
-    return t.data_ptr()
-
-
-def _kv8_block_size(cache: torch.Tensor, h_kv: Optional[int], d_head: int, dev: int) -> int:
-    shape = cache.shape
-    if cache.dtype is not _U8 or len(shape) != 3 or cache.get_device() != dev or not cache.is_contiguous() or \
-            (h_kv is not None and shape[1] != h_kv) or shape[2] % (2 * d_head + 2):
-        raise _bad("an 8-bit cache", "a contiguous uint8 tensor (num_blocks, h_kv, block_size * (2 * d_head + 2))")
-    return shape[2] // (2 * d_head + 2)
+        return torch.zeros(256, dtype=torch.uint8, device=t.device)
+    return workspace(256, t.device)
 
 
 def gqa_kv8_block_bytes(block_size: int, d_head: int) -> int:
@@ -533,7 +503,7 @@ def gqa_kv8_cache(num_blocks: int, block_size: int, h_kv: int, d_head: int, devi
     n = gqa_kv8_block_bytes(block_size, d_head)
     if n == 0:
         raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_kv8_cache")
-    return torch.zeros(num_blocks, h_kv, n, dtype=_U8, device="cuda" if device is None else device)
+    return torch.zeros(num_blocks, h_kv, n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q: int, h_kv: int, slots: torch.Tensor,
@@ -557,82 +527,24 @@ def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q:
             return gqa_append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions=positions, cos_sin=cos_sin,
                               interleaved=interleaved, q_weight=q_weight, k_weight=k_weight, eps=eps, q_out=q_out,
                               workspace_tensor=workspace_tensor)
-    dt, dev, shape = k.dtype, k.get_device(), k.shape
-    if dt not in _HALVES or dev < 0 or len(shape) != 2 or h_kv < 1 or shape[1] % h_kv:
-        raise ValueError("k must be a float16 or bfloat16 CUDA tensor (tokens, h_kv*d_head)")
-    if dev != _device():
-        raise _elsewhere(dev)
-    T, kc = shape
-    D = kc // h_kv
-    if v.dtype is not dt or v.get_device() != dev or v.shape != shape:
-        raise _bad("v", "like k")
-    ks, kd = k.stride()
-    vs, vd = v.stride()
-    if kc > 1 and (kd != 1 or vd != 1):
-        raise _bad("k and v", "tensors with dense rows")
-    qp = op = qs = os_ = 0
-    if q is None:
-        h_q, q_out = 0, None
-    else:
-        qc = h_q * D
-        if q.dtype is not dt or q.get_device() != dev or q.shape != (T, qc):
-            raise _bad("q", f"a {dt} tensor (tokens, h_q*d_head)")
-        if q_out is None:
-            q_out = torch.empty_like(q)          # rows of a fused projection come out dense
-        elif q_out.dtype is not dt or q_out.get_device() != dev or q_out.shape != (T, qc):
-            raise _bad("q_out", "like q")
-        qs, qd = q.stride()
-        os_, od = q_out.stride()
-        if qc > 1 and (qd != 1 or od != 1):
-            raise _bad("q and q_out", "tensors with dense rows")
-        if T < 2:
-            qs = os_ = qc
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    if T < 2:
-        ks = vs = kc
-    cp = pp = rot = rows = 0
-    if cos_sin is not None:
-        if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or cos_sin.get_device() != dev or \
-                not cos_sin.is_contiguous() or positions is None:
-            raise _bad("cos_sin", "a contiguous float32 tensor (max_position, rot_dim) that comes with positions")
-        rows, rot = cos_sin.shape
-        cp, pp = cos_sin.data_ptr(), _index(positions, "positions", _I32, dev, (T,))
-    if k_cache.dtype is _U8:
-        if v_cache is not None:
-            raise ValueError("an 8-bit cache holds K and V: pass no v_cache")
-        layout, bs, vcp = GQA_CACHE_KV8, _kv8_block_size(k_cache, h_kv, D, dev), 0
-    else:
-        cs = k_cache.shape
-        if len(cs) == 5:
-            layout, bs = GQA_CACHE_VLLM, cs[3]
-            want, v_want = (cs[0], h_kv, D // 8, bs, 8), (cs[0], h_kv, D, bs)
-        else:
-            layout, bs = GQA_CACHE_ROWS, cs[1] if len(cs) == 3 else 0
-            want = v_want = (cs[0], bs, kc)
-        if v_cache is None:
-            raise ValueError("a 16-bit cache needs k_cache and v_cache")
-        _index(k_cache, "k_cache", dt, dev, want)
-        vcp = _index(v_cache, "v_cache", dt, dev, v_want)
-    raw = _raw_stream(dev)
-    ws = _status_workspace(dev, raw) if workspace_tensor is None else workspace_tensor
-    st = _append_c(_pack_args(
-        qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs, os_,
-        0 if q_weight is None else _index(q_weight, "q_weight", dt, dev, (D,)),
-        0 if k_weight is None else _index(k_weight, "k_weight", dt, dev, (D,)), cp, pp,
-        _index(slots, "slots", _I64, dev, (T,)), k_cache.data_ptr(), vcp, T, h_q, h_kv, D, rows, rot,
-        1 if interleaved else 0, k_cache.shape[0], bs, layout, 1 if dt is _BF16 else 0, eps),
-        ws.data_ptr(), ws.numel(), raw)
-    if st:
-        raise GQAError(st, "gqa_append")
-    return q_out
-
-
-_kv8_ws_bytes = {}      # (device, shape) -> bytes
+    ws = _status_workspace(k, "k") if workspace_tensor is None else workspace_tensor
+    r = _calls.append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions, cos_sin, interleaved, q_weight, k_weight,
+                      eps, q_out, ws)
+    if r.__class__ is int:
+        raise GQAError(r, "gqa_append")
+    return r
 
 
 def gqa_decode_kv8_workspace_size(num_seqs: int, T_q: int, h_q: int, h_kv: int, d_head: int) -> int:
     """Workspace bytes of gqa_decode_kv8 on the current device (0: invalid shape)."""
     return lib.gqa_decode_kv8_workspace_size(num_seqs, T_q, h_q, h_kv, d_head)
+
+
+def _kv8_workspace_bytes(q: torch.Tensor, h_q: int, h_kv: int) -> int:
+    n = gqa_decode_kv8_workspace_size(1, q.shape[1] if q.dim() == 3 else 1, h_q, h_kv, q.shape[-1] // h_q if h_q else 0)
+    if n == 0:
+        raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_decode_kv8_workspace_size")
+    return n
 
 
 def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, h_q: int,
@@ -641,54 +553,33 @@ def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Ten
                    timeout_us: int = 0, test_stall_cta: int = -1) -> torch.Tensor:
     """Decode attention over the 8-bit cache: q (N, h_q*D) or (N, T_q, h_q*D) float16 or bfloat16 (the output too),
     cache (num_blocks, h_kv, block_size*(2D+2)) uint8, tables (N, max_blocks) and lens (N) int32; G*T_q <= 64.
-    ``causal``: query token t sees keys j <= len - T_q + t only."""
+    ``causal``: query token t sees keys j <= len - T_q + t only.
+
+    Without ``workspace_tensor`` the stream's cached workspace of this call is used; a call that is being captured into
+    a graph gets one of its own, so that graphs may be replayed side by side."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_decode_kv8(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal=causal, out=out,
                                   workspace_tensor=workspace_tensor, timeout_us=timeout_us,
                                   test_stall_cta=test_stall_cta)
-    dt, dev, shape = q.dtype, q.get_device(), q.shape
-    dim = len(shape)
-    if dt not in _HALVES or dev < 0 or dim not in (2, 3) or not q.is_contiguous() or h_q < 1 or shape[-1] % h_q:
-        raise ValueError("q must be a contiguous float16 or bfloat16 CUDA tensor (N, h_q*d_head) or (N, T_q, h_q*d_head)")
-    if dev != _device():
-        raise _elsewhere(dev)
-    N, T_q = shape[0], shape[1] if dim == 3 else 1
-    D = shape[-1] // h_q
-    bs = _kv8_block_size(cache, h_kv, D, dev)
-    if block_tables.dim() != 2:
-        raise _bad("block_tables", "(N, max_blocks)")
-    mb = block_tables.shape[1]
-    tp = _index(block_tables, "block_tables", _I32, dev, (N, mb))
-    lp = _index(seq_lens, "seq_lens", _I32, dev, (N,))
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.dtype is not dt or out.get_device() != dev or out.shape != shape or not out.is_contiguous():
-        raise _bad("out", "like q")
-    raw = _raw_stream(dev)
     ws = workspace_tensor
     if ws is None:
-        key = (dev, T_q, h_q, h_kv, D)
-        n = _kv8_ws_bytes.get(key)
-        if n is None:
-            n = lib.gqa_decode_kv8_workspace_size(N, T_q, h_q, h_kv, D)
-            if n == 0:
-                raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_decode_kv8_workspace_size")
-            _kv8_ws_bytes[key] = n
+        dev, raw = _place(q, "q")
         if _capturing():
-            # a graph keeps its own partials: another graph or call may run beside its replays
-            ws = torch.empty(n, dtype=_U8, device=q.device)
+            ws = torch.empty(_kv8_workspace_bytes(q, h_q, h_kv), dtype=torch.uint8, device=q.device)
             ws[:256].zero_()
         else:
             ws = _ws_cache.get((dev, raw, "kv8"))
-            if ws is None or ws.numel() < n:
-                ws = workspace(n, q.device, use="kv8")
-    st = _decode_kv8_c(q.data_ptr(), cache.data_ptr(), tp, lp, out.data_ptr(), N, T_q, mb, cache.shape[0], bs, h_q,
-                       h_kv, D, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), raw,
-                       _pack_opts(0, 0, timeout_us, test_stall_cta, 0, 1 if causal else 0, 1 if dt is _BF16 else 0, 0))
-    if st:
-        raise GQAError(st, "gqa_decode_kv8")
-    return out
+            if ws is None:
+                ws = workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")
+    r = _calls.decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, timeout_us, test_stall_cta)
+    if r.__class__ is int:
+        if r == GQA_ERR_WORKSPACE and workspace_tensor is None and ws.numel() < _kv8_workspace_bytes(q, h_q, h_kv):
+            workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")       # the cached one grows
+            return gqa_decode_kv8(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal=causal, out=out,
+                                  timeout_us=timeout_us, test_stall_cta=test_stall_cta)
+        raise GQAError(r, "gqa_decode_kv8")
+    return r
 
 
 def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, d_head: int,
@@ -704,39 +595,17 @@ def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torc
         with _in_stream(stream):
             return gqa_kv8_read(cache, block_tables, seq_lens, d_head, out_len, begins=begins, dtype=dtype,
                                 k_out=k_out, v_out=v_out, workspace_tensor=workspace_tensor)
-    dev = cache.get_device()
-    if dev < 0:
-        raise ValueError("cache must be a CUDA tensor")
-    if dev != _device():
-        raise _elsewhere(dev)
-    bs = _kv8_block_size(cache, None, d_head, dev)
-    if block_tables.dim() != 2:
-        raise _bad("block_tables", "(N, max_blocks)")
-    N, mb = block_tables.shape
-    nb, h_kv, _ = cache.shape
-    tp = _index(block_tables, "block_tables", _I32, dev, (N, mb))
-    lp = _index(seq_lens, "seq_lens", _I32, dev, (N,))
-    bp = 0 if begins is None else _index(begins, "begins", _I32, dev, (N,))
-    given = k_out if k_out is not None else v_out
-    if given is None:
+    ws = _status_workspace(cache, "cache") if workspace_tensor is None else workspace_tensor
+    if k_out is None and v_out is None:
         if out_len is None:
             raise ValueError("pass out_len, or k_out / v_out")
-        dt = torch.float16 if dtype is None else dtype
-        k_out, v_out = (torch.zeros(N, out_len, h_kv * d_head, dtype=dt, device=cache.device) for _ in range(2))
-    else:
-        dt = given.dtype
-        if given.dim() != 3 or (out_len is not None and out_len != given.shape[1]) or (dtype is not None and dtype != dt):
-            raise ValueError("k_out and v_out must be (N, out_len, h_kv*d_head) of dtype")
-        out_len = given.shape[1]
-    if dt not in _HALVES:
-        raise ValueError("k_out and v_out must be float16 or bfloat16")
-    shape = (N, out_len, h_kv * d_head)
-    kp = 0 if k_out is None else _index(k_out, "k_out", dt, dev, shape)
-    vp = 0 if v_out is None else _index(v_out, "v_out", dt, dev, shape)
-    raw = _raw_stream(dev)
-    ws = _status_workspace(dev, raw) if workspace_tensor is None else workspace_tensor
-    st = _read_c(cache.data_ptr(), tp, lp, bp, kp, vp, N, out_len, mb, nb, bs, h_kv, d_head, ws.data_ptr(), ws.numel(),
-                 raw, _pack_opts(0, 0, 0, -1, 0, 0, 1 if dt is _BF16 else 0, 0))
-    if st:
-        raise GQAError(st, "gqa_kv8_read")
+        shape = (block_tables.shape[0], out_len, cache.shape[1] * d_head)
+        k_out, v_out = (torch.zeros(shape, dtype=dtype or torch.float16, device=cache.device) for _ in range(2))
+    elif out_len is not None or dtype is not None:
+        for t in (k_out, v_out):
+            if t is not None and (out_len not in (None, t.shape[1]) or dtype not in (None, t.dtype)):
+                raise ValueError("k_out and v_out must be (N, out_len, h_kv*d_head) of dtype")
+    r = _calls.read(cache, block_tables, seq_lens, d_head, begins, k_out, v_out, ws)
+    if r:
+        raise GQAError(r, "gqa_kv8_read")
     return k_out, v_out

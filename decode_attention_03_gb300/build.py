@@ -6,6 +6,9 @@ runtime linked statically (the library needs only the NVIDIA driver at run
 time).  A rebuild happens only when a source or header is newer than the
 library.
 
+``csrc/torch_calls.cpp``, the calls that take torch tensors directly, becomes the extension module
+``_calls.so`` beside it (g++, against the installed torch's headers), linked to the library.
+
 ``build(checked=True)`` makes the checked library instead,
 ``libgqa_decode_checked.so`` (objects in ``_build_checked/``): the same sources
 compiled with ``GQA_BOUNDS_CHECK=1``, under which the kernels range-check every
@@ -17,8 +20,10 @@ from __future__ import annotations
 import glob
 import os
 import shutil
+import importlib.util
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -28,6 +33,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgqa_decode.so")
 BUILD_CHECKED = os.path.join(ROOT, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libgqa_decode_checked.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
           "-I" + os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
@@ -56,12 +63,60 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _run(cmd, verbose: bool, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed")
+
+
+def calls_up_to_date() -> bool:
+    """The extension module is newer than its sources and was built against the torch that is installed."""
+    if not os.path.exists(CALLS):
+        return False
+    t = os.path.getmtime(CALLS)
+    deps = [CALLS_SRC, os.path.join(ROOT, "include", "gqa_decode.h"), os.path.abspath(__file__),
+            importlib.util.find_spec("torch").origin]
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def _compile_calls(verbose: bool) -> str:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(BUILD, "torch_calls.o")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+           sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC"] + [f for p in inc for f in ("-isystem", p)] + ["-c", CALLS_SRC, "-o", obj],
+         verbose, "g++ for torch_calls.cpp")
+    return obj
+
+
+def _link_calls(obj: str, verbose: bool) -> None:
+    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = CALLS + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+          "-L" + PKG, "-lgqa_decode", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], verbose, "link of _calls.so")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checked: bool = False) -> str:
     """Compile and link the library (``checked``: the bounds-checked one); returns its path."""
     lib, bdir = (LIB_CHECKED, BUILD_CHECKED) if checked else (LIB, BUILD)
+    os.makedirs(bdir, exist_ok=True)
+    if checked:
+        return _build_library(lib, bdir, force, verbose, ptxas_verbose, checked)
+    with ThreadPoolExecutor(1) as ex:
+        calls = ex.submit(_compile_calls, verbose) if force or not calls_up_to_date() else None
+        _build_library(lib, bdir, force, verbose, ptxas_verbose, checked)
+        if calls is not None:
+            _link_calls(calls.result(), verbose)
+    return lib
+
+
+def _build_library(lib: str, bdir: str, force: bool, verbose: bool, ptxas_verbose: bool, checked: bool) -> str:
     if not force and up_to_date(lib):
         return lib
-    os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     if checked:
