@@ -190,16 +190,14 @@ gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
 }
 
 struct Kv8Layout {
-  size_t prefix, splits, m, l, o, total;
+  size_t splits, m, l, o, total;
 };
 
-// workspace: the status header, the tiles before each sequence of a launch, the unit each worker cuts and two
-// partials for each worker
+// workspace: the status header, the units that are cut and two partials for each worker
 Kv8Layout kv8_layout(int workers, int rows, int D) {
   Kv8Layout L;
   const size_t n = 2 * (size_t)workers * rows;
-  L.prefix = kHeaderBytes;
-  L.splits = L.prefix + align256((kKv8Seqs + 1) * sizeof(int64_t));
+  L.splits = kHeaderBytes;
   L.m = L.splits + align256((size_t)workers * sizeof(int4));
   L.l = L.m + align256(n * 4);
   L.o = L.l + align256(n * 4);
@@ -253,7 +251,6 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   Kv8Params p = {};
   p.cache = static_cast<const uint8_t*>(cache);
   p.status = reinterpret_cast<uint32_t*>(wsb);
-  p.prefix = reinterpret_cast<int64_t*>(wsb + lay.prefix);
   p.splits = reinterpret_cast<int4*>(wsb + lay.splits);
   p.ws_m = reinterpret_cast<float*>(wsb + lay.m);
   p.ws_l = reinterpret_cast<float*>(wsb + lay.l);
@@ -279,6 +276,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     p.workers = (int)grid * kv8_groups(cls);
     // pieces of a unit: about workers / units + 1 when the sequences are alike
     const bool many = p.workers / units >= 7, cut = seq_tiles > 1;   // (a unit of one tile is never cut)
+    p.sliced = many ? 1 : 0;
     const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, cut, many, st)
                                           : kv8_decode<64, false>(p, cls, grid, cut, many, st))
                                   : (bf16 ? kv8_decode<128, true>(p, cls, grid, cut, many, st)

@@ -40,11 +40,11 @@ struct Kv8Params {
   const uint8_t* cache;
   const int32_t *block_tables, *seq_lens;
   uint32_t* status;
-  int64_t* prefix;       // [N + 1] tiles (of one head) before each sequence
-  int4* splits;          // [workers] the unit that a worker's range cuts first: sequence, head, pieces, first slot
+  int4* splits;          // the units that are cut, for the merge (Kv8Pieces); [workers], sliced: [units]
   float *ws_m, *ws_l;    // [2 * workers][rows]   m in log2 units
   float* ws_o;           // [2 * workers][rows][D]
   int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, bs_log, causal, workers, stall;
+  int sliced;            // few units of many pieces: splits has one entry for each unit
   float scale_log2;
   uint64_t timeout_ns;
 };
@@ -132,7 +132,7 @@ __device__ __forceinline__ Kv8Place kv8_find(int64_t f, const int64_t* prefix, i
   return p;
 }
 
-// Tiles before each sequence of the launch, in shared memory (and, by CTA 0, in the workspace for the merge).
+// Tiles (of one head) before each sequence of the launch, in shared memory.
 __device__ __forceinline__ void kv8_prefix(const Kv8Params& a, int64_t* prefix, int* lens, int64_t* sums) {
   constexpr int PER = kKv8Seqs / kKv8Threads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,12 +164,8 @@ __device__ __forceinline__ void kv8_prefix(const Kv8Params& a, int64_t* prefix, 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int b = threadIdx.x * PER + i;
-    if (b < a.N) {
-      prefix[b + 1] = before + v[i];
-      if (blockIdx.x == 0) a.prefix[b + 1] = before + v[i];
-    }
+    if (b < a.N) prefix[b + 1] = before + v[i];
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[0] = 0;
   __syncthreads();
 }
 
@@ -178,9 +174,12 @@ template <int D>
 __device__ __forceinline__ void kv8_empty_rows(const Kv8Params& a, const int* lens) {
   const int64_t words = (int64_t)a.T_q * a.h_q * D / 8;
   for (int b = blockIdx.x; b < a.N; b += gridDim.x)
-    if (lens[b] == 0)
+    if (lens[b] == 0) {
       for (int64_t i = threadIdx.x; i < words; i += kKv8Threads)
         reinterpret_cast<uint4*>(a.o)[b * words + i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.sliced)
+        for (int g = threadIdx.x; g < a.h_kv; g += kKv8Threads) a.splits[b * a.h_kv + g] = make_int4(0, 0, 0, 0);
+    }
 }
 
 // The copying side of a worker: block ids of the next tiles, one for each lane (-1: no block, or a bad id), and what
@@ -685,7 +684,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   const int64_t wk = (int64_t)grp * gridDim.x + blockIdx.x;
   const int64_t f0 = wk * share, f1 = f0 + share < total ? f0 + share : total;
   if (f0 >= f1) {
-    if (lane == 0 && rg == 0) a.splits[wk] = make_int4(0, 0, 0, 0);
+    if (lane == 0 && rg == 0 && !a.sliced) a.splits[wk] = make_int4(0, 0, 0, 0);
     return;
   }
   const int n = (int)(f1 - f0);
@@ -695,7 +694,9 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
     // before (its slot 0 if the unit begins with that range, else 1), this one and as many more as the unit has tiles
     const bool first_cut = at.t > 0 && at.t <= share;
     const int64_t pieces = first_cut ? 1 + (at.tiles - at.t + share - 1) / share : 0;
-    a.splits[wk] = make_int4(at.b, at.g, (int)pieces, at.t < share ? 1 : 0);
+    const int first = 2 * ((int)wk - 1) + (at.t < share ? 1 : 0);
+    if (!a.sliced) a.splits[wk] = make_int4((int)pieces, first, at.b, at.g);
+    else if (first_cut) a.splits[at.b * a.h_kv + at.g] = make_int4((int)pieces, first, at.b, at.g);
   }
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
@@ -743,6 +744,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
     }
     if (++at.t == at.tiles || i + 1 == n) {
       const bool whole = fresh && at.t == at.tiles;
+      if (whole && a.sliced && lane == 0 && rg == 0) a.splits[at.b * a.h_kv + at.g] = make_int4(0, 0, 0, 0);
       kv8_end<D, NT, RG, BF16>(w, a, at.b, at.g, whole ? -1 : slot, rg, lane);
       if (i + 1 < n) {
         kv8_next_unit(at, prefix, a.N, a.h_kv);
@@ -766,38 +768,20 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   }
 }
 
-// The pieces of a unit that more than one worker streamed: n >= 2 of them, of workers w0, w0 + 1, ...; the first
-// one's slot is 2 w0 + first.
+// The pieces of a unit that more than one worker streamed: n of them (0: the unit is not cut), of neighbouring workers;
+// the first one's slot is `first`, the others have the first slots of the workers after it.
 struct Kv8Pieces {
-  int64_t w0;
   int n, first, row;
 };
 
-// of output row r, for few units: from the lengths
-__device__ __forceinline__ Kv8Pieces kv8_pieces(const Kv8Params& a, int64_t r) {
-  Kv8Pieces p = {0, 0, 0, 0};
-  const int h = (int)(r % a.h_q);
-  const int64_t bt = r / a.h_q;
-  const int t = (int)(bt % a.T_q), b = (int)(bt / a.T_q), g = h / a.G;
-  p.row = t * a.G + h - g * a.G;
-  const int64_t p0 = __ldcg(a.prefix + b), tiles = __ldcg(a.prefix + b + 1) - p0;
-  const int64_t total = __ldcg(a.prefix + a.N) * a.h_kv;
-  if (tiles == 0) return p;
-  const int64_t share = (total + a.workers - 1) / a.workers, start = p0 * a.h_kv + g * tiles;
-  p.w0 = start / share;
-  p.n = (int)((start + tiles - 1) / share - p.w0) + 1;
-  p.first = start > p.w0 * share ? 1 : 0;
-  return p;
-}
-
 __device__ __forceinline__ int64_t kv8_slot_row(const Kv8Params& a, const Kv8Pieces& p, int s) {
-  return (2 * (p.w0 + s) + (s == 0 ? p.first : 0)) * a.rows + p.row;
+  return (int64_t)(s == 0 ? p.first : (p.first & ~1) + 2 * s) * a.rows + p.row;
 }
 
 // Folds the pieces of every unit that more than one worker streamed, in the order of its keys.
 // SLICED = false, for batches whose units have a few pieces each: a warp for each worker's range (whose first cut
 // unit the worker has noted: no search, no division) and row, all D columns.
-// SLICED = true, for few units of many pieces: a CTA for 32 columns of an output row, 8 lanes for each piece.
+// SLICED = true, for few units of many pieces: a CTA for 32 columns of one row of a unit, 8 lanes for each piece.
 template <int D, bool BF16, bool SLICED>
 __global__ void __launch_bounds__(kMergeThreads)
 gqa_kv8_merge_kernel(const Kv8Params a) {
@@ -810,24 +794,23 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
   ptx::grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Kv8Pieces pc;
-  int64_t out;   // element offset of the output row
+  int4 unit;     // pieces, first slot, sequence, head
   int col = lane % LANES * PER;
   if constexpr (SLICED) {
-    const int64_t r = blockIdx.x / (D / 32);
+    const uint32_t r = blockIdx.x / (D / 32), u = r / (uint32_t)a.rows;
     col += (int)(blockIdx.x % (D / 32)) * 32;
-    pc = kv8_pieces(a, r);
-    out = r * D;
+    unit = __ldcg(a.splits + u);
+    pc.row = (int)(r - u * (uint32_t)a.rows);
   } else {
     const uint32_t i = blockIdx.x * WARPS + warp, w = i / (uint32_t)a.rows;
     if (w >= (uint32_t)a.workers) return;
-    const int4 unit = __ldcg(a.splits + w);
-    pc.w0 = (int64_t)w - 1;
-    pc.n = unit.z;
-    pc.first = unit.w;
+    unit = __ldcg(a.splits + w);
     pc.row = (int)(i - w * (uint32_t)a.rows);
-    const int t = pc.row / a.G;
-    out = (((int64_t)unit.x * a.T_q + t) * a.h_q + (int64_t)unit.y * a.G + (pc.row - t * a.G)) * D;
   }
+  pc.n = unit.x;
+  pc.first = unit.y;
+  const int t = pc.row / a.G;
+  const int64_t out = (((int64_t)unit.z * a.T_q + t) * a.h_q + (int64_t)unit.w * a.G + (pc.row - t * a.G)) * D;
   if (pc.n < 2 || !idx_ok(out + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
   float M = -CUDART_INF_F, L = 0.f, acc[PER];
 #pragma unroll
