@@ -274,6 +274,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     const int64_t units = (int64_t)p.N * h_kv;
     const unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
     p.workers = (int)grid * kv8_groups(cls);
+    if (units * seq_tiles / p.workers >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;   // tiles of a worker
     // pieces of a unit: about workers / units + 1 when the sequences are alike
     const bool many = p.workers / units >= 7, cut = seq_tiles > 1;   // (a unit of one tile is never cut)
     p.sliced = many ? 1 : 0;

@@ -648,7 +648,7 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
           *reinterpret_cast<float2*>(a.ws_o + at * D + 16 * j + 2 * r) =
               make_float2(w.acc[j][nt][i] * unit, w.acc[j][nt][2 + i] * unit);
         if (r == 0) {
-          a.ws_m[at] = w.m[nt][i];
+          a.ws_m[at] = l == l ? w.m[nt][i] : 0.f;   // NaN scores move no maximum: not to be taken for an empty piece
           a.ws_l[at] = l;
         }
       }

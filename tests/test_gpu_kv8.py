@@ -344,6 +344,19 @@ def test_read_defaults_and_reports(gqa):
         assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_INVALID_ARG
 
 
+def test_read_into_outputs_on_16_byte_borders(gqa):
+    """Outputs whose addresses are multiples of 16 bytes, but not of 32."""
+    D, hk, bs, n = 128, 3, 16, 50
+    cache, tab = make_cache([n, 20], D, hk, bs, 31)
+    big = torch.full((2, 2 * n * hk * D + 8), 5.0, dtype=torch.float16, device="cuda")
+    k, v = (x[8:].view(2, n, hk * D) for x in big)
+    assert k.data_ptr() % 32 == 16
+    gqa.gqa_kv8_read(dev(cache), dev(tab), dev(np.array([n, 20], np.int32)), D, k_out=k, v_out=v)
+    wk, wv = gqa.gqa_kv8_read(dev(cache), dev(tab), dev(np.array([n, 20], np.int32)), D, n)
+    assert torch.equal(k[0], wk[0]) and torch.equal(v[0], wv[0]) and torch.equal(v[1, :20], wv[1, :20])
+    assert (big[:, :8] == 5.0).all() and (k[1, 20:] == 5.0).all()
+
+
 # ---------------------------------------------------------------- decode
 def check_decode(o, cache, tab, lens, q, hq, hk, D, scale, bs, causal, elem, where):
     ref, a, l, top = ko.decode_kv8(npy(q).reshape(len(lens), -1, hq * D), cache, tab, lens, hq, hk, D, scale, bs, causal)
@@ -441,6 +454,68 @@ def test_decode_one_key_far_away_takes_everything(gqa):
         o = run_decode(gqa, c, tab, [n], q, 4, 1)
         v = torch.from_numpy(ko.get_row(c, int(tab[0, j // bs]) * bs + j % bs, 0, 1, D, bs))
         assert torch.equal(o.view(4, D).cpu(), v.half().expand(4, D)), j
+
+
+def test_f16_outputs_are_as_exact_as_their_rounding(gqa):
+    """With the weights in two f16 numbers the error of an f16 output is its own rounding: relative L2 at most 1.2 of
+    what rounding the oracle's result to f16 gives (weights in one f16 number: about 1.4)."""
+    for D, hq, hk, bs, T in [(128, 32, 8, 16, 1), (64, 8, 2, 16, 1), (128, 16, 1, 32, 2)]:
+        lens = [900, 400, 1300]
+        cache, tab = make_cache(lens, D, hk, bs, 95)
+        q = torch.randn(3, T, hq * D, generator=gen(14)).half()
+        o = run_decode(gqa, cache, tab, lens, q, hq, hk)
+        ref = ko.decode_kv8(npy(q), cache, tab, lens, hq, hk, D, D ** -0.5, bs)[0]
+        own = float((o.double().cpu() - ref).norm() / ref.norm())
+        least = float((ref.half().double() - ref).norm() / ref.norm())
+        assert own <= 1.2 * least, (own, least)
+
+
+def test_not_a_number_stays_in_its_row(gqa):
+    """A NaN query spoils its own row, a NaN value its column for the heads that share it, an infinite query its
+    row; nothing else changes."""
+    D, hq, hk, bs, n = 128, 8, 2, 16, 500
+    cache, tab = make_cache([n], D, hk, bs, 96)
+    q = torch.randn(1, hq * D, generator=gen(15)).half()
+    want = run_decode(gqa, cache, tab, [n], q, hq, hk).view(hq, D)
+    bad = q.clone()
+    bad[0, 3 * D + 5] = math.nan
+    bad[0, 6 * D + 9] = math.inf
+    o = run_decode(gqa, cache, tab, [n], bad, hq, hk).view(hq, D)
+    assert o[[3, 6]].isnan().all()
+    keep = [0, 1, 2, 4, 5, 7]
+    assert torch.equal(o[keep], want[keep])
+    c = cache.copy()
+    j, col = 333, 77
+    c[tab[0, j // bs], 1, ko.row_offsets(j % bs, D, bs, 1)[col]] = 0x7F
+    o = run_decode(gqa, c, tab, [n], q, hq, hk).view(hq, D)
+    assert o[4:, col].isnan().all()
+    o[4:, col] = want[4:, col]
+    assert torch.equal(o, want)
+
+
+def test_one_call_shapes_on_one_workspace(gqa):
+    """The cached workspace grows and serves calls of other shapes, in any order."""
+    cases = []
+    for i, (hq, hk, D, lens) in enumerate([(4, 2, 64, [70]), (64, 1, 128, [900, 33]), (32, 8, 128, [1200] * 5),
+                                           (2, 2, 64, [31] * 30)]):
+        cache, tab = make_cache(lens, D, hk, 16, 150 + i)
+        q = torch.randn(len(lens), hq * D, generator=gen(70 + i)).half()
+        cases.append((cache, tab, lens, q, hq, hk))
+    s = torch.cuda.Stream()
+    want = None
+    for _ in range(2):
+        got = []
+        for cache, tab, lens, q, hq, hk in cases + cases[::-1]:
+            x = q.cuda(), dev(cache), dev(tab), dev(np.array(lens, np.int32))
+            torch.cuda.synchronize()
+            got.append(gqa.gqa_decode_kv8(*x, hq, hk, stream=s))
+            torch.cuda.synchronize()
+        assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(got[:4], got[:3:-1]))
+        want = got
+    for (cache, tab, lens, q, hq, hk), o in zip(cases, want):
+        D = q.shape[1] // hq
+        check_decode(o, cache, tab, lens, q, hq, hk, D, D ** -0.5, 16, False, "f16", f"{hq}")
 
 
 def test_decode_shared_blocks(gqa):
