@@ -61,7 +61,7 @@ cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
   }
   const unsigned per = kAppendThreads / 32;
   const dim3 grid(((unsigned)p.num_tokens + per - 1) / per, (unsigned)sets);
-  return launch_pdl_smem(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, grid, kAppendThreads, 0, st, p);
+  return launch_pdl_smem(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, grid, kAppendThreads, 0, st, 1, p);
 }
 
 template <int D, bool BF16, int CW, bool PAIRS>
@@ -158,8 +158,12 @@ int kv8_groups(int cls) { return cls < 3 ? kKv8Warps : kKv8Warps / 2; }
 
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_prepare() {
-  return cudaFuncSetAttribute(gqa_decode_kv8_kernel<D, NT, RG, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Kv8Cfg<D, NT, RG>::SMEM);
+  constexpr int bytes = Kv8Cfg<D, NT, RG>::SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(gqa_decode_kv8_kernel<D, NT, RG, BF16>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gqa_decode_kv8_short_kernel<D, NT, RG, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              bytes);
 }
 
 template <int D, bool BF16>
@@ -189,6 +193,26 @@ gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
   return GQA_OK;
 }
 
+// Workers for each unit from which the merge gives 32 columns of a row a CTA instead of a whole row a warp.  Measured (us;
+// from 7 / 16 / 32 on): 16 sequences of 250-500 keys, 8 KV heads (9 workers a unit) 15.5 / 12.4 / 12.4, 16 of 1000-2000
+// 20.9 / 18.0 / 18.1; fewer units the same.
+constexpr int kManyPieces = 16;
+
+// CTAs of a unit in the short kernel, a cluster of 1, 2, 4 or 8: the fewest that give each worker one tile, as far as all
+// units' clusters fit on three quarters of the SMs at once (a cluster lies in one GPC).  0: the general kernel, where a
+// worker would have more than kKv8Short tiles, or more than two above what the general kernel, which uses every SM,
+// gives one.  Measured (us, short / general; tiles of a worker in brackets): 8 KV heads of 128: one sequence of 300 keys
+// 7.0 / 8.7 [1, 1], 2000 7.4 / 8.9 [1, 1], 8000 9.9 / 9.9 [4, 2], 16000 13.6 / 11.9 [8, 4]; 4 of 500-1000 7.9 / 10.3 [1, 1];
+// 16 of 1000-2000 13.5 / 18.0 [8, 7]; 2 KV heads of 64: 4096 keys 6.5 / 7.7 [2, 1], 16384 11.1 / 10.5 [8, 1].
+int kv8_short_ctas(int64_t units, int64_t seq_tiles, int sms, int groups) {
+  int ctas = 1;
+  while (ctas < 8 && ctas * groups < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;
+  const int64_t here = (seq_tiles + ctas * groups - 1) / (ctas * groups);
+  const int64_t there = (units * seq_tiles + sms * groups - 1) / (sms * groups);
+  if (units * ctas > sms || here > kKv8Short || here > there + 2) return 0;
+  return ctas;
+}
+
 struct Kv8Layout {
   size_t splits, m, l, o, total;
 };
@@ -207,7 +231,10 @@ Kv8Layout kv8_layout(int workers, int rows, int D) {
 
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_launch(const Kv8Params& p, unsigned grid, cudaStream_t st) {
-  return launch_pdl_smem(gqa_decode_kv8_kernel<D, NT, RG, BF16>, grid, kKv8Threads, Kv8Cfg<D, NT, RG>::SMEM, st, p);
+  constexpr int bytes = Kv8Cfg<D, NT, RG>::SMEM;
+  if (p.ctas > 0)
+    return launch_pdl_smem(gqa_decode_kv8_short_kernel<D, NT, RG, BF16>, grid, kKv8Threads, bytes, st, p.ctas, p);
+  return launch_pdl_smem(gqa_decode_kv8_kernel<D, NT, RG, BF16>, grid, kKv8Threads, bytes, st, 1, p);
 }
 
 template <int D, bool BF16>
@@ -272,11 +299,14 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     p.seq_lens = lens + b0;
     // as many CTAs as there can be tiles, at most one on each SM
     const int64_t units = (int64_t)p.N * h_kv;
-    const unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
+    unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
+    if (units * seq_tiles / ((int64_t)grid * kv8_groups(cls)) >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;   // tiles of a worker
+    // few units that the table bounds to kKv8Short tiles a worker: one launch of clusters
+    p.ctas = kv8_short_ctas(units, seq_tiles, sms, kv8_groups(cls));
+    if (p.ctas > 0) grid = (unsigned)(units * p.ctas);
     p.workers = (int)grid * kv8_groups(cls);
-    if (units * seq_tiles / p.workers >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;   // tiles of a worker
     // pieces of a unit: about workers / units + 1 when the sequences are alike
-    const bool many = p.workers / units >= 7, cut = seq_tiles > 1;   // (a unit of one tile is never cut)
+    const bool many = p.workers / units >= kManyPieces, cut = seq_tiles > 1 && p.ctas == 0;   // (a unit of one tile is never cut)
     p.sliced = many ? 1 : 0;
     const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, cut, many, st)
                                           : kv8_decode<64, false>(p, cls, grid, cut, many, st))
@@ -293,7 +323,7 @@ cudaError_t read_launch(const Kv8ReadParams& p, cudaStream_t st) {
   const int64_t groups = (p.most + ReadCfg<D>::TOKENS - 1) / ReadCfg<D>::TOKENS, per = kReadThreads / 32;
   const int64_t blocks = (groups * p.h_kv + per - 1) / per;
   return launch_pdl_smem(gqa_kv8_read_kernel<D, BF16>, dim3((unsigned)blocks, (unsigned)p.num_seqs), kReadThreads, 0, st,
-                         p);
+                         1, p);
 }
 
 gqa_status read_impl(const void* cache, const int32_t* tables, const int32_t* lens, const int32_t* begins,

@@ -7,6 +7,8 @@
 // time.  A (sequence, head) that lies inside one share is finished by its worker; the others leave partials
 // (m, l, O) that a merge kernel folds in the order of the keys: the same bits every time.
 //
+// Few units that their table bounds to few tiles take another kernel, without a merge: see the short kernel below.
+//
 // A worker streams its tiles through a ring of its own in shared memory: one plain bulk copy for each block
 // (32 keys are 32/block_size of them), K, V and scales together.  No warp waits for another worker's.
 //
@@ -31,6 +33,7 @@ namespace gqa {
 constexpr int kKv8Keys = 32;                   // keys of a tile
 constexpr int kKv8Seqs = 1024;                 // sequences of a launch (the host splits larger batches)
 constexpr int kKv8Warps = 8;
+constexpr int kKv8Short = 8;                   // tiles of a worker of the short kernel: 32 blocks of 8 keys
 constexpr int kKv8Threads = 32 * kKv8Warps;
 constexpr float kKv8Slack = 8.f;               // log2 of the largest weight
 
@@ -45,6 +48,7 @@ struct Kv8Params {
   float* ws_o;           // [2 * workers][rows][D]
   int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, bs_log, causal, workers, stall;
   int sliced;            // few units of many pieces: splits has one entry for each unit
+  int ctas;              // short kernel: CTAs of a unit, one cluster
   float scale_log2;
   uint64_t timeout_ns;
 };
@@ -66,9 +70,11 @@ struct Kv8Cfg {
   // shares are equal (last worker done 22 us after the median instead of 10).
   static constexpr int STAGES = (D == 128 ? 2 : 4) * RG;
   static constexpr int Q_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
-  static constexpr int RING_OFF = (Q_OFF + kKv8Warps * QUERIES + 127) & ~127;
+  static constexpr int ML_OFF = Q_OFF + kKv8Warps * QUERIES;    // m and l of a warp's rows, where a CTA folds its warps'
+  static constexpr int RING_OFF = (ML_OFF + kKv8Warps * 8 * NT * 8 + 127) & ~127;
   static constexpr int SMEM = RING_OFF + GROUPS * STAGES * TILE;
-  static_assert(GROUPS * STAGES <= kKv8Threads && SMEM <= 232448, "ring");
+  static constexpr int AREA = STAGES * TILE / RG;               // a warp's part of the ring: holds its O there
+  static_assert(GROUPS * STAGES <= kKv8Threads && SMEM <= 232448 && AREA >= 8 * NT * D * 4 && AREA % 16 == 0, "ring");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
@@ -229,12 +235,22 @@ __device__ __forceinline__ int kv8_window_end(const Kv8Params& a, const Kv8Place
 }
 
 // this lane's block id of the window that starts at p
-__device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p, const int* lens, int lane) {
-  if (p.b >= a.N) return -1;
+__device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p, int len, int lane) {
   const int j = kv8_first_block(a, p.t) + lane;
-  if (j >= kv8_blocks(a, lens[p.b]) || !idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status))
+  if (j >= kv8_blocks(a, len) || !idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status))
     return -1;
   return __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + j);
+}
+
+template <int D>
+__device__ __forceinline__ void kv8_window_begin(Kv8Stream& s, const Kv8Params& a, int len, int lane) {
+  const int j = kv8_first_block(a, s.at.t) + lane;
+  if (j < kv8_blocks(a, len) && (s.id < 0 || s.id >= a.num_blocks)) {
+    atomicOr(a.status, kDevBadInput);
+    s.id = -1;
+  }
+  s.k = 0;
+  s.head = a.cache + (int64_t)s.at.g * kv8_block_bytes(a.block_size, D);
 }
 
 // Enters the window at s.at, whose ids are in s.id: reports bad ids, finds where the next window begins and starts
@@ -242,13 +258,7 @@ __device__ __forceinline__ int kv8_window(const Kv8Params& a, const Kv8Place& p,
 template <int D>
 __device__ __forceinline__ void kv8_enter(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
                                           int lane) {
-  const int j = kv8_first_block(a, s.at.t) + lane;
-  if (j < kv8_blocks(a, lens[s.at.b]) && (s.id < 0 || s.id >= a.num_blocks)) {
-    atomicOr(a.status, kDevBadInput);
-    s.id = -1;
-  }
-  s.k = 0;
-  s.head = a.cache + (int64_t)s.at.g * kv8_block_bytes(a.block_size, D);
+  kv8_window_begin<D>(s, a, lens[s.at.b], lane);
   s.t_end = kv8_window_end(a, s.at);
   s.ahead = s.at;
   s.ahead.t = s.t_end;
@@ -262,13 +272,14 @@ __device__ __forceinline__ void kv8_enter(Kv8Stream& s, const Kv8Params& a, cons
           asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(
               a.q + (((int64_t)s.ahead.b * a.T_q + t) * a.h_q + (int64_t)s.ahead.g * a.G) * D) + i));
   }
-  s.id_next = kv8_window(a, s.ahead, lens, lane);
+  s.id_next = s.ahead.b < a.N ? kv8_window(a, s.ahead, lens[s.ahead.b], lane) : -1;
 }
 
-// Copies the stream's next tile to `dst` and moves on.  Every lane of the warp calls this.
+// Copies the stream's next tile to `dst`; on to the next tile of the window (true: the window ends).  Every lane of the
+// warp calls this.
 template <int D>
-__device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
-                                         uint32_t dst, uint32_t bar, uint64_t policy, int lane, const Win& ring) {
+__device__ __forceinline__ bool kv8_issue(Kv8Stream& s, const Kv8Params& a, uint32_t dst, uint32_t bar, uint64_t policy,
+                                          int lane, const Win& ring) {
   const bool half = a.block_size > kKv8Keys;
   const int id = __shfl_sync(0xffffffffu, s.id, (s.k + (half ? 0 : lane)) & 31);
   const bool go = lane < s.n && id >= 0;
@@ -281,11 +292,16 @@ __device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const
         smem_ok(dst + s.to, s.size, ring.lo, ring.hi, ring.status))
       bulk_load(dst + s.to, src, s.size, bar, policy);
   }
-  // ---- move on
-  if (++s.at.t < s.t_end) {
-    s.k += half ? 1 - (s.at.t & 1) : s.n;
-    return;
-  }
+  if (++s.at.t == s.t_end) return true;
+  s.k += half ? 1 - (s.at.t & 1) : s.n;
+  return false;
+}
+
+// the same, and on to the next window
+template <int D>
+__device__ __forceinline__ void kv8_copy(Kv8Stream& s, const Kv8Params& a, const int64_t* prefix, const int* lens,
+                                         uint32_t dst, uint32_t bar, uint64_t policy, int lane, const Win& ring) {
+  if (!kv8_issue<D>(s, a, dst, bar, policy, lane, ring)) return;
   s.at = s.ahead;
   s.id = s.id_next;
   if (s.at.b < a.N) kv8_enter<D>(s, a, prefix, lens, lane);
@@ -709,7 +725,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
   if (rg == 0) {
     str.at = at;
     kv8_stream_setup<D>(str, a, lane);
-    str.id = kv8_window(a, at, lens, lane);
+    str.id = kv8_window(a, at, lens[at.b], lane);
     kv8_enter<D>(str, a, prefix, lens, lane);
     for (; issued < n && issued < STAGES; ++issued)
       if (!(issued == 1 && wk == a.stall))
@@ -766,6 +782,220 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
       for (int k = i; k < issued; ++k)
         ptx::mbar_wait_bounded(full + k % STAGES * 8, k / STAGES & 1, a.timeout_ns, nullptr);
   }
+}
+
+// Short kernel: the warps of a CTA leave their states in shared memory (their parts of the drained ring).
+template <int D, int NT, int RG>
+__device__ __forceinline__ void kv8_leave(Kv8Warp<D, NT, RG>& w, float2* ml, float* o, int lane) {
+  constexpr int KD = Kv8Warp<D, NT, RG>::KD;
+  const int r = lane >> 2, c = lane & 3;
+  const float unit = kv8_scale((uint32_t)w.e);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float l = w.l[nt][i];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int row = nt * 8 + 2 * c + i;
+      if (r == 0) ml[row] = make_float2(w.m[nt][i], l);
+#pragma unroll
+      for (int j = 0; j < KD; ++j)
+        *reinterpret_cast<float2*>(o + row * D + 16 * j + 2 * r) =
+            make_float2(w.acc[j][nt][i] * unit, w.acc[j][nt][2 + i] * unit);
+    }
+}
+
+// One row's four columns of n <= 8 states, folded in the order of the keys: state i has its m and l at ml(i), its O at o(i).
+template <typename ML, typename O>
+__device__ __forceinline__ void kv8_fold(int n, ML ml, O o, float& m, float& l, float4& acc) {
+  float2 s[8];
+  float4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] = i < n ? ml(i) : make_float2(-CUDART_INF_F, 0.f);
+    v[i] = i < n ? o(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  m = -CUDART_INF_F;
+  l = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, s[i].x);
+  const float base = m == -CUDART_INF_F ? 0.f : m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = ptx::ex2(s[i].x - base);
+    l += f * s[i].y;      // (NaN scores move no maximum, but their sum is NaN)
+    acc.x += f * v[i].x;
+    acc.y += f * v[i].y;
+    acc.z += f * v[i].z;
+    acc.w += f * v[i].w;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void kv8_store4(const Kv8Params& a, int b, int g, int row, int d, int D, float l, float4 v) {
+  const int t = row / a.G;
+  const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D + d;
+  if (!idx_ok(at + 3, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
+  const float f = l > 0.f ? 1.f / l : 0.f;
+  Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at, v.x * f, v.y * f);
+  Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at + 2, v.z * f, v.w * f);
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
+// Decode of few, short units in one launch: a cluster of a.ctas CTAs for each (sequence, head), its tiles cut evenly over
+// their workers (at most kKv8Short tiles each, so that one window of block ids serves a worker).  There is nothing to
+// search: a CTA needs one length.  The warps of a CTA fold their states in shared memory, the CTAs of the cluster
+// theirs through distributed shared memory, each a part of the columns, both in the order of the keys.
+// Bound by latency: one sequence of 4096 keys, 8 + 2 heads of 64, 5.8-6.6 us (1.1 MB, 0.2 us of HBM) against 7.6 of the general
+// kernel and its merge.
+template <int D, int NT, int RG, bool BF16>
+__global__ void __launch_bounds__(kKv8Threads, 1)
+gqa_decode_kv8_short_kernel(const Kv8Params a) {
+  using C = Kv8Cfg<D, NT, RG>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);   // [0] abort
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp / RG, rg = warp % RG;
+  const int unit = blockIdx.x / a.ctas, c = blockIdx.x - unit * a.ctas, b = unit / a.h_kv, g = unit - b * a.h_kv;
+  const uint32_t full = ptx::smem_u32(smem + C::BAR_OFF) + grp * STAGES * 16, empty = full + STAGES * 8;
+  if (threadIdx.x < C::GROUPS * STAGES) {
+    const uint32_t f = ptx::smem_u32(smem + C::BAR_OFF) + threadIdx.x / STAGES * STAGES * 16 + threadIdx.x % STAGES * 8;
+    ptx::mbar_init(f, 1);
+    ptx::mbar_init(f + STAGES * 8, RG);
+  }
+  if (threadIdx.x == 0) flags[0] = 0;
+  ptx::fence_mbar_init();
+  __syncthreads();
+  ptx::grid_dependency_wait();
+  if (threadIdx.x == 0) ptx::grid_launch_dependents();
+  int len = __ldg(a.seq_lens + b);
+  const int64_t cap = (int64_t)a.max_blocks * a.block_size;
+  if (len < 0 || len > cap) {
+    if (threadIdx.x == 0) atomicOr(a.status, kDevBadInput);
+    len = len < 0 ? 0 : (int)cap;
+  }
+  const int tiles = (int)(((int64_t)len + kKv8Keys - 1) / kKv8Keys);
+  const int per = max((tiles + a.ctas * C::GROUPS - 1) / (a.ctas * C::GROUPS), 1);
+  const int busy_ctas = (tiles + per * C::GROUPS - 1) / (per * C::GROUPS);
+  // workers of this CTA that have tiles
+  const int busy = max(min((tiles - c * C::GROUPS * per + per - 1) / per, C::GROUPS), 0);
+  const int wk = c * C::GROUPS + grp, t0 = wk * per, n = grp < busy ? min(per, tiles - t0) : 0;
+  const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
+  const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
+  const uint64_t policy = ptx::policy_evict_first();
+  const int eb = min(a.block_size, kKv8Keys);
+  const bool stalled = a.stall >= 0 && a.stall == (int)blockIdx.x * C::GROUPS + grp;
+  float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
+  bool good = true;
+  if (n > 0) {
+    Kv8Stream str;
+    int issued = 0;
+    if (rg == 0) {
+      str.at = {b, g, t0, tiles};
+      kv8_stream_setup<D>(str, a, lane);
+      str.id = kv8_window(a, str.at, len, lane);
+    }
+    uint2 raw[NT][D / 16];
+    kv8_load_q<D, NT, RG>(raw, a, b, g, rg, lane);
+    if (rg == 0) {
+      kv8_window_begin<D>(str, a, len, lane);
+      str.t_end = t0 + n;
+      for (; issued < n && issued < STAGES; ++issued)
+        if (!(stalled && issued == 1))
+          kv8_issue<D>(str, a, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
+    }
+    Kv8Warp<D, NT, RG> w;
+    kv8_setup(w, a, ptx::smem_u32(smem + C::Q_OFF) + warp * C::QUERIES, lane);
+    kv8_begin<D, NT, RG, BF16>(w, raw, a, len, lane);
+    const int sees = a.causal ? len - a.T_q : len - 1;       // the fewest keys that a row sees
+    int i = 0, stage = 0, phase = 0;
+    for (; i < n; ++i) {
+      good = ptx::mbar_wait_bounded(full + stage * 8, phase, a.timeout_ns, flags);
+      if (!good) break;
+      const int key0 = (t0 + i) * kKv8Keys;
+      kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, min(len - key0, kKv8Keys), key0,
+                                 kKv8Keys - 1 > sees - key0, rg, lane, ring);
+      __syncwarp();
+      if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
+      if (rg == 0 && i + STAGES < n) {
+        if (RG > 1) {
+          good = ptx::mbar_wait_bounded(empty + stage * 8, phase, a.timeout_ns, flags);
+          if (!good) break;
+        }
+        kv8_issue<D>(str, a, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
+        ++issued;
+      }
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!good) {
+      // a wait gave up: tell the others and wait (bounded) for this worker's copies in flight
+      if (lane == 0) {
+        atomicOr(a.status, kDevTimeout);
+        flags[0] = 1;
+      }
+      if (rg == 0)
+        for (int k = i; k < issued; ++k)
+          ptx::mbar_wait_bounded(full + k % STAGES * 8, k / STAGES & 1, a.timeout_ns, nullptr);
+    }
+    if (RG > 1) __syncwarp();
+    if (RG > 1) ptx::named_bar_sync(1 + grp, 32 * RG);   // the other warp of the ring has read its last tile
+    if (good) kv8_leave<D, NT, RG>(w, ml + warp * 8 * NT, reinterpret_cast<float*>(smem + C::RING_OFF + warp * C::AREA), lane);
+  }
+  __syncthreads();
+  // ---- the CTA's state: m and l where the general kernel has its prefix sums, O in the first worker's areas (an item is
+  // read and written by one thread); the output itself when this CTA has the whole unit
+  float2* cta_ml = reinterpret_cast<float2*>(smem + C::PREFIX_OFF);
+  uint8_t* areas = smem + C::RING_OFF;
+  const bool alone = a.ctas == 1 || tiles == 0;
+  if (flags[0] == 0)
+    for (int i = threadIdx.x; i < a.rows * (D / 4); i += kKv8Threads) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4, part = row / (8 * NT), wrow = row % (8 * NT);
+      float m, l;
+      float4 v;
+      kv8_fold(busy, [&](int k) { return ml[(k * RG + part) * 8 * NT + wrow]; },
+               [&](int k) {
+                 return *reinterpret_cast<const float4*>(areas + (k * RG + part) * C::AREA + (wrow * D + d) * 4);
+               }, m, l, v);
+      if (alone) {
+        if (c == 0) kv8_store4<BF16>(a, b, g, row, d, D, l, v);
+        continue;
+      }
+      *reinterpret_cast<float4*>(areas + part * C::AREA + (wrow * D + d) * 4) = v;
+      if (d == 0) cta_ml[row] = make_float2(m, l);
+    }
+  if (a.ctas == 1) return;
+  // ---- the cluster's fold (every CTA comes here, also one that gave up or has no tiles)
+  ptx::cluster_sync();
+  if (!alone) {
+    const uint32_t ml_at = ptx::smem_u32(cta_ml), o_at = ptx::smem_u32(areas);
+    for (int i = c * kKv8Threads + threadIdx.x; i < a.rows * (D / 4); i += a.ctas * kKv8Threads) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4, part = row / (8 * NT), wrow = row % (8 * NT);
+      float m, l;
+      float4 v;
+      kv8_fold(busy_ctas, [&](int k) { return ld_cluster_v2(ptx::mapa(ml_at + row * 8, k)); },
+               [&](int k) { return ld_cluster_v4(ptx::mapa(o_at + part * C::AREA + (wrow * D + d) * 4, k)); }, m, l, v);
+      kv8_store4<BF16>(a, b, g, row, d, D, l, v);
+    }
+  }
+  ptx::cluster_sync();       // no CTA leaves while another reads its shared memory
 }
 
 // The pieces of a unit that more than one worker streamed: n of them (0: the unit is not cut), of neighbouring workers;

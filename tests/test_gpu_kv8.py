@@ -571,6 +571,147 @@ def test_decode_timeout_is_reported_not_hung(gqa, hq, worker):
     check_decode(o[:2], cache, tab[:2], lens[:2], q[:2], hq, hk, D, D ** -0.5, bs, False, "f16", "after a timeout")
 
 
+# ---------------------------------------------------------------- short units: one launch of clusters
+# The table's width decides: the short form leaves the workspace behind its header alone, the other one notes its cut
+# units there.
+SHORT = [  # D, hq, hk, T, bs, sequences, blocks of the table -> CTAs of a unit, tiles of a worker
+    (128, 16, 8, 1, 32, 16, 64),     # 1, 8
+    (64, 16, 8, 1, 64, 16, 32),      # 1, 8
+    (128, 8, 8, 1, 32, 18, 8),       # 1, 1
+    (128, 32, 4, 1, 16, 10, 32),     # 2, 1
+    (64, 60, 5, 1, 8, 4, 125),       # 4, 1
+    (64, 8, 2, 1, 16, 1, 256),       # 8, 2
+    (128, 8, 1, 4, 8, 5, 520),       # 8, 3, 32 rows
+    (128, 16, 4, 12, 16, 8, 80),     # 2, 5, two warps on a ring of four
+    (64, 80, 2, 1, 32, 12, 72),      # 4, 5: two warps on a ring of eight
+    (64, 64, 1, 1, 8, 3, 21),        # 2, 1: the last CTA has part of its workers
+]
+
+
+def short_case(D, hq, hk, T, bs, N, blocks, seed):
+    full = blocks * bs
+    lens = ([full, 0, 1, full - 1, 33, full // 2 + 5, 64, full - 33, 32, full // 3] * 2)[:N]
+    cache, tab = make_cache(lens, D, hk, bs, seed)
+    tab = np.ascontiguousarray(np.pad(tab, ((0, 0), (0, blocks)))[:, :blocks])
+    return cache, tab, lens, torch.randn(N, T, hq * D, generator=gen(seed)).half()
+
+
+def wide(tab, bs, keys=20000):
+    """The same table, with room for more keys than the short form takes."""
+    return np.ascontiguousarray(np.pad(tab, ((0, 0), (0, keys // bs - tab.shape[1]))))
+
+
+def marked(gqa, N, T, hq, hk, D):
+    ws = torch.full((gqa.gqa_decode_kv8_workspace_size(N, T, hq, hk, D),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    return ws
+
+
+def untouched(ws):
+    return bool((ws[256:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D,hq,hk,T,bs,N,blocks", SHORT)
+def test_decode_of_short_units_in_one_launch(gqa, D, hq, hk, T, bs, N, blocks, causal):
+    cache, tab, lens, q = short_case(D, hq, hk, T, bs, N, blocks, 160 + hq + T)
+    for t, short in ((tab, True), (wide(tab, bs), False)):
+        ws = marked(gqa, N, T, hq, hk, D)
+        o = run_decode(gqa, cache, t, lens, q, hq, hk, causal=causal, workspace_tensor=ws)
+        assert untouched(ws) == short
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+        check_decode(o, cache, t, lens, q, hq, hk, D, D ** -0.5, bs, causal, "f16", f"short {short}")
+        assert torch.equal(o, run_decode(gqa, cache, t, lens, q, hq, hk, causal=causal, workspace_tensor=ws))
+
+
+@pytest.mark.parametrize("D,hq,hk,T,bs,N,blocks,worker", [(128, 16, 8, 1, 32, 16, 64, 3), (128, 16, 4, 12, 16, 8, 80, 1),
+                                                          (64, 8, 2, 1, 16, 1, 256, 9)])
+def test_timeout_of_short_units(gqa, D, hq, hk, T, bs, N, blocks, worker):
+    """A worker whose second tile never comes: alone in its CTA, with two warps on a ring, in a cluster."""
+    cache, tab, lens, q = short_case(D, hq, hk, T, bs, N, blocks, 170)
+    ws = marked(gqa, N, T, hq, hk, D)
+    run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws, timeout_us=20000, test_stall_cta=worker)
+    assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_TIMEOUT
+    o = run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws)
+    assert untouched(ws) and gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+    check_decode(o, cache, tab, lens, q, hq, hk, D, D ** -0.5, bs, False, "f16", "after a timeout")
+
+
+@pytest.mark.parametrize("short", [True, False])
+def test_both_forms_keep_not_a_number_in_its_row_and_report(gqa, short):
+    D, hq, hk, bs = 128, 8, 2, 16
+    lens = [700, 300]
+    cache, tab = make_cache(lens, D, hk, bs, 97)
+    tab = tab if short else wide(tab, bs)
+    q = torch.randn(2, hq * D, generator=gen(16)).half()
+    ws = marked(gqa, 2, 1, hq, hk, D)
+    want = run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws)
+    assert untouched(ws) == short
+    bad = q.clone()
+    bad[0, 3 * D + 5] = math.nan
+    bad[1, 6 * D + 9] = math.inf
+    c = cache.copy()
+    j, col = 650, 77
+    c[tab[0, j // bs], 1, ko.row_offsets(j % bs, D, bs, 1)[col]] = 0x7F
+    o = run_decode(gqa, c, tab, lens, bad, hq, hk).view(2, hq, D)
+    assert o[0, 3].isnan().all() and o[1, 6].isnan().all() and o[0, 4:, col].isnan().all()
+    w = want.view(2, hq, D).clone()
+    w[0, 3], w[1, 6], w[0, 4:, col] = o[0, 3], o[1, 6], o[0, 4:, col]
+    assert torch.equal(o.nan_to_num(9.0), w.nan_to_num(9.0))
+    for at, what in (((1, 2), cache.shape[0]), ((1, 3), -1)):
+        t = tab.copy()
+        t[at] = what
+        o = run_decode(gqa, cache, t, lens, q, hq, hk, workspace_tensor=ws)
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_INVALID_ARG
+        assert torch.equal(o[0], want[0])
+    for n in (10 ** 6, -3):
+        o = run_decode(gqa, cache, tab, [700, n] if n < 0 else [n, 300], q, hq, hk, workspace_tensor=ws)
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_INVALID_ARG
+        i = 0 if n < 0 else 1
+        check_decode(o[i:i + 1], cache, tab[i:i + 1], lens[i:i + 1], q[i:i + 1], hq, hk, D, D ** -0.5, bs, False, "f16",
+                     f"length {n}")
+        assert n > 0 or (o[1] == 0).all()
+
+
+def test_short_units_replayed_with_other_lengths(gqa):
+    """A captured call of clusters follows the lengths, ids and queries that its tensors hold at the replay."""
+    D, hq, hk, T, bs, N, blocks = SHORT[5]
+    cache, tab, _, q = short_case(*SHORT[5], 180)
+    x = [q.cuda(), dev(cache), dev(tab), dev(np.array([blocks * bs], np.int32))]
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    out = torch.empty_like(x[0])
+    with torch.cuda.stream(s):
+        gqa.gqa_decode_kv8(*x, hq, hk, out=out)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        gqa.gqa_decode_kv8(*x, hq, hk, out=out)
+    for n in (blocks * bs, 0, 1, 777, 4000):
+        x[0].copy_(torch.randn(q.shape, generator=gen(n)).half())
+        x[3].fill_(n)
+        out.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_decode(out, cache, tab, [n], x[0].cpu(), hq, hk, D, D ** -0.5, bs, False, "f16", f"{n} keys")
+
+
+def test_bounds_checked_build_of_both_forms(gqa):
+    from decode_attention_03_gb300 import build
+    lib = gqa.open_library(build.build(checked=True))
+    raw = torch.cuda.current_stream().cuda_stream
+    for i, (D, hq, hk, T, bs, N, blocks) in enumerate(SHORT):
+        cache, tab, lens, q = short_case(D, hq, hk, T, bs, N, blocks, 190 + i)
+        for t, short in ((tab, True), (wide(tab, bs), False)):
+            ws = marked(gqa, N, T, hq, hk, D)
+            x = [q.cuda(), dev(cache), dev(t), dev(np.array(lens, np.int32))]
+            o = torch.full_like(x[0], math.nan)
+            assert lib.gqa_decode_kv8(*(y.data_ptr() for y in x), o.data_ptr(), N, T, t.shape[1], cache.shape[0], bs, hq,
+                                      hk, D, D ** -0.5, ws.data_ptr(), ws.numel(), raw, None) == 0
+            assert untouched(ws) == short
+            assert lib.gqa_workspace_check(ws.data_ptr(), raw) == 0
+            check_decode(o, cache, t, lens, q, hq, hk, D, D ** -0.5, bs, False, "f16", f"{SHORT[i]} {short}")
+
+
 def test_offsets_past_32_bits(gqa):
     """Blocks behind the first 4 GiB of a cache, written, attended to and read back."""
     D, hk, bs, hq = 128, 8, 64, 32
