@@ -46,8 +46,8 @@ gqa_status device_locked(Kv8Device** out) {
 // ---------------------------------------------------------------- append
 // Heads of a warp, in groups of HPW: as many as four where the tokens then still fill the GPU's resident warps,
 // so that a token's cosines, sines and weights are loaded once for them; else one, the shortest chain.
-// Measured (us, groups 1 / 2 / 4 / 8): 16384 tokens, 64 + 8 + 8 heads of 128: 173.7 / 125.9 / 120.1 / 125.7;
-// 64 tokens, 32 + 8 + 8 heads, with the read-back of what was stored: 4.5 / 4.8 / 5.6 / 6.8.
+// Measured (us, groups 1 / 2 / 4): 16384 tokens, 64 + 8 + 8 heads of 128: 117.0 / 105.6 / 105.4; 8192 tokens, 32 + 8 + 8
+// heads into the 8-bit cache, with a read-back: 61.9 / 58.1 / 57.2; but 64 tokens with theirs, before the rule 4.5 / 4.8 / 5.6.
 template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
 cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
   constexpr int HPW = 32 / (D / (2 * CW));
@@ -60,7 +60,11 @@ cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
     if (p.iters == 1 || (int64_t)p.num_tokens * sets >= (int64_t)sms * 4 * (kAppendThreads / 32)) break;
   }
   const unsigned per = kAppendThreads / 32;
-  const dim3 grid(((unsigned)p.num_tokens + per - 1) / per, (unsigned)sets);
+  // as many tokens of a warp as leave two rounds of CTAs.  Measured (us, at least 1 / 2 / 3 / 4 rounds): 8192 tokens of
+  // 32 + 8 + 8 heads of 128 with the read-back 58.8 / 57.2 / 57.2 / 60.7; of 8 + 2 + 2 heads of 64 10.1 / 9.8 / 11.4 / 11.3.
+  const int64_t round = (int64_t)sms * kAppendCtas * per;
+  for (p.run = 1; p.run < kAppendRun && (int64_t)p.num_tokens * sets >= 4 * p.run * round;) p.run *= 2;
+  const dim3 grid(((unsigned)p.num_tokens + per * p.run - 1) / (per * p.run), (unsigned)sets);
   return launch_pdl_smem(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, grid, kAppendThreads, 0, st, 1, p);
 }
 

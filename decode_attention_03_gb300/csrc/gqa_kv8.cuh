@@ -14,7 +14,9 @@
 namespace gqa {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 4;    // on an SM
 constexpr int kAppendIters = 4;   // groups of heads of a warp at most
+constexpr int kAppendRun = 4;     // tokens of a warp at most
 constexpr int kReadThreads = 256;
 
 __host__ __device__ constexpr int kv8_block_bytes(int block_size, int D) { return block_size * (2 * D + 2); }
@@ -109,7 +111,7 @@ struct AppendParams {
   const int64_t* slots;
   void *k_cache, *v_cache;
   uint32_t* status;
-  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, bs_log, q_sets, k_sets, iters;
+  int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, bs_log, q_sets, k_sets, iters, run;
   float eps;
 };
 
@@ -141,15 +143,13 @@ __device__ __forceinline__ void copy_chunk(Chunk<CW>* to, const uint16_t* from) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
 }
 
-// of N groups of copies, groups 0 .. i are there
-template <int N>
-__device__ __forceinline__ void wait_copies(int i) {
-  static_assert(N == 4, "groups");
-  switch (i) {
-    case 0: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+// all groups of copies but the last n - 1 are there
+__device__ __forceinline__ void wait_copies(int n) {
+  switch (n) {
+    case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
     case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
   }
 }
 
@@ -173,19 +173,19 @@ __device__ __forceinline__ Chunk<CW> pack_chunk(const float* x) {
   return c;
 }
 
-// n consecutive floats, 4 n bytes aligned to 8
+// n consecutive floats of shared memory, aligned to 8 n bytes or 16
 template <int n>
-__device__ __forceinline__ void load_floats(float* x, const float* p) {
+__device__ __forceinline__ void shared_floats(float* x, const float* p) {
   if constexpr (n % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < n; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
       x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < n; i += 2) {
-      const float2 v = __ldg(reinterpret_cast<const float2*>(p + i));
+      const float2 v = *reinterpret_cast<const float2*>(p + i);
       x[i] = v.x; x[i + 1] = v.y;
     }
   }
@@ -194,174 +194,196 @@ __device__ __forceinline__ void load_floats(float* x, const float* p) {
 // A head's D elements lie on D/(2 CW) lanes, each with two chunks of CW: elements CW s.. and rot/2 + CW s.. for
 // the lanes s < rot/(2 CW) that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
 // thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes
-// heads of one kind (queries, keys or values) of one token: 32/(D/(2 CW)) at a time, up to a.iters times, all
-// of them copied to the threads' own places in shared memory at the start; cosines, sines and norm weights stay in registers over its heads.  Bound by its bytes, the
+// heads of one kind (queries, keys or values): 32/(D/(2 CW)) at a time, up to a.iters times for each of a.run tokens.
+// Heads are copied to the threads' own places in shared memory a token ahead, a token's cosines and sines with
+// its first group, so that the next token is on its way while this one is worked on.  Bound by its bytes, the
 // heads read and written once, when there are many tokens; the sums of squares and maxima go through log2 of
 // the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
-// Four CTAs an SM (64 registers, a few spilled): 16384 tokens of 64 + 8 + 8 heads of 128 took 120.1 us with four,
-// 133.2 with three (76 registers), 176.5 with two; 146 with CW = 4, whose lanes hold half as much and shuffle more.
+// 16384 tokens of 64 + 8 + 8 heads of 128 take 105.3 us (6.45 TB/s, 0.95 of a copy's rate); 110.5 with one token a warp,
+// 117.9 with five CTAs an SM (48 registers) instead of four (64).
 template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
-__global__ void __launch_bounds__(kAppendThreads, 4)
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
 gqa_append_kernel(const AppendParams a) {
-  constexpr int LPH = D / (2 * CW), HPW = 32 / LPH;
+  constexpr int LPH = D / (2 * CW), HPW = 32 / LPH, WARPS = kAppendThreads / 32;
+  __shared__ __align__(16) Chunk<CW> stage[kAppendIters][2][kAppendThreads];   // a thread's own places
+  __shared__ __align__(16) float turn_rows[WARPS][2][D];                       // a warp's: cosines and sines of two tokens
+  __shared__ __align__(16) uint16_t weights[WARPS][D];
   ptx::grid_dependency_wait();
-  const int lane = threadIdx.x & 31, sub = lane % LPH;
-  // a CTA has one set of heads of kAppendThreads / 32 tokens
-  const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPH;
+  // a CTA has one set of heads of WARPS * a.run tokens, a warp every WARPS-th of them
+  int64_t t = (int64_t)blockIdx.x * (WARPS * a.run) + warp;
   if (t >= a.num_tokens) return;
+  int left = min(a.run, (a.num_tokens - 1 - (int)t) / WARPS + 1);   // tokens of this warp
   int set = blockIdx.y;
   const int kind = set < a.q_sets ? 0 : (set < a.q_sets + a.k_sets ? 1 : 2);
   set -= kind == 0 ? 0 : (kind == 1 ? a.q_sets : a.q_sets + a.k_sets);
   const int heads = kind == 0 ? a.h_q : a.h_kv;
-  int h = set * (a.iters * HPW) + lane / LPH;
+  const int h0 = set * (a.iters * HPW) + lane / LPH;
+  const int iters = min(a.iters, (heads - set * (a.iters * HPW) + HPW - 1) / HPW);   // groups of this warp
   const int rot = a.cos_sin != nullptr ? a.rot_dim : 0;
   const bool turns = 2 * CW * sub < rot;
   int off[2];
   off[0] = turns ? CW * sub : rot + CW * (sub - rot / (2 * CW));
   off[1] = off[0] + (turns ? rot / 2 : (D - rot) / 2);
+  const int64_t stride = kind == 0 ? a.q_stride : (kind == 1 ? a.k_stride : a.v_stride);
+  const uint16_t* src = (kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) + t * stride + h0 * D;
 
-  __shared__ __align__(16) Chunk<CW> stage[kAppendIters][2][kAppendThreads];   // a thread's own places
-  {
-    const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+  auto copy_heads = [&](int it) {       // the heads of group `it` of src's token
+    if (h0 + it * HPW < heads) {
 #pragma unroll
-    for (int it = 0; it < kAppendIters; ++it) {
-      if (it < a.iters && h + it * HPW < heads) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) copy_chunk<CW>(&stage[it][j][threadIdx.x], src + (h + it * HPW) * D + off[j]);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      for (int j = 0; j < 2; ++j) copy_chunk<CW>(&stage[it][j][threadIdx.x], src + it * (HPW * D) + off[j]);
     }
-  }
-  int64_t slot = -1, blk = 0;
-  int row = 0;
-  if (kind != 0) {
-    slot = a.slots[t];
+  };
+  auto copy_turn = [&](int pos, int at) {   // the cosines and sines of a position; false: it is not in the table
+    if (pos >= 0 && pos < a.max_position) {
+      if (kind < 2 && 4 * lane < rot)
+        copy_chunk<8>(reinterpret_cast<Chunk<8>*>(&turn_rows[warp][at][4 * lane]),
+                      reinterpret_cast<const uint16_t*>(a.cos_sin + (int64_t)pos * rot + 4 * lane));
+      return true;
+    }
+    if (lane == 0) atomicOr(a.status, kDevBadInput);
+    return false;
+  };
+  // the first token
+  int64_t next_slot = kind != 0 ? a.slots[t] : -1;
+  int pos = rot ? a.positions[t] : 0, next_pos = rot && left > 1 ? a.positions[t + WARPS] : 0;
+#pragma unroll
+  for (int it = 0; it < kAppendIters; ++it)
+    if (it < iters) copy_heads(it);
+  const uint16_t* weight = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
+  if (weight != nullptr && 8 * lane < D)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"     // (through L1: every warp of the GPU reads these bytes)
+                 ::"r"(ptx::smem_u32(&weights[warp][8 * lane])), "l"(weight + 8 * lane)
+                 : "memory");
+  bool next_ok = rot ? copy_turn(pos, 0) : true;
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  int flip = 0;
+#pragma unroll 1
+  for (;; --left, t += WARPS, flip ^= 1) {
+    const bool ok = next_ok;
+    int64_t slot = next_slot;
     if (slot >= (int64_t)a.num_blocks * a.block_size) {
       if (lane == 0) atomicOr(a.status, kDevBadInput);
       slot = -1;
     }
-    blk = (uint32_t)slot >> a.bs_log;
-    row = (int)slot & (a.block_size - 1);
-  }
-  float cs[2][CW];          // cosines and sines of this lane's pairs
-  if (a.cos_sin != nullptr) {
-    const int pos = a.positions[t];
-    if (pos < 0 || pos >= a.max_position) {
-      if (lane == 0) atomicOr(a.status, kDevBadInput);
-      return;
-    }
-    if (turns && kind < 2) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float* c = a.cos_sin + (int64_t)pos * a.rot_dim + k * (rot / 2);
-        if constexpr (PAIRS) {
-          load_floats<CW / 2>(cs[k], c + off[0] / 2);
-          load_floats<CW / 2>(cs[k] + CW / 2, c + off[1] / 2);
-        } else {
-          load_floats<CW>(cs[k], c + off[0]);
-        }
-      }
-    }
-  }
-  if (kind != 0 && slot < 0) return;
-  const uint16_t* weight = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
-  Chunk<CW> wt[2] = {};
-  if (weight != nullptr) {
-    wt[0] = load_chunk<CW>(weight + off[0]);
-    wt[1] = load_chunk<CW>(weight + off[1]);
-  }
+    const int64_t blk = (uint32_t)slot >> a.bs_log;
+    const int row = (int)slot & (a.block_size - 1);
+    if (kind != 0 && left > 1) next_slot = a.slots[t + WARPS];
+    src += WARPS * stride;
+    int h = h0;
 #pragma unroll 1
-  for (int it = 0; it < a.iters; ++it, h += HPW) {
-    float x[2][CW];
-    wait_copies<kAppendIters>(it);
-    unpack_chunk<BF16, CW>(stage[it][0][threadIdx.x], x[0]);
-    unpack_chunk<BF16, CW>(stage[it][1][threadIdx.x], x[1]);
-    if (weight != nullptr) {
-      Two sq[2] = {two(0.f, 0.f), two(0.f, 0.f)};
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < CW; i += 2) {
-          const Two v = two(x[j][i], x[j][i + 1]);
-          sq[j] = fma2(v, v, sq[j]);
-        }
-      const float2 sums = split(add2(sq[0], sq[1]));
-      float ss = sums.x + sums.y;
-#pragma unroll
-      for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float g[CW];
-        // (unpacked anew for every head: kept as floats they would cost 2 CW registers and a third of the warps)
-#pragma unroll
-        for (int i = 0; i < CW / 2; ++i) asm volatile("" : "+r"(wt[j].w[i]));
-        unpack_chunk<BF16, CW>(wt[j], g);
-#pragma unroll
-        for (int i = 0; i < CW; i += 2) {
-          const float2 v = split(mul2(mul2(two(x[j][i], x[j][i + 1]), two(r, r)), two(g[i], g[i + 1])));
-          x[j][i] = v.x;
-          x[j][i + 1] = v.y;
+    for (int it = 0; it < iters; ++it, h += HPW) {
+      float x[2][CW];
+      wait_copies(iters);
+      if (it == 0) __syncwarp();     // the warp's cosines, sines and weights; and all lanes have read those of the last token
+      unpack_chunk<BF16, CW>(stage[it][0][threadIdx.x], x[0]);
+      unpack_chunk<BF16, CW>(stage[it][1][threadIdx.x], x[1]);
+      if (left > 1) {
+        copy_heads(it);
+        if (it == 0 && rot) {
+          next_ok = copy_turn(next_pos, flip ^ 1);
+          if (left > 2) next_pos = a.positions[t + 2 * WARPS];
         }
       }
-    }
-    if (turns && kind < 2) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (!ok || (kind != 0 && slot < 0)) continue;
+      if (weight != nullptr) {
+        Two sq[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < CW; ++i) {
-        // pair i of the lane: (x[0][i], x[1][i]), or neighbours of chunk i / (CW/2)
-        float& p = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2))] : x[0][i];
-        float& n = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2)) + 1] : x[1][i];
-        const float y = p * cs[0][i] - n * cs[1][i];
-        n = n * cs[0][i] + p * cs[1][i];
-        p = y;
-      }
-    }
-    if (kind == 0) {
-      if (h < heads) {
-        uint16_t* to = a.q_out + t * a.q_out_stride + h * D;
-        store_chunk<CW>(to + off[0], pack_chunk<BF16, CW>(x[0]));
-        store_chunk<CW>(to + off[1], pack_chunk<BF16, CW>(x[1]));
-      }
-    } else if constexpr (LAYOUT == 2) {
-      float top = 0.f;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < CW; ++i) top = fmaxf(top, fmaxf(fabsf(x[0][i]), fabsf(x[1][i])));
+          for (int i = 0; i < CW; i += 2) {
+            const Two v = two(x[j][i], x[j][i + 1]);
+            sq[j] = fma2(v, v, sq[j]);
+          }
+        const float2 sums = split(add2(sq[0], sq[1]));
+        float ss = sums.x + sums.y;
 #pragma unroll
-      for (int m = LPH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      const int e = kv8_exponent(top);
-      const int bb = kv8_block_bytes(a.block_size, D);
-      const int64_t at = (blk * a.h_kv + h) * bb;
-      if (h < heads && idx_ok(at + bb - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status)) {
-        uint8_t* base = reinterpret_cast<uint8_t*>(a.k_cache) + at;
-        uint8_t* codes = base + (kind - 1) * a.block_size * D;
-        const float inv = kv8_scale(254 - e);   // 2^-k
+        for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint8_t* to = codes + kv8_chunk<D>(row, off[j] >> 4) + (off[j] & 15);
-          if constexpr (CW == 8) *reinterpret_cast<uint2*>(to) = make_uint2(kv8_codes(x[j], inv), kv8_codes(x[j] + 4, inv));
-          else *reinterpret_cast<uint32_t*>(to) = kv8_codes(x[j], inv);
+          float g[CW];
+          unpack_chunk<BF16, CW>(load_chunk<CW>(&weights[warp][off[j]]), g);
+#pragma unroll
+          for (int i = 0; i < CW; i += 2) {
+            const float2 v = split(mul2(mul2(two(x[j][i], x[j][i + 1]), two(r, r)), two(g[i], g[i + 1])));
+            x[j][i] = v.x;
+            x[j][i + 1] = v.y;
+          }
         }
-        if (sub == 0) base[2 * a.block_size * D + (kind - 1) * a.block_size + row] = (uint8_t)e;
       }
-    } else if (h < heads) {
-      uint16_t* pool = reinterpret_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache);
-      const int64_t size = (int64_t)a.num_blocks * a.block_size * a.h_kv * D;
+      if (turns && kind < 2) {
+        const float* c = turn_rows[warp][flip];
+        float cs[2][CW];          // cosines and sines of this lane's pairs
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Chunk<CW> y = pack_chunk<BF16, CW>(x[j]);
-        if (LAYOUT == 0 || kind == 1) {
-          const int64_t at =
-              LAYOUT == 0 ? (slot * a.h_kv + h) * D + off[j]
-                            : (((blk * a.h_kv + h) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
-          if (idx_ok(at + CW - 1, size, a.status)) store_chunk<CW>(pool + at, y);
-        } else {
-          const int64_t at = ((blk * a.h_kv + h) * D + off[j]) * a.block_size + row;
-          if (!idx_ok(at + (CW - 1) * a.block_size, size, a.status)) continue;
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (PAIRS) {
+            shared_floats<CW / 2>(cs[k], c + k * (rot / 2) + off[0] / 2);
+            shared_floats<CW / 2>(cs[k] + CW / 2, c + k * (rot / 2) + off[1] / 2);
+          } else {
+            shared_floats<CW>(cs[k], c + k * (rot / 2) + off[0]);
+          }
+        }
 #pragma unroll
-          for (int i = 0; i < CW; ++i) pool[at + i * a.block_size] = (uint16_t)(y.w[i / 2] >> (16 * (i & 1)));
+        for (int i = 0; i < CW; ++i) {
+          // pair i of the lane: (x[0][i], x[1][i]), or neighbours of chunk i / (CW/2)
+          float& p = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2))] : x[0][i];
+          float& n = PAIRS ? x[i / (CW / 2)][2 * (i % (CW / 2)) + 1] : x[1][i];
+          const float y = p * cs[0][i] - n * cs[1][i];
+          n = n * cs[0][i] + p * cs[1][i];
+          p = y;
+        }
+      }
+      if (kind == 0) {
+        if (h < heads) {
+          uint16_t* to = a.q_out + t * a.q_out_stride + h * D;
+          store_chunk<CW>(to + off[0], pack_chunk<BF16, CW>(x[0]));
+          store_chunk<CW>(to + off[1], pack_chunk<BF16, CW>(x[1]));
+        }
+      } else if constexpr (LAYOUT == 2) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < CW; ++i) top = fmaxf(top, fmaxf(fabsf(x[0][i]), fabsf(x[1][i])));
+#pragma unroll
+        for (int m = LPH / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        const int e = kv8_exponent(top);
+        const int bb = kv8_block_bytes(a.block_size, D);
+        const int64_t at = (blk * a.h_kv + h) * bb;
+        if (h < heads && idx_ok(at + bb - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status)) {
+          uint8_t* base = reinterpret_cast<uint8_t*>(a.k_cache) + at;
+          uint8_t* codes = base + (kind - 1) * a.block_size * D;
+          const float inv = kv8_scale(254 - e);   // 2^-k
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint8_t* to = codes + kv8_chunk<D>(row, off[j] >> 4) + (off[j] & 15);
+            if constexpr (CW == 8) *reinterpret_cast<uint2*>(to) = make_uint2(kv8_codes(x[j], inv), kv8_codes(x[j] + 4, inv));
+            else *reinterpret_cast<uint32_t*>(to) = kv8_codes(x[j], inv);
+          }
+          if (sub == 0) base[2 * a.block_size * D + (kind - 1) * a.block_size + row] = (uint8_t)e;
+        }
+      } else if (h < heads) {
+        uint16_t* pool = reinterpret_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache);
+        const int64_t size = (int64_t)a.num_blocks * a.block_size * a.h_kv * D;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const Chunk<CW> y = pack_chunk<BF16, CW>(x[j]);
+          if (LAYOUT == 0 || kind == 1) {
+            const int64_t at =
+                LAYOUT == 0 ? (slot * a.h_kv + h) * D + off[j]
+                              : (((blk * a.h_kv + h) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
+            if (idx_ok(at + CW - 1, size, a.status)) store_chunk<CW>(pool + at, y);
+          } else {
+            const int64_t at = ((blk * a.h_kv + h) * D + off[j]) * a.block_size + row;
+            if (!idx_ok(at + (CW - 1) * a.block_size, size, a.status)) continue;
+#pragma unroll
+            for (int i = 0; i < CW; ++i) pool[at + i * a.block_size] = (uint16_t)(y.w[i / 2] >> (16 * (i & 1)));
+          }
         }
       }
     }
+    if (left == 1) return;
   }
 }
 

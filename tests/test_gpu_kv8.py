@@ -262,6 +262,52 @@ def test_append_reports_bad_slots_and_positions(gqa):
     assert good.shape == (6, 8 * D)
 
 
+@pytest.mark.parametrize("layout,D,hq,hk,T,bs,rot,inter,norm,elem", [
+    ("kv8", 128, 4, 2, 20011, 16, 128, False, True, "bf16"), ("rows", 128, 64, 8, 5003, 32, 64, False, True, "bf16"),
+    ("vllm", 64, 4, 2, 20003, 8, 24, True, True, "f16"), ("kv8", 64, 3, 3, 10009, 64, 0, False, True, "f16"),
+    ("rows", 128, 8, 4, 11000, 8, 24, False, False, "f16"), ("kv8", 128, 2, 1, 19999, 8, 128, True, True, "f16")])
+def test_append_warps_with_several_tokens(gqa, layout, D, hq, hk, T, bs, rot, inter, norm, elem):
+    """Calls with more tokens than the GPU has warps give what calls of few tokens give, bit for bit, padding and bad
+    slots and positions among them; in place too."""
+    c = append_case(elem, D, hq, hk, T, 400 + T, norm=norm, rot=rot)
+    nb, dt, g = T // bs + 2, DT[elem], gen(T)
+    slots = slots_for(T, nb, bs, 9, skip=T // 5)
+    slots[torch.randperm(T, generator=g)[:20]] = nb * bs + 7
+    bad = torch.randperm(T, generator=g)[:30] if rot else torch.zeros(0, dtype=torch.long)
+    c["pos"][bad] = torch.tensor([50, -1, 1 << 30] * 10)[:len(bad)].int()
+    part = lambda x, i: None if x is None else x[i:i + 1500]
+
+    def caches():
+        if layout == "kv8":
+            return [torch.full((nb, hk, bs * (2 * D + 2)), 0x5A, dtype=torch.uint8, device="cuda")]
+        if layout == "rows":
+            return [torch.full((nb, bs, hk * D), 3.0, dtype=dt, device="cuda") for _ in range(2)]
+        return [torch.full((nb, hk, D // 8, bs, 8), 3.0, dtype=dt, device="cuda"),
+                torch.full((nb, hk, D, bs), 3.0, dtype=dt, device="cuda")]
+
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want, small = torch.full((T, hq * D), 5.0, dtype=dt, device="cuda"), caches()
+    for i in range(0, T, 1500):
+        p = dict(c, **{n: part(c[n], i) for n in ("qkv", "pos")})
+        run_append(gqa, p, slots[i:i + 1500], *small, inter=inter, q_out=want[i:i + 1500], workspace_tensor=ws)
+    gqa.gqa_workspace_check(ws)
+    once, whole = torch.full_like(want, 5.0), caches()
+    run_append(gqa, c, slots, *whole, inter=inter, q_out=once, workspace_tensor=ws)
+    assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_INVALID_ARG
+    assert torch.equal(once, want) and all(torch.equal(a, b) for a, b in zip(whole, small))
+    assert (once[bad] == 5.0).all()
+    qkv, again = c["qkv"].cuda(), caches()
+    n = hq * D
+    gqa.gqa_append(qkv[:, :n], qkv[:, n:n + hk * D], qkv[:, n + hk * D:], hq, hk, slots.cuda(), *again,
+                   positions=c["pos"].cuda(), cos_sin=cuda(c["cs"]), interleaved=inter, q_weight=cuda(c["qw"]),
+                   k_weight=cuda(c["kw"]), eps=1e-5, q_out=qkv[:, :n], workspace_tensor=ws)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[bad] = False
+    assert torch.equal(qkv[keep, :n], want[keep]) and torch.equal(qkv[:, n:].cpu(), c["qkv"][:, n:])
+    assert torch.equal(qkv[bad, :n].cpu(), c["qkv"][bad, :n])
+    assert all(torch.equal(a, b) for a, b in zip(again, small))
+
+
 # ---------------------------------------------------------------- a cache as one finds it
 def make_cache(lens, D, hk, bs, seed, spread=3, tail=True, extra=2):
     """(cache, tables) numpy: values of normal size, scales spread over 2^spread, NaN codes and 255 exponents
