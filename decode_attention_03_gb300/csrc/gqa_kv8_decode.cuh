@@ -1030,7 +1030,11 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
     const uint32_t r = blockIdx.x / (D / 32), u = r / (uint32_t)a.rows;
     col += (int)(blockIdx.x % (D / 32)) * 32;
     unit = __ldcg(a.splits + u);
+    unit.z = (int)(u / (uint32_t)a.h_kv);
+    unit.w = (int)(u - (uint32_t)unit.z * (uint32_t)a.h_kv);
     pc.row = (int)(r - u * (uint32_t)a.rows);
+    // a worker whose wait gave up has not noted the units behind that tile: what lies there then may be anything
+    if ((uint32_t)unit.y >= 2u * (uint32_t)a.workers || unit.x > a.workers - (unit.y >> 1)) return;
   } else {
     const uint32_t i = blockIdx.x * WARPS + warp, w = i / (uint32_t)a.rows;
     if (w >= (uint32_t)a.workers) return;

@@ -298,7 +298,7 @@ gqa_status gqa_decode_paged_vllm_ex(const uint16_t* q, const uint16_t* k_cache, 
  * kv8: one byte array (num_blocks, h_kv, block_bytes), block_bytes = block_size * (2 * d_head + 2),
  * block_size in {8, 16, 32, 64}.  A (block, head) holds
  *   block_size rows of d_head K codes, block_size rows of d_head V codes  (e4m3 bytes),
- *   block_size K exponents, block_size V exponents                        (bytes e: the scale 2^(e-127));
+ *   block_size K exponents, block_size V exponents                        (bytes e in 1 .. 254: the scale 2^(e-127));
  * the 16-byte chunk c of row r of K or V is stored at chunk c ^ (r % 8) of the row for d_head 128 and at
  * chunk c ^ (r / 2 % 4) for d_head 64.  A row x (one token, one head) is stored as the codes
  * e4m3(x * 2^-k), rounded to nearest even, k the smallest integer with max|x| <= 448 * 2^k, at least

@@ -758,6 +758,28 @@ def test_bounds_checked_build_of_both_forms(gqa):
             check_decode(o, cache, t, lens, q, hq, hk, D, D ** -0.5, bs, False, "f16", f"{SHORT[i]} {short}")
 
 
+def test_timeout_before_a_unit_that_nobody_notes(gqa):
+    """The last worker, which has the end of a long sequence and a sequence of one tile, gives up before the latter; the
+    workspace holds anything at all behind its header, and the merge reads nothing outside of it."""
+    D, hq, hk, bs = 128, 4, 1, 16
+    lens = [100000, 5]
+    tiles = sum((n + 31) // 32 for n in lens)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    share = -(-tiles // (8 * sms))
+    last = (tiles - 1) // share
+    assert tiles - last * share == 3                         # two tiles of the long one, then the short one's
+    cache, tab = make_cache(lens, D, hk, bs, 106, tail=False)
+    q = torch.randn(2, hq * D, generator=gen(16)).half()
+    for junk in (0x5A, 0xFF, 0x7F, 0x00, 0x80):
+        ws = torch.full((gqa.gqa_decode_kv8_workspace_size(2, 1, hq, hk, D),), junk, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws, timeout_us=20000, test_stall_cta=last)
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_TIMEOUT
+        o = run_decode(gqa, cache, tab, lens, q, hq, hk, workspace_tensor=ws)
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+    check_decode(o, cache, tab, lens, q, hq, hk, D, D ** -0.5, bs, False, "f16", "after a timeout")
+
+
 def test_offsets_past_32_bits(gqa):
     """Blocks behind the first 4 GiB of a cache, written, attended to and read back."""
     D, hk, bs, hq = 128, 8, 64, 32
