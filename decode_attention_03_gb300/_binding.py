@@ -482,15 +482,15 @@ def _place(t: torch.Tensor, name: str) -> Tuple[int, int]:
 
 
 def _status_workspace(t: torch.Tensor, name: str) -> torch.Tensor:
-    """A workspace for calls that need its status word alone: the cached one of the stream, which graphs may
-    share with other calls (the kernels only set bits in it)."""
-    key = _place(t, name)
-    ws = _ws_cache.get(key)
+    """A workspace for calls that need its status word alone, ``workspace(256, use="status")`` of the stream.  It never
+    grows, so a graph that was captured with it may be replayed at any time (the kernels only set bits in it)."""
+    dev, raw = _place(t, name)
+    ws = _ws_cache.get((dev, raw, "status"))
     if ws is not None:
         return ws
     if _capturing():
         return torch.zeros(256, dtype=torch.uint8, device=t.device)
-    return workspace(256, t.device)
+    return workspace(256, t.device, use="status")
 
 
 def gqa_kv8_block_bytes(block_size: int, d_head: int) -> int:
@@ -521,7 +521,8 @@ def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q:
     q (T, h_q*D) or None, k, v (T, h_kv*D) float16 or bfloat16, rows dense (views of a fused projection serve).
     The cache: ``k_cache, v_cache`` of gqa_decode_paged (num_blocks, block_size, h_kv*D) or of
     gqa_decode_paged_vllm, or one 8-bit cache (gqa_kv8_cache), quantised as it is written.
-    Returns the queries after norm and rotation (``q_out``, which may be q itself)."""
+    Returns the queries after norm and rotation (``q_out``, which may be q itself).  What the kernel reports is in the
+    status word of ``workspace_tensor``, or of ``workspace(256, use="status")``."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions=positions, cos_sin=cos_sin,

@@ -968,6 +968,32 @@ def test_other_calls_on_the_same_stream_keep_their_counters(gqa):
     check_decode(o, cache, tab, lens, q.cpu(), hq, hk, D, D ** -0.5, bs, False, "f16", "after gqa_decode")
 
 
+def test_status_of_calls_without_a_workspace(gqa):
+    """The status word of the stream's own small workspace, eager and replayed; larger workspaces do not move it."""
+    D, hk = 64, 2
+    x = torch.randn(3, hk * D, generator=gen(60)).half().cuda()
+    cache, slots = gqa.gqa_kv8_cache(2, 16, hk, D), torch.tensor([0, 5, 31]).cuda()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        gqa.gqa_append(None, x, x, 0, hk, slots, cache)
+        status = gqa.workspace(256, use="status")
+        assert gqa.gqa_workspace_check(status) == gqa.GQA_OK
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            gqa.gqa_append(None, x, x, 0, hk, slots, cache)
+        gqa.workspace(1 << 22)
+        graph.replay()
+        assert gqa.gqa_workspace_check(status) == gqa.GQA_OK
+        slots[1] = 32
+        graph.replay()
+        assert gqa.workspace(256, use="status") is status
+        assert gqa.gqa_workspace_check(status) == gqa.GQA_ERR_INVALID_ARG
+        table = torch.tensor([[0, 7]], dtype=torch.int32, device="cuda")
+        gqa.gqa_kv8_read(cache, table, torch.tensor([20], dtype=torch.int32, device="cuda"), D, 20)
+        assert gqa.gqa_workspace_check(status) == gqa.GQA_ERR_INVALID_ARG
+
+
 def test_binding_checks(gqa):
     D, hq, hk, bs = 64, 8, 2, 16
     cache = gqa.gqa_kv8_cache(4, bs, hk, D)
