@@ -197,10 +197,13 @@ gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
   return GQA_OK;
 }
 
-// Workers for each unit from which the merge gives 32 columns of a row a CTA instead of a whole row a warp.  Measured (us;
-// from 7 / 16 / 32 on): 16 sequences of 250-500 keys, 8 KV heads (9 workers a unit) 15.5 / 12.4 / 12.4, 16 of 1000-2000
-// 20.9 / 18.0 / 18.1; fewer units the same.
+// Workers for each unit from which the merge gives 32 columns of a row a CTA instead of a whole row a warp, as long as those
+// are no more than kMergeCtas.  Measured (us, columns a CTA / rows a warp; CTAs in brackets): 9 pieces, 16 sequences of
+// 250-500 keys, 8 KV heads 15.5 / 12.4; 19 pieces, 8 of 8000-16000 38.7 / 40.4 [1024], 64 of 16000-32000 with one KV head of
+// 4 query heads 67.3 / 69.4 [1024], of 16 79.2 / 75.3 [4096]; 38 pieces, 4 of 8000-16000 23.8 / 30.9 [512]; 64 rows of 30 of
+// 8000-16000, d 64, 54.2 / 51.6 [3840].
 constexpr int kManyPieces = 16;
+constexpr int kMergeCtas = 2048;
 
 // CTAs of a unit in the short kernel, a cluster of 1, 2, 4 or 8: the fewest that give each worker one tile, as far as all
 // units' clusters fit on three quarters of the SMs at once (a cluster lies in one GPC).  0: the general kernel, where a
@@ -310,7 +313,8 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
     if (p.ctas > 0) grid = (unsigned)(units * p.ctas);
     p.workers = (int)grid * kv8_groups(cls);
     // pieces of a unit: about workers / units + 1 when the sequences are alike
-    const bool many = p.workers / units >= kManyPieces, cut = seq_tiles > 1 && p.ctas == 0;   // (a unit of one tile is never cut)
+    const bool many = p.workers / units >= kManyPieces && units * rows * (D / 32) <= kMergeCtas;
+    const bool cut = seq_tiles > 1 && p.ctas == 0;   // (a unit of one tile is never cut)
     p.sliced = many ? 1 : 0;
     const cudaError_t e = D == 64 ? (bf16 ? kv8_decode<64, true>(p, cls, grid, cut, many, st)
                                           : kv8_decode<64, false>(p, cls, grid, cut, many, st))
