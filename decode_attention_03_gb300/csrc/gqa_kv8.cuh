@@ -191,6 +191,62 @@ __device__ __forceinline__ void shared_floats(float* x, const float* p) {
   }
 }
 
+// The values of a CTA's tokens into vLLM's value cache, where a token's elements lie block_size apart: a warp takes 64
+// columns of a head of eight tokens, which mostly fill eight neighbouring rows of a block, so that a column's eight are one
+// 16-byte store.  2810 tokens of 64 + 8 + 8 heads of 128: VLLM_FIGURE.
+template <int D, int HPW>
+__device__ __forceinline__ void append_vllm_values(const AppendParams& a, int set) {
+  constexpr int WARPS = kAppendThreads / 32, PARTS = D / 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h0 = set * (a.iters * HPW), heads = min(a.iters * HPW, a.h_kv - h0);
+  const int64_t first = (int64_t)blockIdx.x * (8 * a.run);
+  const int octets = (int)min((int64_t)a.run, (a.num_tokens - first + 7) / 8), per = heads * PARTS;
+  const int64_t rows = (int64_t)a.num_blocks * a.block_size, size = rows * a.h_kv * D;
+  uint16_t* cache = reinterpret_cast<uint16_t*>(a.v_cache);
+  for (int i = warp; i < octets * per; i += WARPS) {
+    const int oct = i / per, part = i - oct * per, h = h0 + part / PARTS, d = part % PARTS * 64 + 2 * lane;
+    const int64_t t0 = first + 8 * oct;
+    const int n = (int)min((int64_t)8, a.num_tokens - t0);
+    uint32_t x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(a.v + (t0 + j) * a.v_stride + h * D + d)) : 0u;
+    // lane j < n: where token j goes, or -1
+    int64_t slot = lane < n ? a.slots[t0 + lane] : -1;
+    bool bad = slot >= rows;
+    if (a.cos_sin != nullptr && lane < n) {
+      const int pos = a.positions[t0 + lane];
+      bad |= pos < 0 || pos >= a.max_position;
+    }
+    if (bad) {
+      atomicOr(a.status, kDevBadInput);
+      slot = -1;
+    }
+    const int s = slot < 0 ? -1 : (int)slot, s0 = __shfl_sync(0xffffffffu, s, 0);
+    const uint32_t follow = __ballot_sync(0xffffffffu, s >= 0 && s == s0 + lane);
+    if ((follow & 0xffu) == 0xffu && (s0 & 7) == 0) {
+      const int64_t at = (((int64_t)(s0 >> a.bs_log) * a.h_kv + h) * D + d) * a.block_size + (s0 & (a.block_size - 1));
+      if (!idx_ok(at + a.block_size + 7, size, a.status)) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t pick = k == 0 ? 0x5410 : 0x7632;
+        *reinterpret_cast<uint4*>(cache + at + k * a.block_size) =
+            make_uint4(__byte_perm(x[0], x[1], pick), __byte_perm(x[2], x[3], pick), __byte_perm(x[4], x[5], pick),
+                       __byte_perm(x[6], x[7], pick));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int sj = __shfl_sync(0xffffffffu, s, j);
+        const int64_t at = (((int64_t)(sj >> a.bs_log) * a.h_kv + h) * D + d) * a.block_size + (sj & (a.block_size - 1));
+        if (sj < 0 || !idx_ok(at + a.block_size, size, a.status)) continue;
+        cache[at] = (uint16_t)x[j];
+        cache[at + a.block_size] = (uint16_t)(x[j] >> 16);
+      }
+    }
+  }
+}
+
 // A head's D elements lie on D/(2 CW) lanes, each with two chunks of CW: elements CW s.. and rot/2 + CW s.. for
 // the lanes s < rot/(2 CW) that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
 // thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes
@@ -211,12 +267,16 @@ gqa_append_kernel(const AppendParams a) {
   ptx::grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPH;
   // a CTA has one set of heads of WARPS * a.run tokens, a warp every WARPS-th of them
-  int64_t t = (int64_t)blockIdx.x * (WARPS * a.run) + warp;
-  if (t >= a.num_tokens) return;
-  int left = min(a.run, (a.num_tokens - 1 - (int)t) / WARPS + 1);   // tokens of this warp
   int set = blockIdx.y;
   const int kind = set < a.q_sets ? 0 : (set < a.q_sets + a.k_sets ? 1 : 2);
   set -= kind == 0 ? 0 : (kind == 1 ? a.q_sets : a.q_sets + a.k_sets);
+  if (LAYOUT == 1 && kind == 2) {
+    append_vllm_values<D, HPW>(a, set);
+    return;
+  }
+  int64_t t = (int64_t)blockIdx.x * (WARPS * a.run) + warp;
+  if (t >= a.num_tokens) return;
+  int left = min(a.run, (a.num_tokens - 1 - (int)t) / WARPS + 1);   // tokens of this warp
   const int heads = kind == 0 ? a.h_q : a.h_kv;
   const int h0 = set * (a.iters * HPW) + lane / LPH;
   const int iters = min(a.iters, (heads - set * (a.iters * HPW) + HPW - 1) / HPW);   // groups of this warp
@@ -369,17 +429,10 @@ gqa_append_kernel(const AppendParams a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const Chunk<CW> y = pack_chunk<BF16, CW>(x[j]);
-          if (LAYOUT == 0 || kind == 1) {
-            const int64_t at =
-                LAYOUT == 0 ? (slot * a.h_kv + h) * D + off[j]
-                              : (((blk * a.h_kv + h) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
-            if (idx_ok(at + CW - 1, size, a.status)) store_chunk<CW>(pool + at, y);
-          } else {
-            const int64_t at = ((blk * a.h_kv + h) * D + off[j]) * a.block_size + row;
-            if (!idx_ok(at + (CW - 1) * a.block_size, size, a.status)) continue;
-#pragma unroll
-            for (int i = 0; i < CW; ++i) pool[at + i * a.block_size] = (uint16_t)(y.w[i / 2] >> (16 * (i & 1)));
-          }
+          const int64_t at = LAYOUT == 0
+                                 ? (slot * a.h_kv + h) * D + off[j]
+                                 : (((blk * a.h_kv + h) * (D / 8) + off[j] / 8) * a.block_size + row) * 8 + off[j] % 8;
+          if (idx_ok(at + CW - 1, size, a.status)) store_chunk<CW>(pool + at, y);
         }
       }
     }

@@ -262,6 +262,33 @@ def test_append_reports_bad_slots_and_positions(gqa):
     assert good.shape == (6, 8 * D)
 
 
+@pytest.mark.parametrize("D,hk,bs", [(128, 8, 32), (64, 3, 8), (128, 1, 16), (64, 21, 64)])
+@pytest.mark.parametrize("T,start,holes", [(1, 0, ()), (8, 8, ()), (200, 0, ()), (333, 5, ()), (97, 16, (3, 40, 41, 96)),
+                                           (30, 7, (0,))])
+def test_append_values_into_vllm_rows_in_order(gqa, D, hk, bs, T, start, holes):
+    """Tokens of a prompt, whose slots follow one another, from an even or odd place on, with padding among them: the
+    values are where the layout has them, bit for bit, and nothing else is written."""
+    nb = (T + start) // bs + 2
+    order = torch.randperm(nb, generator=gen(T))
+    at = torch.arange(start, start + T)
+    slots = order[at // bs] * bs + at % bs
+    slots[list(holes)] = -1
+    x = torch.randn(T, 2 * hk * D, generator=gen(T + 1)).half()
+    x[0, -1] = math.nan
+    k, v = torch.full((nb, hk, D // 8, bs, 8), 3.0).half().cuda(), torch.full((nb, hk, D, bs), 3.0).half().cuda()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    xc = x.cuda()
+    gqa.gqa_append(None, xc[:, :hk * D], xc[:, hk * D:], hk, hk, slots.cuda(), k, v, workspace_tensor=ws)
+    assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+    keep = slots >= 0
+    want_k, want_v = torch.full(k.shape, 3.0).half(), torch.full(v.shape, 3.0).half()
+    b, r = (slots // bs)[keep], (slots % bs)[keep]
+    want_k[b, :, :, r] = x[keep, :hk * D].view(-1, hk, D // 8, 8)
+    want_v[b, :, :, r] = x[keep, hk * D:].view(-1, hk, D)
+    assert torch.equal(k.cpu().view(torch.int16), want_k.view(torch.int16))
+    assert torch.equal(v.cpu().view(torch.int16), want_v.view(torch.int16))
+
+
 @pytest.mark.parametrize("layout,D,hq,hk,T,bs,rot,inter,norm,elem", [
     ("kv8", 128, 4, 2, 20011, 16, 128, False, True, "bf16"), ("rows", 128, 64, 8, 5003, 32, 64, False, True, "bf16"),
     ("vllm", 64, 4, 2, 20003, 8, 24, True, True, "f16"), ("kv8", 64, 3, 3, 10009, 64, 0, False, True, "f16"),
