@@ -24,7 +24,7 @@ gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_E
 // ---------------------------------------------------------------- per-device state
 struct Kv8Device {
   int sms = 0;
-  bool ready[2][4][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
+  bool ready[2][6][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
 };
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -156,9 +156,11 @@ gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
 }
 
 // ---------------------------------------------------------------- decode
-// Kernel shapes: up to 8, 16 or 32 query rows for one warp, 64 for two warps that share a ring.
-int kv8_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 3)); }
-int kv8_groups(int cls) { return cls < 3 ? kKv8Warps : kKv8Warps / 2; }
+// Kernel shapes: up to 8, 16, 24 or 32 query rows for one warp, 48 or 64 for two warps that share a ring.
+// 24 and 48 beside 32 and 64, measured (us, with / without): 131071 keys, 24 rows, d 128 57.1 / 67.7, in f16 65.3 / 85.3; 10
+// sequences of 5000-53000, 35 rows 136 / 175; 43 of 50-1460, 24 rows, d 64 27.8 / 31.4.
+int kv8_class(int rows) { return rows <= 32 ? (rows + 7) / 8 - 1 : (rows <= 48 ? 4 : 5); }
+int kv8_groups(int cls) { return cls < 4 ? kKv8Warps : kKv8Warps / 2; }
 
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_prepare() {
@@ -175,7 +177,9 @@ cudaError_t kv8_prepare_class(int cls) {
   switch (cls) {
     case 0: return kv8_prepare<D, 1, 1, BF16>();
     case 1: return kv8_prepare<D, 2, 1, BF16>();
-    case 2: return kv8_prepare<D, 4, 1, BF16>();
+    case 2: return kv8_prepare<D, 3, 1, BF16>();
+    case 3: return kv8_prepare<D, 4, 1, BF16>();
+    case 4: return kv8_prepare<D, 3, 2, BF16>();
     default: return kv8_prepare<D, 4, 2, BF16>();
   }
 }
@@ -250,7 +254,9 @@ cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool cut, boo
   switch (cls) {
     case 0: e = kv8_launch<D, 1, 1, BF16>(p, grid, st); break;
     case 1: e = kv8_launch<D, 2, 1, BF16>(p, grid, st); break;
-    case 2: e = kv8_launch<D, 4, 1, BF16>(p, grid, st); break;
+    case 2: e = kv8_launch<D, 3, 1, BF16>(p, grid, st); break;
+    case 3: e = kv8_launch<D, 4, 1, BF16>(p, grid, st); break;
+    case 4: e = kv8_launch<D, 3, 2, BF16>(p, grid, st); break;
     default: e = kv8_launch<D, 4, 2, BF16>(p, grid, st); break;
   }
   if (e != cudaSuccess || !cut) return e;

@@ -658,6 +658,10 @@ SHORT = [  # D, hq, hk, T, bs, sequences, blocks of the table -> CTAs of a unit,
     (128, 16, 4, 12, 16, 8, 80),     # 2, 5, two warps on a ring of four
     (64, 80, 2, 1, 32, 12, 72),      # 4, 5: two warps on a ring of eight
     (64, 64, 1, 1, 8, 3, 21),        # 2, 1: the last CTA has part of its workers
+    (128, 24, 2, 2, 16, 6, 100),     # 8, 1, 24 rows
+    (64, 7, 1, 3, 32, 20, 60),       # 4, 2, 21 rows
+    (128, 40, 1, 1, 16, 9, 64),      # 8, 1, 40 rows
+    (64, 48, 2, 2, 8, 8, 240),       # 4, 4, 48 rows, a ring of two warps goes round
 ]
 
 
