@@ -298,6 +298,11 @@ gqa_append_kernel(const AppendParams a) {
   const int64_t stride = kind == 0 ? a.q_stride : (kind == 1 ? a.k_stride : a.v_stride);
   const uint16_t* src = (kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) + t * stride + h0 * D;
 
+  // where a lane's four cosines or sines lie: as in the table, but where eight threads read eight each (SPLIT) the first fours
+  // of all and then the second ones, free of bank conflicts (1024 tokens of 64 + 8 + 8 heads 8.4 -> 7.8 us)
+  constexpr bool SPLIT = D == 128 && CW == 8 && !PAIRS;
+  const int quarter = rot / 8, q4 = lane < quarter ? lane : lane - quarter;
+  const int place = SPLIT ? 4 * ((lane - q4) + (q4 >> 1) + (q4 & 1) * (quarter >> 1)) : 4 * lane;
   auto copy_heads = [&](int it) {       // the heads of group `it` of src's token
     if (h0 + it * HPW < heads) {
 #pragma unroll
@@ -307,7 +312,7 @@ gqa_append_kernel(const AppendParams a) {
   auto copy_turn = [&](int pos, int at) {   // the cosines and sines of a position; false: it is not in the table
     if (pos >= 0 && pos < a.max_position) {
       if (kind < 2 && 4 * lane < rot)
-        copy_chunk<8>(reinterpret_cast<Chunk<8>*>(&turn_rows[warp][at][4 * lane]),
+        copy_chunk<8>(reinterpret_cast<Chunk<8>*>(&turn_rows[warp][at][place]),
                       reinterpret_cast<const uint16_t*>(a.cos_sin + (int64_t)pos * rot + 4 * lane));
       return true;
     }
@@ -389,7 +394,10 @@ gqa_append_kernel(const AppendParams a) {
         float cs[2][CW];          // cosines and sines of this lane's pairs
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if constexpr (PAIRS) {
+          if constexpr (SPLIT) {
+            shared_floats<4>(cs[k], c + k * (rot / 2) + off[0] / 2);
+            shared_floats<4>(cs[k] + 4, c + k * (rot / 2) + rot / 4 + off[0] / 2);
+          } else if constexpr (PAIRS) {
             shared_floats<CW / 2>(cs[k], c + k * (rot / 2) + off[0] / 2);
             shared_floats<CW / 2>(cs[k] + CW / 2, c + k * (rot / 2) + off[1] / 2);
           } else {
