@@ -16,13 +16,17 @@
 // query rows on its N side (n = 8: with 4 query heads a KV head only half of the tile is idle).  K codes come
 // by ldmatrix -- a thread's 4 bytes are the elements 16j + 4c .. +3 of one key, and since the order of the
 // summed index is free, Q is laid out to match -- and become f16 by one conversion for two codes, exactly.
-// The K scale multiplies the fp32 score, the V scale multiplies the weight: P = p 2^(ev - e), e the largest V
-// exponent so far, so that P <= 2^8 stays in f16's range whatever the scales are (O is rescaled when e grows,
-// together with the running maximum).  V codes come by transposing ldmatrix as byte pairs of two d for each of
-// two keys, one byte permutation turns them into pairs of keys, the MMA's A operand of O^T += V^T P^T.
+// The K scale multiplies the fp32 score, the V scale multiplies the weight: P = p 2^(ev - e + 11), e the largest V
+// exponent so far (O is rescaled when e grows, together with the running maximum), so that P <= 2^15.  f16 holds a
+// weight with all its bits down to 2^-25 of the running maximum's, and nothing below 2^-36; as long as the V exponents seen
+// lie within 10 of one another, that is at most 2^-26 of the row's largest term.  Where they lie further apart (a row of
+// zeros, an infinity, an outlier), a weight of 1 may belong to the smallest terms of its row, and the worker goes on with
+// the wide form of a tile's products (kv8_wide), which has a reference of its own for every tile, row and range of
+// exponents.  V codes come by transposing ldmatrix as byte pairs of two d for each of two keys, one byte permutation turns
+// them into pairs of keys, the MMA's A operand of O^T += V^T P^T.
 // bfloat16 queries are brought into f16's range by a power of two for each row (8 bits of fraction fit into
 // 11: nothing is rounded that fp32 sums would keep); O, m and l are fp32.
-// The running maximum is only moved when a score exceeds it by 2^8: the weights stay below 2^8 and the
+// The running maximum is only moved when a score exceeds it by 2^4: the weights stay below 2^4 and the
 // common tile needs no cross-lane maximum and no rescaling.
 #pragma once
 #include "gqa_kv8.cuh"
@@ -35,7 +39,13 @@ constexpr int kKv8Seqs = 1024;                 // sequences of a launch (the hos
 constexpr int kKv8Warps = 8;
 constexpr int kKv8Short = 8;                   // tiles of a worker of the short kernel: 32 blocks of 8 keys
 constexpr int kKv8Threads = 32 * kKv8Warps;
-constexpr float kKv8Slack = 8.f;               // log2 of the largest weight
+// log2 of the largest weight.  8 leaves a lift of 7 bits instead of 11, and a weight of 2^-26 none of its bits; fewer moves
+// of the maximum then (131071 keys, 32 rows 71.9 us instead of 73.5, one n-tile the same).
+constexpr float kKv8Slack = 4.f;
+constexpr int kKv8Lift = 11;                   // P in f16 is the weight times 2^this: at most 2^15
+constexpr int kKv8Spread = 10;                 // V exponents further apart than this: the wide form
+constexpr int kKv8Wide = 1024;                 // Kv8Warp::lo of a worker that has gone over to it, above every exponent
+constexpr int kKv8WideUnit = 16;               // log2 of the unit of its O: sums of many values of 448 * 2^120 fit
 
 struct Kv8Params {
   const uint16_t* q;
@@ -105,7 +115,7 @@ __device__ __forceinline__ uint32_t kv8_transpose(uint32_t x) {
   return y;
 }
 
-// 2^(e - 127 + d) for d <= 0, 0 where that leaves the range
+// 2^d for d <= 127, 0 below 2^-126
 __device__ __forceinline__ float kv8_ratio(int d) { return __uint_as_float((uint32_t)max(d + 127, 0) << 23); }
 
 // A place on the axis of tiles: tile t of the `tiles` tiles of head g of sequence b.
@@ -317,8 +327,7 @@ struct Kv8Warp {
   uint32_t q_at;
   float acc[KD][NT][4];
   float m[NT][2], l[NT][2];
-  int last;             // last key of the sequence
-  int e;                // largest V exponent byte so far
+  int e, lo;            // largest and smallest V exponent byte so far; lo = kKv8Wide: the wide form
   // the same for every unit and tile
   uint32_t rows[2];     // byte offset in a tile of this lane's ldmatrix row, keys 16p + lane % 16
   uint32_t ex[4];       // and of the K exponent of key 8o + lane / 4
@@ -413,7 +422,6 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT
       w.l[nt][i] = 0.f;
     }
   }
-  w.last = len - 1;
 #pragma unroll
   for (int j = 0; j < KD; ++j)
 #pragma unroll
@@ -421,34 +429,131 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT
 #pragma unroll
       for (int i = 0; i < 4; ++i) w.acc[j][nt][i] = 0.f;
   w.e = 1;
+  w.lo = 255;
   if constexpr (W::Q_SMEM) __syncwarp();
 }
 
-// One tile of `valid` keys (key0 the first), `st` its place in the ring; masked: some key of it is hidden
-// from some row.
+// O += the products of a tile whose V exponents, or those before it, lie far apart.  y qs + off: a key's weight in log2
+// units, -inf where it is hidden.  The keys go by ranges of 11 exponents from the largest on, and a row's weights in a
+// range are relative to its largest one there: a product too small for f16 is at most 2^-29 of the largest of its tile,
+// row and range.  The sums of a range start from zero and are added to O in fp32, whose unit is 2^kKv8WideUnit.
+// Values below 2^-88 beside much larger ones, and terms below 2^-110, are not kept.  Rare: each n-tile reads V again, and
+// it is a call with its arrays in local memory, so that the common form keeps its registers.  Measured (us; no V row of
+// zeros / the first row of every sequence / one row of 64): 64 sequences of 8000-16000 keys, 4 rows 228 / 346 / 452; 131071
+// keys, 32 rows 73.6 / 205 / 385; 4096 keys, d 64 7.3 / 8.9 / 10.1.
+template <int D, int NT>
+struct Kv8WideTile {
+  float acc[D / 16][NT][4];
+  float2 x[4][NT];          // log2 of the weights of keys 8o + lane / 4
+  int ev[4];                // and their V exponents
+  uint32_t v[2], turn;      // this lane's rows of V for ldmatrix, and its chunk swizzle
+  Win ring;
+};
+
+template <int D, int NT, bool FINE>
+__device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
+  constexpr int KD = D / 16, kUp = 14;
+#pragma unroll 1
+  for (int hi = 255;;) {
+    int top = 0;       // this range: exponents top - kKv8Spread .. top
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+      if (w.ev[o] <= hi) top = max(top, w.ev[o]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (top == 0) return;
+    hi = top - kKv8Spread - 1;
+    const float back = kv8_ratio(top - 127 - kUp - kKv8WideUnit);
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      float2 x[4];
+      float m[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const bool in = w.ev[o] <= top && w.ev[o] > hi;
+        x[o] = in ? w.x[o][nt] : make_float2(-CUDART_INF_F, -CUDART_INF_F);
+        m[0] = fmaxf(m[0], x[o].x);
+        m[1] = fmaxf(m[1], x[o].y);
+      }
+      float up[2], base[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 4));
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+        base[i] = m[i] == -CUDART_INF_F ? 0.f : m[i];
+        up[i] = ptx::ex2(base[i]);
+      }
+      uint32_t pf[2][2], pl[2][2];
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const float v = w.ev[o] <= top && w.ev[o] > hi ? kv8_ratio(w.ev[o] - top + kUp) : 0.f;
+        const float2 p = make_float2(ptx::ex2(x[o].x - base[0]) * v, ptx::ex2(x[o].y - base[1]) * v);
+        const uint32_t h = ptx::pack_half2(p.x, p.y);
+        pf[o >> 1][o & 1] = kv8_transpose(h);
+        if constexpr (FINE) {
+          const float2 f = half2_floats(h);
+          pl[o >> 1][o & 1] = kv8_transpose(ptx::pack_half2(p.x - f.x, p.y - f.y));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KD; j += 2) {
+        float sum[2][4] = {};
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t v[4], f[2][4];
+          ptx::ldmatrix_x4_trans(v, smem_clamp(w.v[p] + ((uint32_t)(j << 4) ^ w.turn), 16, w.ring.lo, w.ring.hi,
+                                               w.ring.status));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            kv8_unpack(__byte_perm(v[i], 0, 0x3120), f[i >> 1][(i & 1) * 2], f[i >> 1][(i & 1) * 2 + 1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            kv8_mma(sum[k], f[k], pf[p]);
+            if constexpr (FINE) kv8_mma(sum[k], f[k], pl[p]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)      // (a row without keys in this range meets none of its NaN)
+            if (m[i & 1] != -CUDART_INF_F) w.acc[j + k][nt][i] = fmaf(sum[k][i] * up[i & 1], back, w.acc[j + k][nt][i]);
+      }
+    }
+  }
+}
+
+// One tile of `valid` keys, `st` its place in the ring; last: the sequence's last key, counted from the tile's first;
+// masked: some key of it is hidden from some row.
 // FINE: the weights as two f16 numbers, the rounded one and what was lost.  A weight rounded to f16 is off by as much as
 // an f16 output is (64 sequences, against 64 bits: 2.9e-4 instead of 2.1e-4, 1.41 times), so f16 calls take the
 // second product; the rounding of a bf16 output is eight times as coarse.
 template <int D, int NT, int RG, bool FINE>
 __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, uint32_t st, int eb, int valid,
-                                         int key0, bool masked, int rg, int lane, const Win& ring) {
+                                         int last, bool masked, int rg, int lane, const Win& ring) {
   using W = Kv8Warp<D, NT, RG>;
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2;
   if (valid < kKv8Keys) {
-    // V rows that hold no key: zeros, so that a weight of 0 meets no NaN.  Then the writes are ordered before
-    // the next copy into this place.
+    // V rows that hold no key: zeros, so that a weight of 0 meets no NaN, and the exponent of the first key, which spreads
+    // nothing.  Then the writes are ordered before the next copy into this place.
     for (int i = lane; i < (kKv8Keys - valid) * KD; i += 32) {
       const int key = valid + i / KD;
       const uint32_t to = st + key / eb * kv8_block_bytes(eb, D) + (eb + key % eb) * D + i % KD * 16;
       if (smem_ok(to, 16, ring.lo, ring.hi, ring.status))
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
     }
+    const uint32_t v_exp = st + 2 * eb * D + eb;
+    uint32_t first;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(first) : "r"(smem_clamp(v_exp, 1, ring.lo, ring.hi, ring.status)));
+    if (lane >= valid) {
+      const uint32_t to = v_exp + lane / eb * kv8_block_bytes(eb, D) + lane % eb;
+      if (smem_ok(to, 1, ring.lo, ring.hi, ring.status)) asm volatile("st.shared.u8 [%0], %1;" ::"r"(to), "r"(first) : "memory");
+    }
     ptx::fence_proxy_async_smem();
     __syncwarp();
   }
   // ---- exponents of this lane's keys 8o + r
-  int ek[4], ev[4], top = 1;
+  int ek[4], ev[4];
 #pragma unroll
   for (int o = 0; o < 4; ++o) {
     uint32_t x, y;
@@ -456,8 +561,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at));
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(smem_clamp(st + w.ex[o] + eb, 1, ring.lo, ring.hi, ring.status)));
     ek[o] = (int)x;
-    ev[o] = 8 * o + r < valid ? (int)y : 1;
-    top = max(top, ev[o]);
+    ev[o] = (int)y;
   }
   // ---- S^T = K Q^T
   float s[2][NT][4];
@@ -499,8 +603,8 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
   }
   // ---- y = the scores by the K scales; the logit in log2 units is y qs, qs >= 0 of the row.
   // s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
-  top = __reduce_max_sync(0xffffffffu, top);
-  bool over = false;
+  // over: a score far above the running maximum, or a V exponent outside of what has been seen
+  bool over = max(max(ev[0], ev[1]), max(ev[2], ev[3])) > w.e || min(min(ev[0], ev[1]), min(ev[2], ev[3])) < w.lo;
   float mx[NT][2];
   Two y[4][NT], qs[NT];
 #pragma unroll
@@ -529,7 +633,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = (rg * NT + nt) * 8 + 2 * (lane & 3) + i;
-        lim[i] = w.last - key0 - (a.causal ? max(a.T_q - 1 - row / a.G, 0) : 0);
+        lim[i] = last - (a.causal ? max(a.T_q - 1 - row / a.G, 0) : 0);
       }
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
@@ -547,28 +651,48 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     mx[nt][1] = t.y;
     over |= t.x > w.m[nt][0] + kKv8Slack || t.y > w.m[nt][1] + kKv8Slack;
   }
-  const bool grow = __any_sync(0xffffffffu, over);
-  if (grow || top > w.e) {
-    const int e = max(top, w.e);
-    const float fe = kv8_ratio(w.e - e);
-    w.e = e;
+  bool wide = false;
+  if (__any_sync(0xffffffffu, over)) {
+    float fe = 1.f;
+    if (w.lo != kKv8Wide) {
+      int top = w.e, low = w.lo;
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        top = max(top, ev[o]);
+        low = min(low, ev[o]);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      low = __reduce_min_sync(0xffffffffu, low);
+      if (top - low > kKv8Spread) {
+        const float f = kv8_ratio(w.e - 127 - kKv8Lift - kKv8WideUnit);
+#pragma unroll
+        for (int j = 0; j < KD; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f;
+        w.lo = kKv8Wide;
+      } else {
+        fe = kv8_ratio(w.e - top);
+        w.e = top;
+        w.lo = low;
+      }
+    }
+    wide = w.lo == kKv8Wide;
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        f[nt][i] = fe;
-        if (grow) {
-          float x = mx[nt][i];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, w.m[nt][i]);
-          const float alpha = ptx::ex2(w.m[nt][i] - (x == -CUDART_INF_F ? 0.f : x));
-          w.m[nt][i] = x;
-          w.l[nt][i] *= alpha;
-          f[nt][i] *= alpha;
-        }
+        float x = mx[nt][i];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        x = fmaxf(x, w.m[nt][i]);
+        f[nt][i] = ptx::ex2(w.m[nt][i] - (x == -CUDART_INF_F ? 0.f : x));
+        w.m[nt][i] = x;
+        w.l[nt][i] *= f[nt][i];
+        f[nt][i] *= fe;
       }
 #pragma unroll
     for (int j = 0; j < KD; ++j)
@@ -578,16 +702,51 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
         for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f[nt][i & 1];
   }
   // ---- weights, and P as the B operand
-  uint32_t pf[2][NT][2], pl[2][NT][2];
   Two off[NT], sum[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     off[nt] = two(w.m[nt][0] == -CUDART_INF_F ? 0.f : -w.m[nt][0], w.m[nt][1] == -CUDART_INF_F ? 0.f : -w.m[nt][1]);
     sum[nt] = two(w.l[nt][0], w.l[nt][1]);
   }
+  if (wide) {
+    Kv8WideTile<D, NT> t;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const float2 x = split(fma2(y[o][nt], qs[nt], off[nt]));
+        sum[nt] = add2(sum[nt], two(ptx::ex2(x.x), ptx::ex2(x.y)));
+        t.x[o][nt] = x;
+      }
+      const float2 f = split(sum[nt]);
+      w.l[nt][0] = f.x;
+      w.l[nt][1] = f.y;
+    }
+#pragma unroll
+    for (int o = 0; o < 4; ++o) t.ev[o] = ev[o];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) t.v[p] = st + w.rows[p] + eb * D;
+    t.turn = w.turn;
+    t.ring = ring;
+#pragma unroll
+    for (int j = 0; j < KD; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.acc[j][nt][i] = w.acc[j][nt][i];
+    kv8_wide<D, NT, FINE>(t);
+#pragma unroll
+    for (int j = 0; j < KD; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.acc[j][nt][i] = t.acc[j][nt][i];
+    return;
+  }
+  uint32_t pf[2][NT][2], pl[2][NT][2];
 #pragma unroll
   for (int o = 0; o < 4; ++o) {
-    const float v = kv8_ratio(ev[o] - w.e);
+    const float v = kv8_ratio(ev[o] - w.e + kKv8Lift);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 x = split(fma2(y[o][nt], qs[nt], off[nt]));
@@ -630,12 +789,26 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     }
 }
 
+// A state as it leaves the worker: m + shift, l 2^-shift and O times `unit` stand for m, l and O.
+template <int D, int NT, int RG>
+struct Kv8Units {
+  float shift, l, o;
+  __device__ __forceinline__ explicit Kv8Units(const Kv8Warp<D, NT, RG>& w) {
+    const bool wide = w.lo == kKv8Wide;
+    shift = wide ? (float)kKv8WideUnit : -(float)kKv8Lift;
+    l = wide ? 1.f / (float)(1ull << kKv8WideUnit) : (float)(1 << kKv8Lift);
+    o = wide ? 1.f : kv8_scale((uint32_t)w.e);
+  }
+};
+
 // The end of a piece: the whole unit's output, or the partial of slot >= 0.
 template <int D, int NT, int RG, bool BF16>
 __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, int b, int g, int64_t slot, int rg,
                                         int lane) {
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2, c = lane & 3;
+  const Kv8Units<D, NT, RG> u(w);
+  const float unit = u.o;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -644,14 +817,14 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
+      l *= u.l;
       const int row = (rg * NT + nt) * 8 + 2 * c + i;
       if (row >= a.rows) continue;
-      const float unit = kv8_scale((uint32_t)w.e);
       if (slot < 0) {
         const int t = row / a.G;
         const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D;
         if (!idx_ok(at + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) continue;
-        const float f = l > 0.f ? 1.f / l : 0.f;
+        const float f = l > 0.f ? 1.f / l : l;      // (0, or NaN)
 #pragma unroll
         for (int j = 0; j < KD; ++j)
           Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at + 16 * j + 2 * r, w.acc[j][nt][i] * f * unit,
@@ -664,7 +837,7 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
           *reinterpret_cast<float2*>(a.ws_o + at * D + 16 * j + 2 * r) =
               make_float2(w.acc[j][nt][i] * unit, w.acc[j][nt][2 + i] * unit);
         if (r == 0) {
-          a.ws_m[at] = l == l ? w.m[nt][i] : 0.f;   // NaN scores move no maximum: not to be taken for an empty piece
+          a.ws_m[at] = l == l ? w.m[nt][i] + u.shift : 0.f;   // NaN scores move no maximum: not to be taken for an empty piece
           a.ws_l[at] = l;
         }
       }
@@ -743,7 +916,7 @@ gqa_decode_kv8_kernel(const Kv8Params a) {
     const int key0 = at.t * kKv8Keys;
     const int valid = min(len - key0, kKv8Keys);
     const int sees = a.causal ? len - a.T_q : len - 1;       // the fewest keys that a row sees
-    kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, valid, key0, kKv8Keys - 1 > sees - key0, rg, lane, ring);
+    kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, valid, len - 1 - key0, kKv8Keys - 1 > sees - key0, rg, lane, ring);
     __syncwarp();
     if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
     if (rg == 0 && i + STAGES < n) {
@@ -789,7 +962,8 @@ template <int D, int NT, int RG>
 __device__ __forceinline__ void kv8_leave(Kv8Warp<D, NT, RG>& w, float2* ml, float* o, int lane) {
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2, c = lane & 3;
-  const float unit = kv8_scale((uint32_t)w.e);
+  const Kv8Units<D, NT, RG> u(w);
+  const float unit = u.o;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -798,8 +972,9 @@ __device__ __forceinline__ void kv8_leave(Kv8Warp<D, NT, RG>& w, float2* ml, flo
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
+      l *= u.l;
       const int row = nt * 8 + 2 * c + i;
-      if (r == 0) ml[row] = make_float2(w.m[nt][i], l);
+      if (r == 0) ml[row] = make_float2(w.m[nt][i] + u.shift, l);
 #pragma unroll
       for (int j = 0; j < KD; ++j)
         *reinterpret_cast<float2*>(o + row * D + 16 * j + 2 * r) =
@@ -839,7 +1014,7 @@ __device__ __forceinline__ void kv8_store4(const Kv8Params& a, int b, int g, int
   const int t = row / a.G;
   const int64_t at = (((int64_t)b * a.T_q + t) * a.h_q + (int64_t)g * a.G + (row - t * a.G)) * D + d;
   if (!idx_ok(at + 3, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
-  const float f = l > 0.f ? 1.f / l : 0.f;
+  const float f = l > 0.f ? 1.f / l : l;
   Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at, v.x * f, v.y * f);
   Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), at + 2, v.z * f, v.w * f);
 }
@@ -928,7 +1103,7 @@ gqa_decode_kv8_short_kernel(const Kv8Params a) {
       good = ptx::mbar_wait_bounded(full + stage * 8, phase, a.timeout_ns, flags);
       if (!good) break;
       const int key0 = (t0 + i) * kKv8Keys;
-      kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, min(len - key0, kKv8Keys), key0,
+      kv8_tile<D, NT, RG, !BF16>(w, a, ring0 + stage * C::TILE, eb, min(len - key0, kKv8Keys), len - 1 - key0,
                                  kKv8Keys - 1 > sees - key0, rg, lane, ring);
       __syncwarp();
       if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
@@ -1121,7 +1296,7 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
       for (int i = 0; i < PER; ++i) acc[i] += g * sm[k][lane * PER + i];
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L > 0.f ? 1.f / L : L;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
     Elem<BF16>::store2(reinterpret_cast<__half*>(a.o), out + col + i, acc[i] * inv, acc[i + 1] * inv);
