@@ -45,6 +45,8 @@ constexpr float kKv8Slack = 4.f;
 constexpr int kKv8Lift = 11;                   // P in f16 is the weight times 2^this: at most 2^15
 constexpr int kKv8Spread = 10;                 // V exponents further apart than this: the wide form
 constexpr int kKv8Wide = 1024;                 // Kv8Warp::lo of a worker that has gone over to it, above every exponent
+constexpr int kKv8ByToken = 1025;              // the same, and a row is not to meet the values that it does not see
+constexpr int kKv8ToToken = 1026;              // that, from the next products on
 constexpr int kKv8WideUnit = 16;               // log2 of the unit of its O: sums of many values of 448 * 2^120 fit
 
 struct Kv8Params {
@@ -448,21 +450,38 @@ struct Kv8WideTile {
   int ev[4];                // and their V exponents
   uint32_t v[2], turn;      // this lane's rows of V for ldmatrix, and its chunk swizzle
   Win ring;
+  // tokens > 0: the rows of each of so many query tokens by themselves, with only the values that the token sees.
+  // last: the last key of the newest one, row0: this lane's first row, G: rows of a token
+  int tokens, last, row0, G;
 };
 
 template <int D, int NT, bool FINE>
 __device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
   constexpr int KD = D / 16, kUp = 14;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  int token = w.tokens - 1, lim = w.tokens > 0 ? w.last : kKv8Keys - 1;   // the last key of this pass
 #pragma unroll 1
   for (int hi = 255;;) {
     int top = 0;       // this range: exponents top - kKv8Spread .. top
 #pragma unroll
     for (int o = 0; o < 4; ++o)
-      if (w.ev[o] <= hi) top = max(top, w.ev[o]);
+      if (w.ev[o] <= hi && 8 * o + r <= lim) top = max(top, w.ev[o]);
     top = __reduce_max_sync(0xffffffffu, top);
-    if (top == 0) return;
+    if (top == 0) {    // no more keys; an older token sees one key less
+      if (--token < 0 || --lim < 0) return;
+      hi = 255;
+      continue;
+    }
     hi = top - kKv8Spread - 1;
     const float back = kv8_ratio(top - 127 - kUp - kKv8WideUnit);
+    uint32_t keep[2][2];   // bytes of the pairs of keys 16p + 8i + 2c, + 1
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = 16 * p + 8 * i + 2 * c;
+        keep[p][i] = (key <= lim ? 0x00ff00ffu : 0u) | (key < lim ? 0xff00ff00u : 0u);
+      }
 #pragma unroll 1
     for (int nt = 0; nt < NT; ++nt) {
       float2 x[4];
@@ -475,6 +494,7 @@ __device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
         m[1] = fmaxf(m[1], x[o].y);
       }
       float up[2], base[2];
+      bool mine[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 4));
@@ -482,6 +502,8 @@ __device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
         m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
         base[i] = m[i] == -CUDART_INF_F ? 0.f : m[i];
         up[i] = ptx::ex2(base[i]);
+        // a row without keys in this range meets none of its NaN
+        mine[i] = m[i] != -CUDART_INF_F && (w.tokens == 0 || (w.row0 + 8 * nt + i) / w.G == token);
       }
       uint32_t pf[2][2], pl[2][2];
 #pragma unroll
@@ -505,7 +527,7 @@ __device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
                                                w.ring.status));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            kv8_unpack(__byte_perm(v[i], 0, 0x3120), f[i >> 1][(i & 1) * 2], f[i >> 1][(i & 1) * 2 + 1]);
+            kv8_unpack(__byte_perm(v[i], 0, 0x3120) & keep[p][i & 1], f[i >> 1][(i & 1) * 2], f[i >> 1][(i & 1) * 2 + 1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             kv8_mma(sum[k], f[k], pf[p]);
@@ -515,11 +537,28 @@ __device__ __noinline__ void kv8_wide(Kv8WideTile<D, NT>& w) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)      // (a row without keys in this range meets none of its NaN)
-            if (m[i & 1] != -CUDART_INF_F) w.acc[j + k][nt][i] = fmaf(sum[k][i] * up[i & 1], back, w.acc[j + k][nt][i]);
+          for (int i = 0; i < 4; ++i)
+            if (mine[i & 1]) w.acc[j + k][nt][i] = fmaf(sum[k][i] * up[i & 1], back, w.acc[j + k][nt][i]);
       }
     }
   }
+}
+
+// Whether a value of the keys first .. valid - 1 is NaN: some token does not see them, and a weight of 0 is not enough.
+template <int D>
+__device__ __noinline__ bool kv8_hidden_nan(uint32_t st, int eb, int first, int valid, const Win& ring) {
+  bool nan = false;
+  for (int i = threadIdx.x & 31; i < (valid - first) * (D / 16); i += 32) {
+    const int key = first + i / (D / 16);
+    const uint32_t at = st + key / eb * kv8_block_bytes(eb, D) + (eb + key % eb) * D + i % (D / 16) * 16;
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(smem_clamp(at, 16, ring.lo, ring.hi, ring.status)));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) nan |= __vcmpeq4(v[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+  }
+  return __any_sync(0xffffffffu, nan);
 }
 
 // One tile of `valid` keys, `st` its place in the ring; last: the sequence's last key, counted from the tile's first;
@@ -533,9 +572,12 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
   using W = Kv8Warp<D, NT, RG>;
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2;
-  if (valid < kKv8Keys) {
-    // V rows that hold no key: zeros, so that a weight of 0 meets no NaN, and the exponent of the first key, which spreads
-    // nothing.  Then the writes are ordered before the next copy into this place.
+  if (masked) {
+    if (a.causal && a.T_q > 1 && kv8_hidden_nan<D>(st, eb, max(last - (a.T_q - 1) + 1, 0), valid, ring))
+      w.lo = w.lo < kKv8Wide ? kKv8ToToken : kKv8ByToken;
+    // V rows that hold no key (there are some in every last tile that is not full): zeros, so that a weight of 0 meets no
+    // NaN, and the exponent of the first key, which spreads nothing.  Then the writes are ordered before the next copy
+    // into this place.
     for (int i = lane; i < (kKv8Keys - valid) * KD; i += 32) {
       const int key = valid + i / KD;
       const uint32_t to = st + key / eb * kv8_block_bytes(eb, D) + (eb + key % eb) * D + i % KD * 16;
@@ -654,7 +696,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
   bool wide = false;
   if (__any_sync(0xffffffffu, over)) {
     float fe = 1.f;
-    if (w.lo != kKv8Wide) {
+    if (w.lo < kKv8Wide || w.lo == kKv8ToToken) {
       int top = w.e, low = w.lo;
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
@@ -663,7 +705,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       }
       top = __reduce_max_sync(0xffffffffu, top);
       low = __reduce_min_sync(0xffffffffu, low);
-      if (top - low > kKv8Spread) {
+      if (top - low > kKv8Spread || w.lo == kKv8ToToken) {
         const float f = kv8_ratio(w.e - 127 - kKv8Lift - kKv8WideUnit);
 #pragma unroll
         for (int j = 0; j < KD; ++j)
@@ -671,14 +713,14 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f;
-        w.lo = kKv8Wide;
+        w.lo = w.lo == kKv8ToToken ? kKv8ByToken : kKv8Wide;
       } else {
         fe = kv8_ratio(w.e - top);
         w.e = top;
         w.lo = low;
       }
     }
-    wide = w.lo == kKv8Wide;
+    wide = w.lo >= kKv8Wide;
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -728,6 +770,10 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     for (int p = 0; p < 2; ++p) t.v[p] = st + w.rows[p] + eb * D;
     t.turn = w.turn;
     t.ring = ring;
+    t.tokens = w.lo == kKv8ByToken ? a.T_q : 0;
+    t.last = last;
+    t.row0 = rg * NT * 8 + 2 * (lane & 3);
+    t.G = a.G;
 #pragma unroll
     for (int j = 0; j < KD; ++j)
 #pragma unroll
@@ -794,7 +840,7 @@ template <int D, int NT, int RG>
 struct Kv8Units {
   float shift, l, o;
   __device__ __forceinline__ explicit Kv8Units(const Kv8Warp<D, NT, RG>& w) {
-    const bool wide = w.lo == kKv8Wide;
+    const bool wide = w.lo >= kKv8Wide;
     shift = wide ? (float)kKv8WideUnit : -(float)kKv8Lift;
     l = wide ? 1.f / (float)(1ull << kKv8WideUnit) : (float)(1 << kKv8Lift);
     o = wide ? 1.f : kv8_scale((uint32_t)w.e);

@@ -193,3 +193,28 @@ def test_scales_of_any_order(gqa, elem):
                         rng.integers(-8, 8, (n, hk)), 60, 125)
         q = torch.randn(1, 1, hq * D, generator=gen(14)) * 3
         check(gqa, *rows_to_cache(k, ke, v, ve, bs, 15, room), n, q, hq, hk, D, bs, elem)
+
+
+@pytest.mark.parametrize("elem", ["f16", "bf16"])
+@pytest.mark.parametrize("D,hq,hk,T", [(128, 2, 1, 4), (64, 8, 2, 2), (128, 8, 1, 3), (64, 2, 1, 8), (128, 8, 1, 4),
+                                       (64, 4, 1, 16), (128, 6, 1, 7), (64, 1, 1, 40)])
+def test_not_a_number_that_the_causal_tail_hides(gqa, D, hq, hk, T, elem):
+    """NaN in values of the newest tokens: it spoils its column for the tokens that see it, and for no other."""
+    for bs in (8, 64):
+        for n in (5000, 33, 64, T + 1, max(T - 2, 2)):        # the tail in one tile or two, or longer than the sequence
+            for room in (0, 4000):
+                k, ke, v, ve = keys(n, hk, D, n + T)
+                for back, col in ((1, 5), (2, 40), (min(T, n) // 2 + 1, 11), (min(T + 3, n), 23)):
+                    v[n - back, 0, col] = 0x7F if back % 2 else 0xFF
+                if n > 100:
+                    ve[n - 1] += 20
+                    ve[n // 2] -= 3
+                cache, tab = rows_to_cache(k, ke, v, ve, bs, 16, room)
+                q = torch.randn(1, T, hq * D, generator=gen(17)).to(DT[elem])
+                o = gqa.gqa_decode_kv8(q.cuda(), dev(cache), dev(tab), torch.tensor([n], dtype=torch.int32).cuda(), hq,
+                                       hk, causal=True).double().cpu()
+                ref, a, _, _ = ko.decode_kv8(npy(q), cache, tab, [n], hq, hk, D, D ** -0.5, bs, True)
+                where = f"{bs} {n} {room}"
+                assert torch.equal(o.isnan(), ref.isnan()), where
+                err, tol = (o - ref).abs(), U[elem] * ref.abs() + 4 * 2.0 ** -11 * a + TINY[elem]
+                assert not (err > tol).any(), where
