@@ -52,7 +52,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
         [os.path.join(ROOT, "include", "gqa_decode.h"), os.path.abspath(__file__)]
 
 

@@ -31,6 +31,7 @@
 #pragma once
 #include "gqa_kv8.cuh"
 #include "gqa_merge.cuh"   // kMergeThreads, kMergeChunk
+#include "kv8_notes.h"
 
 namespace gqa {
 
@@ -55,7 +56,7 @@ struct Kv8Params {
   const uint8_t* cache;
   const int32_t *block_tables, *seq_lens;
   uint32_t* status;
-  int4* splits;          // the units that are cut, for the merge (Kv8Pieces); [workers], sliced: [units]
+  int4* splits;          // the units that are cut, for the merge (Kv8Note); [workers], sliced: [units]
   float *ws_m, *ws_l;    // [2 * workers][rows]   m in log2 units
   float* ws_o;           // [2 * workers][rows][D]
   int N, T_q, h_q, h_kv, G, rows, max_blocks, num_blocks, block_size, bs_log, causal, workers, stall;
@@ -1219,16 +1220,6 @@ gqa_decode_kv8_short_kernel(const Kv8Params a) {
   ptx::cluster_sync();       // no CTA leaves while another reads its shared memory
 }
 
-// The pieces of a unit that more than one worker streamed: n of them (0: the unit is not cut), of neighbouring workers;
-// the first one's slot is `first`, the others have the first slots of the workers after it.
-struct Kv8Pieces {
-  int n, first, row;
-};
-
-__device__ __forceinline__ int64_t kv8_slot_row(const Kv8Params& a, const Kv8Pieces& p, int s) {
-  return (int64_t)(s == 0 ? p.first : (p.first & ~1) + 2 * s) * a.rows + p.row;
-}
-
 // Folds the pieces of every unit that more than one worker streamed, in the order of its keys.
 // SLICED = false, for batches whose units have a few pieces each: a warp for each worker's range (whose first cut
 // unit the worker has noted: no search, no division) and row, all D columns.
@@ -1245,39 +1236,36 @@ gqa_kv8_merge_kernel(const Kv8Params a) {
   if (threadIdx.x == 0) ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Kv8Pieces pc;
-  int4 unit;     // pieces, first slot, sequence, head
-  int col = lane % LANES * PER;
+  int4 noted;    // pieces, first slot, sequence, head
+  int row, col = lane % LANES * PER;
   if constexpr (SLICED) {
     const uint32_t r = blockIdx.x / (D / 32), u = r / (uint32_t)a.rows;
     col += (int)(blockIdx.x % (D / 32)) * 32;
-    unit = __ldcg(a.splits + u);
-    unit.z = (int)(u / (uint32_t)a.h_kv);
-    unit.w = (int)(u - (uint32_t)unit.z * (uint32_t)a.h_kv);
-    pc.row = (int)(r - u * (uint32_t)a.rows);
-    // a worker whose wait gave up has not noted the units behind that tile: what lies there then may be anything
-    if ((uint32_t)unit.y >= 2u * (uint32_t)a.workers || unit.x > a.workers - (unit.y >> 1)) return;
+    noted = __ldcg(a.splits + u);
+    noted.z = (int)(u / (uint32_t)a.h_kv);
+    noted.w = (int)(u - (uint32_t)noted.z * (uint32_t)a.h_kv);
+    row = (int)(r - u * (uint32_t)a.rows);
   } else {
     const uint32_t i = blockIdx.x * WARPS + warp, w = i / (uint32_t)a.rows;
     if (w >= (uint32_t)a.workers) return;
-    unit = __ldcg(a.splits + w);
-    pc.row = (int)(i - w * (uint32_t)a.rows);
+    noted = __ldcg(a.splits + w);
+    row = (int)(i - w * (uint32_t)a.rows);
   }
-  pc.n = unit.x;
-  pc.first = unit.y;
-  const int t = pc.row / a.G;
-  const int64_t out = (((int64_t)unit.z * a.T_q + t) * a.h_q + (int64_t)unit.w * a.G + (pc.row - t * a.G)) * D;
-  if (pc.n < 2 || !idx_ok(out + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
+  const Kv8Note unit = {noted.x, noted.y, noted.z, noted.w};
+  if (!kv8_note_ok(unit, a.workers, a.N, a.h_kv)) return;
+  const int t = row / a.G;
+  const int64_t out = (((int64_t)unit.b * a.T_q + t) * a.h_q + (int64_t)unit.g * a.G + (row - t * a.G)) * D;
+  if (!idx_ok(out + D - 1, (int64_t)a.N * a.T_q * a.h_q * D, a.status)) return;
   float M = -CUDART_INF_F, L = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  for (int s0 = SLICED ? warp * SUBS + lane / LANES : 0; s0 < pc.n; s0 += LOADS * STEP) {
+  for (int s0 = SLICED ? warp * SUBS + lane / LANES : 0; s0 < unit.pieces; s0 += LOADS * STEP) {
     float mj[LOADS], lj[LOADS], oj[LOADS][PER];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       const int s = s0 + j * STEP;
-      const int64_t at = kv8_slot_row(a, pc, s);
-      const bool have = s < pc.n && idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status);
+      const int64_t at = (int64_t)kv8_slot(unit, s) * a.rows + row;
+      const bool have = s < unit.pieces && idx_ok(at, 2 * (int64_t)a.workers * a.rows, a.status);
       mj[j] = have ? __ldcg(a.ws_m + at) : -CUDART_INF_F;
       lj[j] = have ? __ldcg(a.ws_l + at) : 0.f;
       const float* src = a.ws_o + at * D + col;
