@@ -30,6 +30,12 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 Kv8Device g_kv8[kMaxDevices];
 
+// The launches of one decode call hand partials on through its workspace, so that no other call's launches on it may come
+// between them: host threads that share a stream and its workspace take turns.
+constexpr int kTurns = 64;
+std::mutex g_turn[kTurns];
+std::mutex& turn_of(const void* ws) { return g_turn[(reinterpret_cast<uintptr_t>(ws) >> 8) % kTurns]; }
+
 // SMs of the current device, with g_mu held by the caller
 gqa_status device_locked(Kv8Device** out) {
   int dev = 0;
@@ -304,6 +310,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   p.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t seq_tiles = ((int64_t)max_blocks * block_size + kKv8Keys - 1) / kKv8Keys;
+  std::lock_guard<std::mutex> turn(turn_of(ws));
   for (int b0 = 0; b0 < N; b0 += kKv8Seqs) {
     p.N = N - b0 < kKv8Seqs ? N - b0 : kKv8Seqs;
     p.q = q + (int64_t)b0 * T_q * h_q * D;
