@@ -159,6 +159,7 @@ PyObject* append(PyObject* const* p) {
     a.rot_dim = as_int(cs->size(1), "rot_dim");
     a.cos_sin = whole<float>(*cs, "cos_sin", at::kFloat, dev, {cs->size(0), cs->size(1)});
     a.positions = whole<int32_t>(*pos, "positions", at::kInt, dev, {T});
+    if (T == 0) a.positions = reinterpret_cast<const int32_t*>(a.cos_sin);   // (an empty tensor has no address; none is read)
   }
   a.interleaved = truth(p[10]);
   if (const at::Tensor* w = optional(p[11], "q_weight")) a.q_weight = whole<uint16_t>(*w, "q_weight", type, dev, {D});

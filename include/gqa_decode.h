@@ -324,7 +324,7 @@ typedef struct {
   const uint16_t* q_weight; /* (d_head) weight of the norm of every query head, NULL = no norm */
   const uint16_t* k_weight; /* the same for the key heads */
   const float* cos_sin;     /* (max_position, rot_dim): rot_dim/2 cosines, then rot_dim/2 sines; NULL = no rotation */
-  const int32_t* positions; /* (num_tokens) row of cos_sin of each token; not read without cos_sin */
+  const int32_t* positions; /* (num_tokens) row of cos_sin of each token; not read without cos_sin, not NULL with it */
   const int64_t* slots;     /* (num_tokens) block * block_size + row; negative: the token's K and V are not stored */
   void* k_cache;            /* the pool of cache_layout (kv8: the one array) */
   void* v_cache;            /* NULL for kv8 */

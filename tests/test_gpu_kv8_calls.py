@@ -75,3 +75,24 @@ def test_threads_on_one_stream(gqa):
     for t in threads:
         t.join()
     assert sorted(bad) == [(i, 0) for i in range(len(cases))]
+
+
+# ---------------------------------------------------------------- calls without tokens
+@pytest.mark.parametrize("layout", ["rows", "vllm", "kv8"])
+def test_append_of_no_tokens(gqa, layout):
+    """An empty call with norms and rotation is a no-op, as one without them."""
+    D, hq, hk, bs = 128, 8, 2, 16
+    x = torch.zeros(0, (hq + 2 * hk) * D, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    shapes = {"rows": [(4, bs, hk * D)] * 2, "vllm": [(4, hk, D // 8, bs, 8), (4, hk, D, bs)], "kv8": []}[layout]
+    caches = [torch.full(s, 3.0, dtype=torch.bfloat16, device="cuda") for s in shapes] or \
+        [torch.full((4, hk, bs * (2 * D + 2)), 9, dtype=torch.uint8, device="cuda")]
+    before = [c.clone() for c in caches]
+    none = dict(positions=torch.zeros(0, dtype=torch.int32, device="cuda"), cos_sin=torch.zeros(16, D, device="cuda"),
+                q_weight=w, k_weight=w)
+    for kw in ({}, none, dict(none, interleaved=True)):
+        for q in (x[:, :hq * D], None):
+            out = gqa.gqa_append(q, x[:, hq * D:(hq + hk) * D], x[:, (hq + hk) * D:], hq, hk,
+                                 torch.zeros(0, dtype=torch.int64, device="cuda"), *caches, **kw)
+            assert out is None if q is None else out.shape == (0, hq * D)
+    assert all(torch.equal(a, b) for a, b in zip(caches, before))
