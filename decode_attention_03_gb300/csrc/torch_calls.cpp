@@ -56,7 +56,14 @@ double real(PyObject* o, const char* name) {
   return v;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(name, "true or false");
+  }
+  return v == 1;
+}
 
 bool is_half(const at::Tensor& t) { return t.scalar_type() == at::kHalf || t.scalar_type() == at::kBFloat16; }
 
@@ -161,7 +168,7 @@ PyObject* append(PyObject* const* p) {
     a.positions = whole<int32_t>(*pos, "positions", at::kInt, dev, {T});
     if (T == 0) a.positions = reinterpret_cast<const int32_t*>(a.cos_sin);   // (an empty tensor has no address; none is read)
   }
-  a.interleaved = truth(p[10]);
+  a.interleaved = truth(p[10], "interleaved");
   if (const at::Tensor* w = optional(p[11], "q_weight")) a.q_weight = whole<uint16_t>(*w, "q_weight", type, dev, {D});
   if (const at::Tensor* w = optional(p[12], "k_weight")) a.k_weight = whole<uint16_t>(*w, "k_weight", type, dev, {D});
   a.eps = (float)real(p[13], "eps");
@@ -233,7 +240,7 @@ PyObject* decode(PyObject* const* p) {
   if (limit < 0 || limit > UINT32_MAX) refuse("timeout_us", "a number of microseconds in 32 bits");
   opt.timeout_us = (uint32_t)limit;
   opt.test_stall_cta = small(p[11], "test_stall_cta");
-  opt.causal = truth(p[7]);
+  opt.causal = truth(p[7], "causal");
   opt.bf16 = q.scalar_type() == at::kBFloat16;
   const Workspace ws = workspace(tensor(p[9], "workspace_tensor"), dev);
   void* st = stream_of(dev);

@@ -96,3 +96,21 @@ def test_append_of_no_tokens(gqa, layout):
                                  torch.zeros(0, dtype=torch.int64, device="cuda"), *caches, **kw)
             assert out is None if q is None else out.shape == (0, hq * D)
     assert all(torch.equal(a, b) for a, b in zip(caches, before))
+
+
+# ---------------------------------------------------------------- arguments
+def test_flags_that_are_neither_true_nor_false(gqa):
+    """Refused before anything is launched."""
+    D, hq, hk, bs = 64, 8, 2, 16
+    x = torch.randn(3, (hq + 2 * hk) * D, generator=gen(1)).half().cuda()
+    cache = gqa.gqa_kv8_cache(2, bs, hk, D)
+    pos, cs = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.ones(4, D, device="cuda")
+    slots = torch.arange(3, device="cuda")
+    for flag in (torch.zeros(2), np.zeros(3)):
+        with pytest.raises(ValueError, match="interleaved"):
+            gqa.gqa_append(None, x[:, :hk * D], x[:, :hk * D], hq, hk, slots, cache, positions=pos, cos_sin=cs,
+                           interleaved=flag)
+        with pytest.raises(ValueError, match="causal"):
+            gqa.gqa_decode_kv8(x[:, :hq * D].contiguous(), cache, slots.int().view(3, 1), pos, hq, hk, causal=flag)
+    torch.cuda.synchronize()
+    assert (cache == 0).all()
