@@ -18,7 +18,7 @@ _BINDING_NAMES = (
     "gqa_decode", "gqa_decode_noalloc", "gqa_decode_noalloc_check", "gqa_decode_partial", "gqa_merge", "gqa_merge_partial", "gqa_decode_paged",
     "gqa_decode_paged_vllm",
     "gqa_append", "gqa_decode_kv8", "gqa_kv8_read", "gqa_kv8_cache", "gqa_kv8_block_bytes",
-    "gqa_decode_kv8_workspace_size", "gqa_append_args", "GQA_CACHE_ROWS", "GQA_CACHE_VLLM", "GQA_CACHE_KV8",
+    "gqa_decode_kv8_workspace_size", "gqa_status_check", "gqa_append_args", "GQA_CACHE_ROWS", "GQA_CACHE_VLLM", "GQA_CACHE_KV8",
     "gqa_decode_workspace_size", "gqa_workspace_size", "gqa_paged_workspace_size", "gqa_decode_num_splits",
     "gqa_decode_plan", "gqa_paged_plan",
     "gqa_workspace_init", "gqa_workspace_check", "gqa_status_string", "gqa_version",

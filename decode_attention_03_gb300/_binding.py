@@ -101,6 +101,8 @@ _SIGS = {
     "gqa_append": ([ctypes.POINTER(gqa_append_args), _p, _sz, _p], _i),
     "gqa_decode_kv8_workspace_size": ([_i, _i, _i, _i, _i], _sz),
     "gqa_decode_kv8": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _p, _opt], _i),
+    "gqa_decode_kv8_status": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _p, _p, _opt], _i),
+    "gqa_device_status": ([], _p),
     "gqa_kv8_read": ([_p, _p, _p, _p, _p, _p, _i, _i64, _i, _i, _i, _i, _i, _p, _sz, _p, _opt], _i),
     "gqa_decode_paged_vllm_ex": ([_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p,
                                   _opt], _i),
@@ -481,16 +483,31 @@ def _place(t: torch.Tensor, name: str) -> Tuple[int, int]:
     return dev, _raw_stream(dev)
 
 
-def _status_workspace(t: torch.Tensor, name: str) -> torch.Tensor:
-    """A workspace for calls that need its status word alone, ``workspace(256, use="status")`` of the stream.  It never
-    grows, so a graph that was captured with it may be replayed at any time (the kernels only set bits in it)."""
+def _status_workspace(t: torch.Tensor, name: str) -> Optional[torch.Tensor]:
+    """The status word of calls without a workspace, ``workspace(256, use="status")`` of the stream.  It never grows, so a
+    graph that was captured with it may be replayed at any time (the kernels only set bits in it).  None, the library's own
+    status word of the device, for a call that is captured on a stream that has none yet."""
     dev, raw = _place(t, name)
     ws = _ws_cache.get((dev, raw, "status"))
-    if ws is not None:
+    if ws is not None or _capturing():
         return ws
-    if _capturing():
-        return torch.zeros(256, dtype=torch.uint8, device=t.device)
     return workspace(256, t.device, use="status")
+
+
+def gqa_status_check(device=None) -> int:
+    """Status of the calls of gqa_append, gqa_decode_kv8 and gqa_kv8_read without a ``workspace_tensor`` on a device (the
+    current one), of all streams, eager and replayed, since the last check; synchronises the device and clears it."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        torch.cuda.synchronize()
+        index = torch.cuda.current_device()
+        with _ws_lock:
+            words = [t.data_ptr() for key, t in _ws_cache.items() if key[0] == index and key[2:] in (("status",), ("kv8",))]
+        own = lib.gqa_device_status()
+        if own is None:
+            return GQA_ERR_CUDA
+        seen = [lib.gqa_workspace_check(ctypes.c_void_p(at), _stream(None)) for at in words + [own]]
+    return next((s for s in (GQA_ERR_CUDA, GQA_ERR_BOUNDS, GQA_ERR_TIMEOUT, GQA_ERR_INVALID_ARG) if s in seen), GQA_OK)
 
 
 def gqa_kv8_block_bytes(block_size: int, d_head: int) -> int:
@@ -522,7 +539,7 @@ def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q:
     The cache: ``k_cache, v_cache`` of gqa_decode_paged (num_blocks, block_size, h_kv*D) or of
     gqa_decode_paged_vllm, or one 8-bit cache (gqa_kv8_cache), quantised as it is written.
     Returns the queries after norm and rotation (``q_out``, which may be q itself).  What the kernel reports is in the
-    status word of ``workspace_tensor``, or of ``workspace(256, use="status")``."""
+    status word of ``workspace_tensor``; without one, gqa_status_check has it, for captured calls too."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions=positions, cos_sin=cos_sin,
@@ -557,23 +574,25 @@ def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Ten
     ``causal``: query token t sees keys j <= len - T_q + t only.
 
     Without ``workspace_tensor`` the stream's cached workspace of this call is used; a call that is being captured into
-    a graph gets one of its own, so that graphs may be replayed side by side."""
+    a graph gets one of its own, so that graphs may be replayed side by side.  What such calls report, gqa_status_check has."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_decode_kv8(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal=causal, out=out,
                                   workspace_tensor=workspace_tensor, timeout_us=timeout_us,
                                   test_stall_cta=test_stall_cta)
-    ws = workspace_tensor
+    ws = status = workspace_tensor
     if ws is None:
         dev, raw = _place(q, "q")
         if _capturing():
+            status = _ws_cache.get((dev, raw, "status"))
             ws = torch.empty(_kv8_workspace_bytes(q, h_q, h_kv), dtype=torch.uint8, device=q.device)
-            ws[:256].zero_()
         else:
             ws = _ws_cache.get((dev, raw, "kv8"))
             if ws is None:
                 ws = workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")
-    r = _calls.decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, timeout_us, test_stall_cta)
+            status = ws
+    r = _calls.decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, status, timeout_us,
+                      test_stall_cta)
     if r.__class__ is int:
         if r == GQA_ERR_WORKSPACE and workspace_tensor is None and ws.numel() < _kv8_workspace_bytes(q, h_q, h_kv):
             workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")       # the cached one grows
@@ -591,7 +610,7 @@ def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torc
     """Tokens [begins[b], min(begins[b] + out_len, seq_lens[b])) of every sequence of an 8-bit cache as 16-bit
     K and V (N, out_len, h_kv*D), the layout of gqa_decode.  Into ``k_out`` / ``v_out`` (the one left out is
     not read; rows past a sequence's last token stay as they were), or, with neither, into zeros of ``dtype``
-    (float16) and ``out_len`` tokens.  begins (N) int32, default 0."""
+    (float16) and ``out_len`` tokens.  begins (N) int32, default 0.  Reports as those of gqa_append."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_kv8_read(cache, block_tables, seq_lens, d_head, out_len, begins=begins, dtype=dtype,

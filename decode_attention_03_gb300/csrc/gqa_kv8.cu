@@ -24,9 +24,11 @@ gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_E
 // ---------------------------------------------------------------- per-device state
 struct Kv8Device {
   int sms = 0;
+  void* status = nullptr;     // g_status on this device
   bool ready[2][6][2] = {};   // [d index][row class][bf16]: the kernel's shared memory is allowed
 };
 constexpr int kMaxDevices = 64;
+__device__ __align__(256) unsigned char g_status[kHeaderBytes];   // the library's own status word, zero from the start
 std::mutex g_mu;
 Kv8Device g_kv8[kMaxDevices];
 
@@ -47,6 +49,22 @@ gqa_status device_locked(Kv8Device** out) {
   }
   *out = &d;
   return GQA_OK;
+}
+
+// Address of the current device's g_status.  The lookup is no work on a stream, but may load the module: allowed while this
+// thread captures a graph.
+void* device_status() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  Kv8Device* d = nullptr;
+  if (device_locked(&d) != GQA_OK) return nullptr;
+  if (d->status == nullptr) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_status) == cudaSuccess) d->status = p;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+  }
+  return d->status;
 }
 
 // ---------------------------------------------------------------- append
@@ -275,7 +293,7 @@ cudaError_t kv8_decode(const Kv8Params& p, int cls, unsigned grid, bool cut, boo
 
 gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* tables, const int32_t* lens,
                            uint16_t* o, int N, int T_q, int max_blocks, int num_blocks, int block_size, int h_q,
-                           int h_kv, int D, float scale, void* ws, size_t ws_bytes, void* stream,
+                           int h_kv, int D, float scale, void* ws, size_t ws_bytes, void* status, void* stream,
                            const gqa_options* opt_in) {
   const gqa_options opt = opt_in ? *opt_in : gqa_default_options();
   gqa_status s = check_rows(N, T_q, h_q, h_kv, D);
@@ -284,8 +302,8 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   if (!std::isfinite(scale)) return GQA_ERR_INVALID_ARG;
   if ((int64_t)(N < kKv8Seqs ? N : kKv8Seqs) * T_q * h_q >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
   if (N == 0) return GQA_OK;
-  if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(ws) || !aligned_to(tables, 4) ||
-      !aligned_to(lens, 4))
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(ws) || !aligned16(status) ||
+      !aligned_to(tables, 4) || !aligned_to(lens, 4))
     return GQA_ERR_INVALID_ARG;
   if (ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
   const int rows = h_q / h_kv * T_q, cls = kv8_class(rows), bf16 = opt.bf16 ? 1 : 0;
@@ -296,7 +314,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   Kv8Params p = {};
   p.cache = static_cast<const uint8_t*>(cache);
-  p.status = reinterpret_cast<uint32_t*>(wsb);
+  p.status = static_cast<uint32_t*>(status);
   p.splits = reinterpret_cast<int4*>(wsb + lay.splits);
   p.ws_m = reinterpret_cast<float*>(wsb + lay.m);
   p.ws_l = reinterpret_cast<float*>(wsb + lay.l);
@@ -416,9 +434,29 @@ gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* b
                           const gqa_options* opt) {
   try {
     return decode_kv8_impl(q, cache, block_tables, seq_lens, o, num_seqs, T_q, max_blocks_per_seq, num_blocks,
-                           block_size, h_q, h_kv, d_head, scale, workspace, ws_bytes, stream, opt);
+                           block_size, h_q, h_kv, d_head, scale, workspace, ws_bytes, workspace, stream, opt);
   } catch (...) {
     return GQA_ERR_CUDA;
+  }
+}
+
+gqa_status gqa_decode_kv8_status(const uint16_t* q, const void* cache, const int32_t* block_tables,
+                                 const int32_t* seq_lens, uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq,
+                                 int num_blocks, int block_size, int h_q, int h_kv, int d_head, float scale,
+                                 void* workspace, size_t ws_bytes, void* status, void* stream, const gqa_options* opt) {
+  try {
+    return decode_kv8_impl(q, cache, block_tables, seq_lens, o, num_seqs, T_q, max_blocks_per_seq, num_blocks,
+                           block_size, h_q, h_kv, d_head, scale, workspace, ws_bytes, status, stream, opt);
+  } catch (...) {
+    return GQA_ERR_CUDA;
+  }
+}
+
+void* gqa_device_status(void) {
+  try {
+    return device_status();
+  } catch (...) {
+    return nullptr;
   }
 }
 

@@ -106,10 +106,17 @@ struct Workspace {
   size_t bytes;
 };
 
-Workspace workspace(const at::Tensor& t, int dev) {
+Workspace workspace(PyObject* o, int dev) {
+  const at::Tensor& t = tensor(o, "workspace_tensor");
   if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
     refuse("workspace_tensor", "a contiguous tensor on the device of the others");
   return {t.data_ptr(), (size_t)t.nbytes()};
+}
+
+// where a call reports: a workspace, or None, the library's own status word
+Workspace status_word(PyObject* o, int dev) {
+  if (o != Py_None) return workspace(o, dev);
+  return {gqa_device_status(), 256};
 }
 
 int32_t as_int(int64_t n, const char* name) {
@@ -130,7 +137,7 @@ int kv8_block_size(const at::Tensor& cache, int64_t h_kv, int64_t D, int dev) {
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
 // append(q|None, k, v, h_q, h_kv, slots, k_cache, v_cache|None, positions|None, cos_sin|None, interleaved, q_weight|None,
-//        k_weight|None, eps, q_out|None, workspace) -> q_out or None, or a status
+//        k_weight|None, eps, q_out|None, workspace|None) -> q_out or None, or a status
 PyObject* append(PyObject* const* p) {
   const at::Tensor *q = optional(p[0], "q"), &k = tensor(p[1], "k"), &v = tensor(p[2], "v");
   if (k.dim() != 2 || !is_half(k)) refuse("k", "a float16 or bfloat16 CUDA tensor (tokens, h_kv*d_head)");
@@ -197,7 +204,7 @@ PyObject* append(PyObject* const* p) {
     }
   }
   a.num_blocks = as_int(kc_t.size(0), "num_blocks");
-  const Workspace ws = workspace(tensor(p[15], "workspace_tensor"), dev);
+  const Workspace ws = status_word(p[15], dev);
   void* st = stream_of(dev);
   gqa_status s;
   Py_BEGIN_ALLOW_THREADS
@@ -209,8 +216,8 @@ PyObject* append(PyObject* const* p) {
   return THPVariable_Wrap(std::move(made));
 }
 
-// decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale|None, causal, out|None, workspace, timeout_us, stall) -> out, or a
-// status
+// decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale|None, causal, out|None, workspace, status|None, timeout_us, stall)
+// -> out, or a status
 PyObject* decode(PyObject* const* p) {
   const at::Tensor& q = tensor(p[0], "q");
   const int64_t dim = q.dim();
@@ -236,28 +243,29 @@ PyObject* decode(PyObject* const* p) {
     refuse("out", "like q");
   }
   gqa_options opt = {};
-  const int64_t limit = integer(p[10], "timeout_us");
+  const int64_t limit = integer(p[11], "timeout_us");
   if (limit < 0 || limit > UINT32_MAX) refuse("timeout_us", "a number of microseconds in 32 bits");
   opt.timeout_us = (uint32_t)limit;
-  opt.test_stall_cta = small(p[11], "test_stall_cta");
+  opt.test_stall_cta = small(p[12], "test_stall_cta");
   opt.causal = truth(p[7], "causal");
   opt.bf16 = q.scalar_type() == at::kBFloat16;
-  const Workspace ws = workspace(tensor(p[9], "workspace_tensor"), dev);
+  const Workspace ws = workspace(p[9], dev), status = status_word(p[10], dev);
+  if (status.bytes < 256) return PyLong_FromLong(GQA_ERR_WORKSPACE);
   void* st = stream_of(dev);
   const int n = as_int(N, "N"), t = as_int(T_q, "T_q"), blocks = as_int(mb, "max_blocks"),
             nb = as_int(cache.size(0), "num_blocks"), d = as_int(D, "d_head");
   gqa_status s;
   Py_BEGIN_ALLOW_THREADS
-  s = gqa_decode_kv8(static_cast<const uint16_t*>(q.data_ptr()), cache.data_ptr(), tp, lp,
-                     static_cast<uint16_t*>(out->data_ptr()), n, t, blocks, nb, bs, h_q, h_kv, d, scale, ws.at, ws.bytes,
-                     st, &opt);
+  s = gqa_decode_kv8_status(static_cast<const uint16_t*>(q.data_ptr()), cache.data_ptr(), tp, lp,
+                            static_cast<uint16_t*>(out->data_ptr()), n, t, blocks, nb, bs, h_q, h_kv, d, scale, ws.at,
+                            ws.bytes, status.at, st, &opt);
   Py_END_ALLOW_THREADS
   if (s != GQA_OK) return PyLong_FromLong(s);
   if (out != &made) return Py_NewRef(p[8]);
   return THPVariable_Wrap(std::move(made));
 }
 
-// read(cache, block_tables, seq_lens, d_head, begins|None, k_out|None, v_out|None, workspace) -> a status
+// read(cache, block_tables, seq_lens, d_head, begins|None, k_out|None, v_out|None, workspace|None) -> a status
 PyObject* read(PyObject* const* p) {
   const at::Tensor &cache = tensor(p[0], "cache"), &tables = tensor(p[1], "block_tables");
   const int dev = device_of(cache, "cache");
@@ -279,7 +287,7 @@ PyObject* read(PyObject* const* p) {
   gqa_options opt = {};
   opt.test_stall_cta = -1;
   opt.bf16 = type == at::kBFloat16;
-  const Workspace ws = workspace(tensor(p[7], "workspace_tensor"), dev);
+  const Workspace ws = status_word(p[7], dev);
   void* st = stream_of(dev);
   const int num = as_int(N, "N"), blocks = as_int(mb, "max_blocks"), nb = as_int(cache.size(0), "num_blocks"),
             heads = as_int(h_kv, "h_kv"), d = as_int(D, "d_head");
@@ -315,7 +323,7 @@ PyCFunction function() {
 }
 
 PyMethodDef kMethods[] = {{"append", function<append, 16>(), METH_FASTCALL, nullptr},
-                          {"decode", function<decode, 12>(), METH_FASTCALL, nullptr},
+                          {"decode", function<decode, 13>(), METH_FASTCALL, nullptr},
                           {"read", function<read, 8>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -372,6 +372,19 @@ gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* b
                           int h_q, int h_kv, int d_head, float scale, void* workspace, size_t ws_bytes, void* stream,
                           const gqa_options* opt);
 
+/* gqa_decode_kv8 that reports to `status` (256 zeroed bytes, any workspace of this library, or gqa_device_status)
+ * instead of to its workspace, which may then hold anything. */
+gqa_status gqa_decode_kv8_status(const uint16_t* q, const void* cache, const int32_t* block_tables,
+                                 const int32_t* seq_lens, uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq,
+                                 int num_blocks, int block_size, int h_q, int h_kv, int d_head, float scale,
+                                 void* workspace, size_t ws_bytes, void* status, void* stream, const gqa_options* opt);
+
+/* The library's own status word of the current device: 256 bytes of device memory, zero from the start and held until
+ * the process exits, for calls that outlive every workspace, as those captured into a graph may.  To be given as the
+ * workspace of gqa_append and gqa_kv8_read, the status of gqa_decode_kv8_status, and to gqa_workspace_check.  May be
+ * asked for during a capture.  NULL when no device is usable. */
+void* gqa_device_status(void);
+
 /* Tokens [begins[b], min(begins[b] + out_len, seq_lens[b])) of every sequence b as 16-bit values (the codes
  * times their scales, rounded to nearest even), in rows 0, 1, ... of
  *   k_out, v_out (num_seqs, out_len, h_kv*d_head)

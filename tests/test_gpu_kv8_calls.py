@@ -2,6 +2,7 @@
 arguments that are no numbers."""
 from __future__ import annotations
 
+import ctypes
 import threading
 
 import numpy as np
@@ -114,3 +115,135 @@ def test_flags_that_are_neither_true_nor_false(gqa):
             gqa.gqa_decode_kv8(x[:, :hq * D].contiguous(), cache, slots.int().view(3, 1), pos, hq, hk, causal=flag)
     torch.cuda.synchronize()
     assert (cache == 0).all()
+
+
+# ---------------------------------------------------------------- reports of calls without a workspace
+def step(gqa, slots, x, cache, tab, lens, q, hq, hk, D, **kw):
+    """One layer of a decode step: append, attention, and a look at the first tokens."""
+    gqa.gqa_append(None, x[:, :hk * D], x[:, hk * D:], hk, hk, slots, cache)
+    o = gqa.gqa_decode_kv8(q, cache, tab, lens, hq, hk, **kw)
+    return o, gqa.gqa_kv8_read(cache, tab, lens, D, 8)[0]
+
+
+def step_case(gqa, room=0, seed=400, lens=(900, 70, 3000)):
+    D, hq, hk, bs = 128, 8, 2, 16
+    cache, tab, ln = sequences(gqa, lens, hk, D, bs, seed, room)
+    x = torch.randn(len(lens), 2 * hk * D, generator=gen(seed + 2)).half().cuda()
+    q = torch.randn(len(lens), hq * D, generator=gen(seed + 3)).half().cuda()
+    slots = torch.stack([tab[b, (n - 1) // bs].long() * bs + (n - 1) % bs for b, n in enumerate(lens)])
+    return slots, x, cache, tab, ln, q, hq, hk, D
+
+
+@pytest.mark.parametrize("room", [0, 2000])
+def test_reports_of_replayed_calls(gqa, room):
+    """Captured on a stream that had no call before: bad slots, blocks and lengths of a replay are reported, and the graph
+    holds the library's kernels alone."""
+    case = step_case(gqa, room)
+    slots, cache, tab, ln = case[0], case[2], case[3], case[4]
+    want = step(gqa, *case)
+    torch.cuda.synchronize()
+    assert gqa.gqa_status_check() == gqa.GQA_OK
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(gqa, *case)
+    side = torch.cuda.Stream()
+
+    def replay():
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        return gqa.gqa_status_check()
+
+    assert replay() == gqa.GQA_OK and all(torch.equal(a, b) for a, b in zip(got, want))
+    for t, at, bad in ((slots, 1, 1 << 40), (tab, (2, 5), cache.shape[0]), (ln, 0, -4)):
+        keep = t[at].clone()
+        t[at] = bad
+        assert replay() == gqa.GQA_ERR_INVALID_ARG
+        t[at] = keep
+        assert replay() == gqa.GQA_OK and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_timeout_of_a_replayed_call_is_reported(gqa):
+    case = step_case(gqa, 0, 410, [90000, 30000])
+    tiles = 2 * (-(-90000 // 32) - (-30000 // 32))
+    assert tiles > 2 * 8 * torch.cuda.get_device_properties(0).multi_processor_count       # a worker has a second tile
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        step(gqa, *case, timeout_us=20000, test_stall_cta=0)
+    torch.cuda.synchronize()
+    assert gqa.gqa_status_check() == gqa.GQA_OK
+    graph.replay()
+    assert gqa.gqa_status_check() == gqa.GQA_ERR_TIMEOUT
+    assert gqa.gqa_status_check() == gqa.GQA_OK
+
+
+def test_captured_calls_make_no_other_nodes(gqa):
+    """A captured append, decode and read are as many nodes as they are launches: nothing is filled beside them."""
+    if not hasattr(torch.cuda.CUDAGraph, "raw_cuda_graph"):
+        pytest.skip("this torch does not give the captured graph away")
+    nodes_of = ctypes.CDLL("libcuda.so.1").cuGraphGetNodes
+    for room, kernels in ((0, 3), (2000, 4)):
+        case = step_case(gqa, room)
+        out = torch.empty_like(case[5])
+        back = [torch.zeros(3, 8, 256, dtype=torch.float16, device="cuda") for _ in range(2)]
+        graph, s = torch.cuda.CUDAGraph(keep_graph=True), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            slots, x, cache, tab, ln, q, hq, hk, D = case
+            gqa.gqa_append(None, x[:, :hk * D], x[:, hk * D:], hk, hk, slots, cache)
+            gqa.gqa_decode_kv8(q, cache, tab, ln, hq, hk, out=out)
+            gqa.gqa_kv8_read(cache, tab, ln, D, k_out=back[0], v_out=back[1])
+        n = ctypes.c_size_t(0)
+        assert nodes_of(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+        assert n.value == kernels
+
+
+def test_the_first_call_of_a_process_is_captured(gqa):
+    """Nothing of the library was called before on the device: the capture makes everything that it needs."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, decode_attention_03_gb300 as gqa
+cache = gqa.gqa_kv8_cache(4, 16, 2, 128)
+x = torch.randn(3, 512, device="cuda").half()
+q = torch.randn(1, 1024, device="cuda").half()
+slots = torch.arange(3, device="cuda")
+tab = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+ln = torch.tensor([3], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gqa.gqa_append(None, x[:, :256], x[:, 256:], 2, 2, slots, cache)
+    o = gqa.gqa_decode_kv8(q, cache, tab, ln, 8, 2)
+g.replay()
+assert gqa.gqa_status_check() == gqa.GQA_OK
+assert torch.equal(o, gqa.gqa_decode_kv8(q, cache, tab, ln, 8, 2))
+slots[2] = 64
+g.replay()
+assert gqa.gqa_status_check() == gqa.GQA_ERR_INVALID_ARG and gqa.gqa_status_check() == gqa.GQA_OK
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_decode_with_a_status_word_of_its_own(gqa):
+    """gqa_decode_kv8_status: the workspace is scratch from its first byte on."""
+    _, _, cache, tab, ln, q, hq, hk, D = step_case(gqa, 2000, 430)
+    want = gqa.gqa_decode_kv8(q, cache, tab, ln, hq, hk)
+    ws = torch.full((gqa.gqa_decode_kv8_workspace_size(3, 1, hq, hk, D),), 0xC3, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    raw = torch.cuda.current_stream().cuda_stream
+
+    def call(out, table):
+        return gqa.lib.gqa_decode_kv8_status(q.data_ptr(), cache.data_ptr(), table.data_ptr(), ln.data_ptr(), out.data_ptr(), 3,
+                                             1, tab.shape[1], cache.shape[0], 16, hq, hk, D, D ** -0.5, ws.data_ptr(),
+                                             ws.numel(), status.data_ptr(), raw, None)
+
+    out = torch.empty_like(q)
+    assert call(out, tab) == gqa.GQA_OK
+    assert gqa.gqa_workspace_check(status) == gqa.GQA_OK and torch.equal(out, want)
+    bad = tab.clone()
+    bad[2, 0] = 1 << 20
+    assert call(out, bad) == gqa.GQA_OK
+    assert gqa.gqa_workspace_check(status) == gqa.GQA_ERR_INVALID_ARG and bool((ws[:256] == 0xC3).all())
