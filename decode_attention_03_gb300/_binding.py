@@ -502,7 +502,7 @@ def gqa_status_check(device=None) -> int:
         torch.cuda.synchronize()
         index = torch.cuda.current_device()
         with _ws_lock:
-            words = [t.data_ptr() for key, t in _ws_cache.items() if key[0] == index and key[2:] in (("status",), ("kv8",))]
+            words = [t.data_ptr() for key, t in _ws_cache.items() if key[0] == index and key[2:] == ("status",)]
         own = lib.gqa_device_status()
         if own is None:
             return GQA_ERR_CUDA
@@ -583,14 +583,14 @@ def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Ten
     ws = status = workspace_tensor
     if ws is None:
         dev, raw = _place(q, "q")
+        status = _ws_cache.get((dev, raw, "status"))
         if _capturing():
-            status = _ws_cache.get((dev, raw, "status"))
             ws = torch.empty(_kv8_workspace_bytes(q, h_q, h_kv), dtype=torch.uint8, device=q.device)
         else:
             ws = _ws_cache.get((dev, raw, "kv8"))
-            if ws is None:
+            if ws is None or status is None:
+                status = _status_workspace(q, "q")
                 ws = workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")
-            status = ws
     r = _calls.decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, status, timeout_us,
                       test_stall_cta)
     if r.__class__ is int:

@@ -227,6 +227,18 @@ print("captured first")
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
+def test_a_report_outlives_a_larger_call(gqa):
+    """The stream's workspace grows between the report and the check."""
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        slots, x, cache, tab, ln, q, hq, hk, D = step_case(gqa, 2000, 420)
+        tab[0, 3] = -2
+        gqa.gqa_decode_kv8(q, cache, tab, ln, hq, hk)
+        gqa.gqa_decode_kv8(torch.zeros(1, 8, 8 * D, dtype=torch.float16, device="cuda"), cache, tab[1:2], ln[1:2], 8, hk)
+        assert gqa.gqa_workspace_check(gqa.workspace(256, use="status")) == gqa.GQA_ERR_INVALID_ARG
+    assert gqa.gqa_status_check() == gqa.GQA_OK
+
+
 def test_decode_with_a_status_word_of_its_own(gqa):
     """gqa_decode_kv8_status: the workspace is scratch from its first byte on."""
     _, _, cache, tab, ln, q, hq, hk, D = step_case(gqa, 2000, 430)
