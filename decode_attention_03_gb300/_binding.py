@@ -11,6 +11,7 @@ importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -462,8 +463,25 @@ def gqa_decode_noalloc_check(stream=None) -> int:
 # ---------------------------------------------------------------- filling a cache; the 8-bit cache
 # These calls are made for every layer of every decode step, where the host's time is what counts: their checks
 # are in ``_calls`` (csrc/torch_calls.cpp), which reads the tensors' fields directly.
-from . import _calls  # noqa: E402
+class _Calls:
+    """The extension module, imported by the first call that needs it: it belongs to one torch and one Python, and the
+    other calls of this module do without it."""
 
+    def __getattr__(self, name):
+        again = "rebuild it with this Python and torch (python -c 'import __graft_entry__ as g; g.build()')"
+        try:
+            module = importlib.import_module("._calls", __package__)
+        except ImportError as e:
+            raise ImportError(f"the extension module _calls cannot be loaded ({e}): {again}") from e
+        if module.torch_version != torch.__version__:
+            raise ImportError(f"the extension module _calls was built against torch {module.torch_version}, "
+                              f"this is {torch.__version__}: {again}")
+        for call in ("append", "decode", "read"):
+            setattr(self, call, getattr(module, call))       # found without this function from now on
+        return self.__dict__[name]
+
+
+_calls = _Calls()
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)

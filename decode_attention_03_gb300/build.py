@@ -7,7 +7,8 @@ time).  A rebuild happens only when a source or header is newer than the
 library.
 
 ``csrc/torch_calls.cpp``, the calls that take torch tensors directly, becomes the extension module
-``_calls.so`` beside it (g++, against the installed torch's headers), linked to the library.
+``_calls`` beside it (g++, against the installed torch's headers), linked to the library.  Its file carries Python's
+tag, it carries the torch version that it was built against, and another torch or Python builds it anew.
 
 ``build(checked=True)`` makes the checked library instead,
 ``libgqa_decode_checked.so`` (objects in ``_build_checked/``): the same sources
@@ -19,6 +20,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import importlib.util
 import subprocess
@@ -33,7 +35,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgqa_decode.so")
 BUILD_CHECKED = os.path.join(ROOT, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libgqa_decode_checked.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALLS_FOR = os.path.join(BUILD, "calls.for")     # what CALLS was built against
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -71,10 +74,23 @@ def _run(cmd, verbose: bool, what: str) -> None:
         raise RuntimeError(f"{what} failed")
 
 
+def torch_version() -> str:
+    """Version of the installed torch, without importing it."""
+    with open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")) as f:
+        return re.search(r"^__version__ = ['\"](.+?)['\"]", f.read(), re.M).group(1)
+
+
+def _calls_for() -> str:
+    return f"{importlib.util.find_spec('torch').origin} {torch_version()} {sys.version}"
+
+
 def calls_up_to_date() -> bool:
     """The extension module is newer than its sources and was built against the torch that is installed."""
-    if not os.path.exists(CALLS):
+    if not os.path.exists(CALLS) or not os.path.exists(CALLS_FOR):
         return False
+    with open(CALLS_FOR) as f:
+        if f.read() != _calls_for():
+            return False
     t = os.path.getmtime(CALLS)
     deps = [CALLS_SRC, os.path.join(ROOT, "include", "gqa_decode.h"), os.path.abspath(__file__),
             importlib.util.find_spec("torch").origin]
@@ -87,7 +103,7 @@ def _compile_calls(verbose: bool) -> str:
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
            sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
-    _run(["g++", "-O2", "-std=c++17", "-fPIC"] + [f for p in inc for f in ("-isystem", p)] + ["-c", CALLS_SRC, "-o", obj],
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f'-DGQA_TORCH="{torch_version()}"'] + [f for p in inc for f in ("-isystem", p)] + ["-c", CALLS_SRC, "-o", obj],
          verbose, "g++ for torch_calls.cpp")
     return obj
 
@@ -96,8 +112,11 @@ def _link_calls(obj: str, verbose: bool) -> None:
     lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
     tmp = CALLS + ".tmp"
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
-          "-L" + PKG, "-lgqa_decode", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], verbose, "link of _calls.so")
+          "-L" + PKG, "-lgqa_decode", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], verbose,
+         f"link of {os.path.basename(CALLS)}")
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_calls_for())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, checked: bool = False) -> str:
