@@ -559,6 +559,7 @@ gqa_status decode_impl(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   dim3 grid((unsigned)h_kv, (unsigned)p.n_splits, (unsigned)B);
+  std::lock_guard<std::mutex> turn(turn_of(ws));
   if (launch_unit(p.di, p.cls, kind, bf16, grid, st, tk, tv, a) != cudaSuccess) return GQA_ERR_CUDA;
   if (p.n_splits > 1 && !a.merge_in_kernel) {
     return merge_launch(a.ws_m, a.ws_l, a.ws_o, p.n_splits, p.R, D, a.o, a.m_out, a.l_out, a.o_part_out, st, bf16,
@@ -690,6 +691,7 @@ gqa_status paged_impl(const uint16_t* q, const uint16_t* k_pool, const uint16_t*
   // persistent: one wave of CTAs pulling (sequence, partition, KV head) items from a queue;
   // batches beyond kPagedSeqs sequences run as consecutive launches on the same stream
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> turn(turn_of(ws));
   for (int s0 = 0; s0 < N; s0 += kPagedSeqs) {
     const int n = std::min(kPagedSeqs, N - s0);
     a.q = reinterpret_cast<const __half*>(q) + (int64_t)s0 * h_q * D;

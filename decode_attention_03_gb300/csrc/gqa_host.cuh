@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 namespace gqa {
 
@@ -13,6 +14,14 @@ constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The launches of one call hand partials on through its workspace, so that no other call's launches on it may come between
+// them: host threads that share a stream and its workspace take turns.
+inline std::mutex& turn_of(const void* ws) {
+  constexpr int kTurns = 64;
+  static std::mutex turns[kTurns];
+  return turns[(reinterpret_cast<uintptr_t>(ws) >> 8) % kTurns];
+}
 
 // Launch with programmatic stream serialisation: the kernel may begin launching while the
 // previous kernel in the stream finishes (it waits in griddepcontrol.wait before reading).

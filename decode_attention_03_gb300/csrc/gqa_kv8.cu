@@ -32,12 +32,6 @@ __device__ __align__(256) unsigned char g_status[kHeaderBytes];   // the library
 std::mutex g_mu;
 Kv8Device g_kv8[kMaxDevices];
 
-// The launches of one decode call hand partials on through its workspace, so that no other call's launches on it may come
-// between them: host threads that share a stream and its workspace take turns.
-constexpr int kTurns = 64;
-std::mutex g_turn[kTurns];
-std::mutex& turn_of(const void* ws) { return g_turn[(reinterpret_cast<uintptr_t>(ws) >> 8) % kTurns]; }
-
 // SMs of the current device, with g_mu held by the caller
 gqa_status device_locked(Kv8Device** out) {
   int dev = 0;

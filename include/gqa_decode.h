@@ -24,6 +24,8 @@
  *  - All tensors are dense row-major, in device memory of the CURRENT CUDA
  *    device, 16-byte aligned.  The caller owns every buffer; the library never
  *    allocates device memory and never synchronises (except gqa_workspace_check).
+ *  - Calls that share a workspace must not overlap on the GPU: one stream at a time.  Host threads may
+ *    call with one workspace on one stream: the launches of a call stay together.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls are
  *    asynchronous; arguments are validated on the host before any launch and
  *    a failed validation returns an error code without touching the GPU.
@@ -365,8 +367,7 @@ size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, i
  * keys: the same call gives the same bits.  Block ids outside [0, num_blocks) are not loaded, lengths outside
  * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check.
  * Only the first 256 bytes of the workspace have to be zero; the rest is left dirty, so that a workspace of this
- * call needs gqa_workspace_init before it serves gqa_decode or gqa_decode_paged.  Host threads may call with one
- * workspace on one stream: the launches of a call stay together. */
+ * call needs gqa_workspace_init before it serves gqa_decode or gqa_decode_paged. */
 gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
                           uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
                           int h_q, int h_kv, int d_head, float scale, void* workspace, size_t ws_bytes, void* stream,

@@ -78,6 +78,49 @@ def test_threads_on_one_stream(gqa):
     assert sorted(bad) == [(i, 0) for i in range(len(cases))]
 
 
+@pytest.mark.parametrize("paged", [False, True])
+def test_threads_on_one_stream_over_16_bit_caches(gqa, paged):
+    """The same for the calls over contiguous and paged caches that fold their splits in a second launch."""
+    D, hq, hk, bs, n, raw = 128, 8, 2, 16, 4096, torch.cuda.current_stream().cuda_stream
+    size = max(gqa.gqa_paged_workspace_size(2, hq, hk, D, n, 512), gqa.gqa_decode_workspace_size(2, 1, n, hq, hk, D, 9))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    opt = ctypes.byref(gqa._opts(9, 1))
+    calls, want, held = [], [], []
+    for i in range(4):
+        q = torch.randn(2, hq * D, generator=gen(500 + i)).half().cuda()
+        k, v = (torch.randn(2, n, hk * D, generator=gen(510 + 2 * i + w)).half().cuda() for w in (0, 1))
+        tab = torch.arange(2 * n // bs, dtype=torch.int32, device="cuda")
+        ln = torch.full((2,), n - 100 * i, dtype=torch.int32, device="cuda")
+        held += [q, k, v, tab, ln]
+        at = [x.data_ptr() for x in (q, k, v, tab, ln)]
+        if paged:
+            calls.append(lambda out, p=at: gqa.lib.gqa_decode_paged(*p, out.data_ptr(), 2, n // bs, 2 * n // bs, bs, 512, hq,
+                                                                    hk, D, D ** -0.5, n, ws.data_ptr(), size, raw))
+        else:
+            calls.append(lambda out, p=at: gqa.lib.gqa_decode_ex(*p[:3], out.data_ptr(), 2, 1, n, hq, hk, D, D ** -0.5,
+                                                                 ws.data_ptr(), size, raw, opt))
+        want.append(torch.empty_like(q))
+        assert calls[i](want[i]) == gqa.GQA_OK
+    torch.cuda.synchronize()
+    bad, start = [], threading.Barrier(len(calls))
+
+    def work(i):
+        torch.cuda.set_device(want[i].device)
+        out = [torch.empty_like(want[i]) for _ in range(2000)]
+        start.wait()
+        for o in out:
+            calls[i](o)
+        torch.cuda.synchronize()
+        bad.append((i, sum(not torch.equal(o, want[i]) for o in out)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(bad) == [(i, 0) for i in range(len(calls))]
+
+
 # ---------------------------------------------------------------- calls without tokens
 @pytest.mark.parametrize("layout", ["rows", "vllm", "kv8"])
 def test_append_of_no_tokens(gqa, layout):
