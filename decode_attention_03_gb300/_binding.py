@@ -463,25 +463,25 @@ def gqa_decode_noalloc_check(stream=None) -> int:
 # ---------------------------------------------------------------- filling a cache; the 8-bit cache
 # These calls are made for every layer of every decode step, where the host's time is what counts: their checks
 # are in ``_calls`` (csrc/torch_calls.cpp), which reads the tensors' fields directly.
-class _Calls:
-    """The extension module, imported by the first call that needs it: it belongs to one torch and one Python, and the
-    other calls of this module do without it."""
-
-    def __getattr__(self, name):
-        again = "rebuild it with this Python and torch (python -c 'import __graft_entry__ as g; g.build()')"
-        try:
-            module = importlib.import_module("._calls", __package__)
-        except ImportError as e:
-            raise ImportError(f"the extension module _calls cannot be loaded ({e}): {again}") from e
-        if module.torch_version != torch.__version__:
-            raise ImportError(f"the extension module _calls was built against torch {module.torch_version}, "
-                              f"this is {torch.__version__}: {again}")
-        for call in ("append", "decode", "read"):
-            setattr(self, call, getattr(module, call))       # found without this function from now on
-        return self.__dict__[name]
+_calls = None
 
 
-_calls = _Calls()
+def _load_calls():
+    """The extension module, imported by the first call that needs it: it belongs to one torch and one Python, and the other
+    calls of this module do without it."""
+    global _calls
+    again = "rebuild it with this Python and torch (python -c 'import __graft_entry__ as g; g.build()')"
+    try:
+        module = importlib.import_module("._calls", __package__)
+    except ImportError as e:
+        raise ImportError(f"the extension module _calls cannot be loaded ({e}): {again}") from e
+    if module.torch_version != torch.__version__:
+        raise ImportError(f"the extension module _calls was built against torch {module.torch_version}, "
+                          f"this is {torch.__version__}: {again}")
+    _calls = module
+    return module
+
+
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -564,8 +564,8 @@ def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q:
                               interleaved=interleaved, q_weight=q_weight, k_weight=k_weight, eps=eps, q_out=q_out,
                               workspace_tensor=workspace_tensor)
     ws = _status_workspace(k, "k") if workspace_tensor is None else workspace_tensor
-    r = _calls.append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions, cos_sin, interleaved, q_weight, k_weight,
-                      eps, q_out, ws)
+    r = (_calls or _load_calls()).append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions, cos_sin, interleaved,
+                                         q_weight, k_weight, eps, q_out, ws)
     if r.__class__ is int:
         raise GQAError(r, "gqa_append")
     return r
@@ -609,8 +609,8 @@ def gqa_decode_kv8(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Ten
             if ws is None or status is None:
                 status = _status_workspace(q, "q")
                 ws = workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")
-    r = _calls.decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, status, timeout_us,
-                      test_stall_cta)
+    r = (_calls or _load_calls()).decode(q, cache, block_tables, seq_lens, h_q, h_kv, scale, causal, out, ws, status,
+                                         timeout_us, test_stall_cta)
     if r.__class__ is int:
         if r == GQA_ERR_WORKSPACE and workspace_tensor is None and ws.numel() < _kv8_workspace_bytes(q, h_q, h_kv):
             workspace(_kv8_workspace_bytes(q, h_q, h_kv), q.device, use="kv8")       # the cached one grows
@@ -643,7 +643,7 @@ def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torc
         for t in (k_out, v_out):
             if t is not None and (out_len not in (None, t.shape[1]) or dtype not in (None, t.dtype)):
                 raise ValueError("k_out and v_out must be (N, out_len, h_kv*d_head) of dtype")
-    r = _calls.read(cache, block_tables, seq_lens, d_head, begins, k_out, v_out, ws)
+    r = (_calls or _load_calls()).read(cache, block_tables, seq_lens, d_head, begins, k_out, v_out, ws)
     if r:
         raise GQAError(r, "gqa_kv8_read")
     return k_out, v_out
