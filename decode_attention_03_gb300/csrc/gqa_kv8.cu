@@ -175,7 +175,7 @@ gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
 
 // ---------------------------------------------------------------- decode
 // Kernel shapes: up to 8, 16, 24 or 32 query rows for one warp, 48 or 64 for two warps that share a ring.
-// 24 and 48 beside 32 and 64, measured (us, with / without): 131071 keys, 24 rows, d 128 57.1 / 67.7, in f16 65.3 / 85.3; 10
+// 24 and 48 beside 32 and 64, measured (us, with / without): 131071 keys, 24 rows, d 128 56.6 / 67.7, in f16 65.5 / 85.3; 10
 // sequences of 5000-53000, 35 rows 136 / 175; 43 of 50-1460, 24 rows, d 64 27.8 / 31.4.
 int kv8_class(int rows) { return rows <= 32 ? (rows + 7) / 8 - 1 : (rows <= 48 ? 4 : 5); }
 int kv8_groups(int cls) { return cls < 4 ? kKv8Warps : kKv8Warps / 2; }
@@ -230,9 +230,9 @@ constexpr int kMergeCtas = 2048;
 // CTAs of a unit in the short kernel, a cluster of 1, 2, 4 or 8: the fewest that give each worker one tile, as far as all
 // units' clusters fit on three quarters of the SMs at once (a cluster lies in one GPC).  0: the general kernel, where a
 // worker would have more than kKv8Short tiles, or more than two above what the general kernel, which uses every SM,
-// gives one.  Measured (us, short / general; tiles of a worker in brackets): 8 KV heads of 128: one sequence of 300 keys
-// 7.0 / 8.7 [1, 1], 2000 7.4 / 8.9 [1, 1], 8000 9.9 / 9.9 [4, 2], 16000 13.6 / 11.9 [8, 4]; 4 of 500-1000 7.9 / 10.3 [1, 1];
-// 16 of 1000-2000 13.5 / 18.0 [8, 7]; 2 KV heads of 64: 4096 keys 6.5 / 7.7 [2, 1], 16384 11.1 / 10.5 [8, 1].
+// gives one.  Measured (us of a replayed call, short / general; tiles of a worker in brackets): 8 KV heads of 128: one
+// sequence of 300 keys 5.3 / 7.6 [1, 1], 2000 5.7 / 7.6 [1, 1], 8000 8.9 / 8.9 [4, 2], 16000 13.1 / 11.0 [8, 4]; 4 of 500-1000
+// 6.5 / 9.6 [1, 1]; 16 of 1000-2000 13.0 / 17.0 [8, 7]; 2 KV heads of 64: 4096 keys 5.5 / 6.6 [2, 1], 16384 10.2 / 8.3 [8, 1].
 int kv8_short_ctas(int64_t units, int64_t seq_tiles, int sms, int groups) {
   int ctas = 1;
   while (ctas < 8 && ctas * groups < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;

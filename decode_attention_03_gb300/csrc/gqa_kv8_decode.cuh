@@ -567,8 +567,8 @@ __device__ __noinline__ bool kv8_hidden_nan(uint32_t st, int eb, int first, int 
 // FINE: the weights as two f16 numbers, the rounded one and what was lost.  A weight rounded to f16 is off by as much as
 // an f16 output is (64 sequences, against 64 bits: 2.9e-4 instead of 2.1e-4, 1.41 times), so f16 calls take the
 // second product; the rounding of a bf16 output is eight times as coarse (1 % more error with one number), and there it
-// costs time.  Measured (us, bf16 calls, one number / two): up to 8 rows: 384 sequences of 1000-2000 keys 190.3 / 189.6, 23 of 2000-3900
-// 15.2 / 15.6, 16 of 1000-2000 11.5 / 12.4; 16 rows: 64 of 16000-32000 72.6 / 78.7, 64 of 4000-8000 126.3 / 136.1.
+// costs time.  Measured (us, bf16 calls, one number / two): up to 8 rows: 384 sequences of 1000-2000 keys 190.3 / 189.6, 23 of
+// 2000-3900 15.2 / 15.6, 16 of 1000-2000 11.5 / 12.4; 16 rows: 64 of 16000-32000 72.6 / 78.7, 64 of 4000-8000 126.3 / 136.1.
 template <int D, int NT, int RG, bool FINE>
 __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params& a, uint32_t st, int eb, int valid,
                                          int last, bool masked, int rg, int lane, const Win& ring) {
@@ -1084,8 +1084,8 @@ __device__ __forceinline__ float2 ld_cluster_v2(uint32_t addr) {
 // their workers (at most kKv8Short tiles each, so that one window of block ids serves a worker).  There is nothing to
 // search: a CTA needs one length.  The warps of a CTA fold their states in shared memory, the CTAs of the cluster
 // theirs through distributed shared memory, each a part of the columns, both in the order of the keys.
-// Bound by latency: one sequence of 4096 keys, 8 + 2 heads of 64, 5.8-6.6 us (1.1 MB, 0.2 us of HBM) against 7.6 of the general
-// kernel and its merge.
+// Bound by latency: one sequence of 4096 keys, 8 + 2 heads of 64, 5.5 us replayed (1.1 MB, 0.2 us of HBM) against 6.6 of the
+// general kernel and its merge.
 template <int D, int NT, int RG, bool BF16>
 __global__ void __launch_bounds__(kKv8Threads, 1)
 gqa_decode_kv8_short_kernel(const Kv8Params a) {
