@@ -366,8 +366,9 @@ size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, i
  * all sequences are split evenly over the workers, whatever the lengths, and joined in the order of the
  * keys: the same call gives the same bits.  Block ids outside [0, num_blocks) are not loaded, lengths outside
  * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check.
- * Weights keep 11 bits (f16 calls 22) whatever the sizes of scores and values; only values below 2^-88 may be lost
- * where the same sequence and head has values more than 2^10 times as large.
+ * A key's weight is rounded to 11 bits (f16 calls: 22) or, where it is very small, to within 2^-26 of its row's largest
+ * term, a weight times the scale of its value; values below 2^-88 may be lost where the same sequence and head has values
+ * more than 2^10 times as large.
  * Only the first 256 bytes of the workspace have to be zero; the rest is left dirty, so that a workspace of this
  * call needs gqa_workspace_init before it serves gqa_decode or gqa_decode_paged. */
 gqa_status gqa_decode_kv8(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
