@@ -838,15 +838,16 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     }
 }
 
-// A state as it leaves the worker: m + shift, l 2^-shift and O times `unit` stand for m, l and O.
+// A state as it leaves the worker: m + shift, l times `l` = 2^-shift and O times `o` stand for m, l and O.  The shift
+// keeps sums of the largest values, and of the smallest, in float's range.
 template <int D, int NT, int RG>
 struct Kv8Units {
   float shift, l, o;
   __device__ __forceinline__ explicit Kv8Units(const Kv8Warp<D, NT, RG>& w) {
-    const bool wide = w.lo >= kKv8Wide;
-    shift = wide ? (float)kKv8WideUnit : -(float)kKv8Lift;
-    l = wide ? 1.f / (float)(1ull << kKv8WideUnit) : (float)(1 << kKv8Lift);
-    o = wide ? 1.f : kv8_scale((uint32_t)w.e);
+    const int s = w.lo >= kKv8Wide || w.e >= 192 ? kKv8WideUnit : (w.e < 64 ? -64 : 0);
+    shift = (float)s;
+    l = kv8_ratio(-s);
+    o = w.lo >= kKv8Wide ? 1.f : kv8_ratio(w.e - 127 - kKv8Lift - s);
   }
 };
 

@@ -218,3 +218,19 @@ def test_not_a_number_that_the_causal_tail_hides(gqa, D, hq, hk, T, elem):
                 assert torch.equal(o.isnan(), ref.isnan()), where
                 err, tol = (o - ref).abs(), U[elem] * ref.abs() + 4 * 2.0 ** -11 * a + TINY[elem]
                 assert not (err > tol).any(), where
+
+
+@pytest.mark.parametrize("elem", ["f16", "bf16"])
+@pytest.mark.parametrize("D,hq,hk,T", SHAPES)
+def test_pieces_of_values_of_any_one_size(gqa, D, hq, hk, T, elem):
+    """A last tile whose only key has the largest exponent that an infinity leaves, or the smallest, behind tiles of ordinary
+    ones: its worker has seen no other scale.  And sequences of one scale throughout, from the smallest to the largest."""
+    bs = 16
+    for n, last, rest in ((1633, 247, 120), (1633, 1, 120), (97, 247, 120), (1633, 30, 30), (4097, 2, 2), (1633, 215, 215),
+                          (1633, 235, 235), (1633, 63, 63), (1633, 64, 64), (1633, 191, 191), (1633, 192, 192)):
+        for room in (0, 3000):
+            k, ke, v, ve = keys(n, hk, D, n + last)
+            ve[:] = rest
+            ve[n - 1] = last
+            q = torch.randn(1, T, hq * D, generator=gen(25))
+            check(gqa, *rows_to_cache(k, ke, v, ve, bs, 26, room), n, q, hq, hk, D, bs, elem, where=f"{n} {last} {rest} {room}")
