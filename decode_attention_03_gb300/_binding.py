@@ -15,7 +15,7 @@ import importlib
 import math
 import os
 import threading
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -33,6 +33,7 @@ GQA_BUILD_BOUNDS_CHECK = 1
 GQA_CACHE_ROWS = 0
 GQA_CACHE_VLLM = 1
 GQA_CACHE_KV8 = 2
+GQA_CACHE_KV4 = 4
 
 
 class GQAError(RuntimeError):
@@ -105,6 +106,12 @@ _SIGS = {
     "gqa_decode_kv8_status": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _p, _p, _opt], _i),
     "gqa_device_status": ([], _p),
     "gqa_kv8_read": ([_p, _p, _p, _p, _p, _p, _i, _i64, _i, _i, _i, _i, _i, _p, _sz, _p, _opt], _i),
+    "gqa_kv4_block_bytes": ([_i, _i], _sz),
+    "gqa_append_axes": ([ctypes.POINTER(gqa_append_args), _p, _i, _p, _sz, _p], _i),
+    "gqa_decode_window_workspace_size": ([_i, _i, _i, _i, _i, _i], _sz),
+    "gqa_decode_kv4": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i, _p, _sz, _p, _p, _opt], _i),
+    "gqa_decode_window": ([_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i, _p, _sz, _p, _p, _opt], _i),
+    "gqa_kv4_read": ([_p, _p, _p, _p, _p, _p, _i, _i64, _i, _i, _i, _i, _i, _p, _sz, _p, _opt], _i),
     "gqa_decode_paged_vllm_ex": ([_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p,
                                   _opt], _i),
 }
@@ -513,8 +520,9 @@ def _status_workspace(t: torch.Tensor, name: str) -> Optional[torch.Tensor]:
 
 
 def gqa_status_check(device=None) -> int:
-    """Status of the calls of gqa_append, gqa_decode_kv8 and gqa_kv8_read without a ``workspace_tensor`` on a device (the
-    current one), of all streams, eager and replayed, since the last check; synchronises the device and clears it."""
+    """Status of the calls of the cache operators (gqa_append, gqa_decode_kv8, gqa_decode_kv4, gqa_decode_window, gqa_kv8_read,
+    gqa_kv4_read) without a ``workspace_tensor`` on a device (the current one), of all streams, eager and replayed, since the
+    last check; synchronises the device and clears it."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         torch.cuda.synchronize()
@@ -546,26 +554,28 @@ def gqa_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, h_q:
                positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None,
                interleaved: bool = False, q_weight: Optional[torch.Tensor] = None,
                k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
-               workspace_tensor: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+               workspace_tensor: Optional[torch.Tensor] = None, stream=None,
+               pair_axes: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """Put new tokens into a paged cache: per-head RMS norms of q and k (where ``q_weight`` / ``k_weight`` (D)
     are given), their rotation (where ``cos_sin`` (max_position, rot_dim) float32 and ``positions`` (T) int32
     are given: rot_dim/2 cosines then rot_dim/2 sines a row; ``interleaved``: pairs (2i, 2i+1) instead of
-    (i, i + rot_dim/2)), and the write of k and v into the cache rows ``slots`` (T) int64
+    (i, i + rot_dim/2); with ``pair_axes`` (rot_dim/2) uint8, as gqa_pair_axes makes it, ``positions`` are
+    (axes, T) and pair i is turned by the position on axis pair_axes[i]), and the write of k and v into the cache rows ``slots`` (T) int64
     (block * block_size + row; negative: not stored; no slot twice).
 
     q (T, h_q*D) or None, k, v (T, h_kv*D) float16 or bfloat16, rows dense (views of a fused projection serve).
     The cache: ``k_cache, v_cache`` of gqa_decode_paged (num_blocks, block_size, h_kv*D) or of
-    gqa_decode_paged_vllm, or one 8-bit cache (gqa_kv8_cache), quantised as it is written.
+    gqa_decode_paged_vllm, or one 8-bit or 4-bit cache (gqa_kv8_cache, gqa_kv4_cache), quantised as it is written.
     Returns the queries after norm and rotation (``q_out``, which may be q itself).  What the kernel reports is in the
     status word of ``workspace_tensor``; without one, gqa_status_check has it, for captured calls too."""
     if stream is not None:
         with _in_stream(stream):
             return gqa_append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions=positions, cos_sin=cos_sin,
                               interleaved=interleaved, q_weight=q_weight, k_weight=k_weight, eps=eps, q_out=q_out,
-                              workspace_tensor=workspace_tensor)
+                              workspace_tensor=workspace_tensor, pair_axes=pair_axes)
     ws = _status_workspace(k, "k") if workspace_tensor is None else workspace_tensor
     r = (_calls or _load_calls()).append(q, k, v, h_q, h_kv, slots, k_cache, v_cache, positions, cos_sin, interleaved,
-                                         q_weight, k_weight, eps, q_out, ws)
+                                         q_weight, k_weight, eps, q_out, ws, pair_axes)
     if r.__class__ is int:
         raise GQAError(r, "gqa_append")
     return r
@@ -629,10 +639,16 @@ def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torc
     K and V (N, out_len, h_kv*D), the layout of gqa_decode.  Into ``k_out`` / ``v_out`` (the one left out is
     not read; rows past a sequence's last token stay as they were), or, with neither, into zeros of ``dtype``
     (float16) and ``out_len`` tokens.  begins (N) int32, default 0.  Reports as those of gqa_append."""
+    return _read("gqa_kv8_read", cache, block_tables, seq_lens, d_head, out_len, begins, dtype, k_out, v_out, workspace_tensor,
+                 stream)
+
+
+def _read(name, cache, block_tables, seq_lens, d_head, out_len, begins, dtype, k_out, v_out, workspace_tensor, stream):
+    """gqa_kv8_read and gqa_kv4_read."""
     if stream is not None:
         with _in_stream(stream):
-            return gqa_kv8_read(cache, block_tables, seq_lens, d_head, out_len, begins=begins, dtype=dtype,
-                                k_out=k_out, v_out=v_out, workspace_tensor=workspace_tensor)
+            return _read(name, cache, block_tables, seq_lens, d_head, out_len, begins, dtype, k_out, v_out, workspace_tensor,
+                         None)
     ws = _status_workspace(cache, "cache") if workspace_tensor is None else workspace_tensor
     if k_out is None and v_out is None:
         if out_len is None:
@@ -643,7 +659,117 @@ def gqa_kv8_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torc
         for t in (k_out, v_out):
             if t is not None and (out_len not in (None, t.shape[1]) or dtype not in (None, t.dtype)):
                 raise ValueError("k_out and v_out must be (N, out_len, h_kv*d_head) of dtype")
-    r = (_calls or _load_calls()).read(cache, block_tables, seq_lens, d_head, begins, k_out, v_out, ws)
+    calls = _calls or _load_calls()
+    r = (calls.read if name == "gqa_kv8_read" else calls.read4)(cache, block_tables, seq_lens, d_head, begins, k_out, v_out, ws)
     if r:
-        raise GQAError(r, "gqa_kv8_read")
+        raise GQAError(r, name)
     return k_out, v_out
+
+
+# ---------------------------------------------------------------- several position axes; the 4-bit cache; windows
+def gqa_pair_axes(sections: Sequence[int], *, in_turn: bool = False, device=None) -> torch.Tensor:
+    """The axis of each rotated pair for gqa_append's ``pair_axes``, uint8 (sum(sections),): sections[i] pairs on axis i, as
+    runs one after the other, or ``in_turn``: dealt out one to each axis in turn until its section is used up."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 32 or min(sections) < 0:
+        raise ValueError("sections must be one to 32 whole numbers, none below 0")
+    if in_turn:
+        order = [i for k in range(max(sections)) for i, n in enumerate(sections) if k < n]
+    else:
+        order = [i for i, n in enumerate(sections) for _ in range(n)]
+    return torch.tensor(order, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def gqa_kv4_block_bytes(block_size: int, d_head: int) -> int:
+    """Bytes of one (block, head) of the 4-bit cache; 0 for a block size or d_head it does not have."""
+    return lib.gqa_kv4_block_bytes(int(block_size), int(d_head))
+
+
+def gqa_kv4_cache(num_blocks: int, block_size: int, h_kv: int, d_head: int, device=None) -> torch.Tensor:
+    """An empty 4-bit cache: uint8 (num_blocks, h_kv, block_size * (d_head + d_head / 8))."""
+    n = gqa_kv4_block_bytes(block_size, d_head)
+    if n == 0:
+        raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_kv4_cache")
+    return torch.zeros(num_blocks, h_kv, n, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def gqa_decode_window_workspace_size(num_seqs: int, T_q: int, h_q: int, h_kv: int, d_head: int,
+                                     cache_layout: int = GQA_CACHE_ROWS) -> int:
+    """Workspace bytes of gqa_decode_window (GQA_CACHE_ROWS) or gqa_decode_kv4 (GQA_CACHE_KV4) on the current device
+    (0: invalid shape)."""
+    return lib.gqa_decode_window_workspace_size(num_seqs, T_q, h_q, h_kv, d_head, cache_layout)
+
+
+def _window_workspace_bytes(q: torch.Tensor, h_q: int, h_kv: int, layout: int) -> int:
+    n = gqa_decode_window_workspace_size(1, q.shape[1] if q.dim() == 3 else 1, h_q, h_kv, q.shape[-1] // h_q if h_q else 0,
+                                         layout)
+    if n == 0:
+        raise GQAError(GQA_ERR_UNSUPPORTED, "gqa_decode_window_workspace_size")
+    return n
+
+
+def _window(name, layout, q, k, v, block_tables, seq_lens, h_q, h_kv, scale, window, sinks, causal, out, workspace_tensor,
+            timeout_us, test_stall_cta):
+    """gqa_decode_kv4 (v None) and gqa_decode_window on the current stream."""
+    ws = status = workspace_tensor
+    if ws is None:
+        dev, raw = _place(q, "q")
+        status = _ws_cache.get((dev, raw, "status"))
+        if _capturing():
+            ws = torch.empty(_window_workspace_bytes(q, h_q, h_kv, layout), dtype=torch.uint8, device=q.device)
+        else:
+            ws = _ws_cache.get((dev, raw, "window"))
+            if ws is None or status is None:
+                status = _status_workspace(q, "q")
+                ws = workspace(_window_workspace_bytes(q, h_q, h_kv, layout), q.device, use="window")
+    r = (_calls or _load_calls()).window(q, k, v, block_tables, seq_lens, h_q, h_kv, scale, window, sinks, causal, out, ws,
+                                         status, timeout_us, test_stall_cta)
+    if r.__class__ is int:
+        if r == GQA_ERR_WORKSPACE and workspace_tensor is None and ws.numel() < _window_workspace_bytes(q, h_q, h_kv, layout):
+            workspace(_window_workspace_bytes(q, h_q, h_kv, layout), q.device, use="window")       # the cached one grows
+            return _window(name, layout, q, k, v, block_tables, seq_lens, h_q, h_kv, scale, window, sinks, causal, out, None,
+                           timeout_us, test_stall_cta)
+        raise GQAError(r, name)
+    return r
+
+
+def gqa_decode_kv4(q: torch.Tensor, cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, h_q: int,
+                   h_kv: int, scale: Optional[float] = None, *, causal: bool = False, window: int = 0, sinks: int = 0,
+                   out: Optional[torch.Tensor] = None, workspace_tensor: Optional[torch.Tensor] = None, stream=None,
+                   timeout_us: int = 0, test_stall_cta: int = -1) -> torch.Tensor:
+    """Decode attention over the 4-bit cache: q (N, h_q*D) or (N, T_q, h_q*D) float16 or bfloat16 (the output too),
+    cache (num_blocks, h_kv, block_size*(D + D/8)) uint8, tables (N, max_blocks) and lens (N) int32; G*T_q <= 64.
+    ``causal``: query token t has the place len - T_q + t and sees the keys up to it only.  ``window`` > 0: of those only the
+    ``window`` newest, its own among them, and the first ``sinks`` of the sequence; blocks that no token sees are not looked
+    up in the table.  Workspaces and reports as those of gqa_decode_kv8."""
+    if stream is not None:
+        with _in_stream(stream):
+            return _window("gqa_decode_kv4", GQA_CACHE_KV4, q, cache, None, block_tables, seq_lens, h_q, h_kv, scale, window,
+                           sinks, causal, out, workspace_tensor, timeout_us, test_stall_cta)
+    return _window("gqa_decode_kv4", GQA_CACHE_KV4, q, cache, None, block_tables, seq_lens, h_q, h_kv, scale, window, sinks,
+                   causal, out, workspace_tensor, timeout_us, test_stall_cta)
+
+
+def gqa_decode_window(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, h_q: int, h_kv: int, scale: Optional[float] = None, *, window: int,
+                      sinks: int = 0, causal: bool = False, out: Optional[torch.Tensor] = None,
+                      workspace_tensor: Optional[torch.Tensor] = None, stream=None, timeout_us: int = 0,
+                      test_stall_cta: int = -1) -> torch.Tensor:
+    """gqa_decode_kv4 over the 16-bit pools of gqa_decode_paged: k_pool, v_pool (num_blocks, block_size, h_kv*D) of q's dtype.
+    ``window`` 0: every key is visible."""
+    if stream is not None:
+        with _in_stream(stream):
+            return _window("gqa_decode_window", GQA_CACHE_ROWS, q, k_pool, v_pool, block_tables, seq_lens, h_q, h_kv, scale,
+                           window, sinks, causal, out, workspace_tensor, timeout_us, test_stall_cta)
+    return _window("gqa_decode_window", GQA_CACHE_ROWS, q, k_pool, v_pool, block_tables, seq_lens, h_q, h_kv, scale, window,
+                   sinks, causal, out, workspace_tensor, timeout_us, test_stall_cta)
+
+
+def gqa_kv4_read(cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, d_head: int,
+                 out_len: Optional[int] = None, *, begins: Optional[torch.Tensor] = None, dtype=None,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 workspace_tensor: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """gqa_kv8_read of a 4-bit cache."""
+    return _read("gqa_kv4_read", cache, block_tables, seq_lens, d_head, out_len, begins, dtype, k_out, v_out, workspace_tensor,
+                 stream)

@@ -1,0 +1,4 @@
+// Filling a paged cache, d_head 128, bfloat16.
+#include "gqa_append_inst.cuh"
+
+GQA_APPEND_INSTANCE(128, true)

@@ -1,4 +1,4 @@
-// Host side of the cache operators: gqa_append, gqa_decode_kv8 and gqa_kv8_read.
+// Host side of gqa_append, gqa_decode_kv8 and gqa_kv8_read.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -6,20 +6,12 @@
 #include <mutex>
 
 #include "../../include/gqa_decode.h"
-#include "gqa_host.cuh"
+#include "gqa_cache_host.cuh"
 #include "gqa_kv8.cuh"
 #include "gqa_kv8_decode.cuh"
 
 namespace gqa {
 namespace {
-
-bool block_size_ok(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64; }
-
-int log2_of(int block_size) { return block_size == 8 ? 3 : (block_size == 16 ? 4 : (block_size == 32 ? 5 : 6)); }
-
-bool aligned_to(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-gqa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
 
 // ---------------------------------------------------------------- per-device state
 struct Kv8Device {
@@ -62,54 +54,15 @@ void* device_status() {
 }
 
 // ---------------------------------------------------------------- append
-// Heads of a warp, in groups of HPW: as many as four where the tokens then still fill the GPU's resident warps,
-// so that a token's cosines, sines and weights are loaded once for them; else one, the shortest chain.
-// Measured (us, groups 1 / 2 / 4): 16384 tokens, 64 + 8 + 8 heads of 128: 117.0 / 105.6 / 105.4; 8192 tokens, 32 + 8 + 8
-// heads into the 8-bit cache, with a read-back: 61.9 / 58.1 / 57.2; but 64 tokens with theirs, before the rule 4.5 / 4.8 / 5.6.
-template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
-cudaError_t append_launch(AppendParams p, int sms, cudaStream_t st) {
-  constexpr int HPW = 32 / (D / (2 * CW));
-  const int qg = (p.h_q + HPW - 1) / HPW, kg = (p.h_kv + HPW - 1) / HPW;
-  int sets = 0;
-  for (p.iters = kAppendIters;; p.iters /= 2) {
-    p.q_sets = (qg + p.iters - 1) / p.iters;
-    p.k_sets = (kg + p.iters - 1) / p.iters;
-    sets = p.q_sets + 2 * p.k_sets;
-    if (p.iters == 1 || (int64_t)p.num_tokens * sets >= (int64_t)sms * 4 * (kAppendThreads / 32)) break;
-  }
-  const unsigned per = kAppendThreads / 32;
-  // as many tokens of a warp as leave two rounds of CTAs.  Measured (us, at least 1 / 2 / 3 / 4 rounds): 8192 tokens of
-  // 32 + 8 + 8 heads of 128 with the read-back 58.8 / 57.2 / 57.2 / 60.7; of 8 + 2 + 2 heads of 64 10.1 / 9.8 / 11.4 / 11.3.
-  const int64_t round = (int64_t)sms * kAppendCtas * per;
-  for (p.run = 1; p.run < kAppendRun && (int64_t)p.num_tokens * sets >= 4 * p.run * round;) p.run *= 2;
-  const dim3 grid(((unsigned)p.num_tokens + per * p.run - 1) / (per * p.run), (unsigned)sets);
-  return launch_pdl_smem(gqa_append_kernel<D, BF16, CW, PAIRS, LAYOUT>, grid, kAppendThreads, 0, st, 1, p);
-}
-
-template <int D, bool BF16, int CW, bool PAIRS>
-cudaError_t append_layout(const AppendParams& p, int layout, int sms, cudaStream_t st) {
-  switch (layout) {
-    case GQA_CACHE_ROWS: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_ROWS>(p, sms, st);
-    case GQA_CACHE_VLLM: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_VLLM>(p, sms, st);
-    default: return append_launch<D, BF16, CW, PAIRS, GQA_CACHE_KV8>(p, sms, st);
-  }
-}
-
-template <int D, bool BF16>
-cudaError_t append_run(const AppendParams& p, int layout, int sms, cudaStream_t st) {
-  const bool pairs = p.cos_sin != nullptr && p.interleaved;
-  if (p.cos_sin != nullptr && p.rot_dim % 16 != 0)
-    return pairs ? append_layout<D, BF16, 4, true>(p, layout, sms, st) : append_layout<D, BF16, 4, false>(p, layout, sms, st);
-  return pairs ? append_layout<D, BF16, 8, true>(p, layout, sms, st) : append_layout<D, BF16, 8, false>(p, layout, sms, st);
-}
-
-gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void* stream) {
+gqa_status append_impl(const gqa_append_args& a, const uint8_t* pair_axes, int num_axes, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (num_axes < 1 || num_axes > kAppendAxes || (num_axes > 1 && pair_axes == nullptr)) return GQA_ERR_INVALID_ARG;
   if (a.num_tokens < 0 || a.h_q < 0 || a.h_kv < 1 || a.num_blocks < 0) return GQA_ERR_INVALID_ARG;
   if (a.h_q > 32767 || a.h_kv > 16383 || a.h_q % a.h_kv != 0) return GQA_ERR_INVALID_ARG;   // sets fit a grid's y
   if (a.d_head != 64 && a.d_head != 128) return GQA_ERR_UNSUPPORTED;
   if (!block_size_ok(a.block_size) || (int64_t)a.num_blocks * a.block_size >= (int64_t(1) << 31))
     return GQA_ERR_INVALID_ARG;
-  if (a.cache_layout < GQA_CACHE_ROWS || a.cache_layout > GQA_CACHE_KV8) return GQA_ERR_INVALID_ARG;
+  if ((a.cache_layout < GQA_CACHE_ROWS || a.cache_layout > GQA_CACHE_KV8) && a.cache_layout != GQA_CACHE_KV4) return GQA_ERR_INVALID_ARG;
   if (!std::isfinite(a.eps) || a.eps < 0.f) return GQA_ERR_INVALID_ARG;
   if (a.cos_sin != nullptr &&
       (a.rot_dim < 8 || a.rot_dim > a.d_head || a.rot_dim % 8 != 0 || a.max_position < 1 || !aligned16(a.cos_sin) ||
@@ -122,7 +75,7 @@ gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void
                       !aligned16(a.q) || !aligned16(a.q_out)))
       return GQA_ERR_INVALID_ARG;
     if (!aligned16(a.k) || !aligned16(a.v) || !aligned_to(a.slots, 8) || !aligned16(a.k_cache) ||
-        (a.cache_layout != GQA_CACHE_KV8 && !aligned16(a.v_cache)))
+        (a.cache_layout < GQA_CACHE_KV8 && !aligned16(a.v_cache)))
       return GQA_ERR_INVALID_ARG;
     if ((a.q_weight != nullptr && !aligned16(a.q_weight)) || (a.k_weight != nullptr && !aligned16(a.k_weight)))
       return GQA_ERR_INVALID_ARG;
@@ -149,37 +102,14 @@ gqa_status append_impl(const gqa_append_args& a, void* ws, size_t ws_bytes, void
   p.max_position = a.max_position; p.rot_dim = a.rot_dim; p.interleaved = a.interleaved ? 1 : 0;
   p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.bs_log = log2_of(a.block_size);
   p.eps = a.eps;
+  p.pair_axes = pair_axes; p.num_axes = num_axes;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.d_head == 64)
     return cuda_status(a.bf16 ? append_run<64, true>(p, a.cache_layout, sms, st) : append_run<64, false>(p, a.cache_layout, sms, st));
   return cuda_status(a.bf16 ? append_run<128, true>(p, a.cache_layout, sms, st) : append_run<128, false>(p, a.cache_layout, sms, st));
 }
 
-// ---------------------------------------------------------------- shapes of the kv8 calls
-gqa_status check_kv8(int N, int h_kv, int D, int max_blocks, int num_blocks, int block_size) {
-  if (N < 0 || N > 65535 || h_kv < 1 || h_kv > 65535 || max_blocks < 1 || num_blocks < 0) return GQA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
-  if (!block_size_ok(block_size)) return GQA_ERR_INVALID_ARG;
-  if ((int64_t)max_blocks * block_size >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
-  if ((int64_t)num_blocks * block_size >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
-  return GQA_OK;
-}
-
-gqa_status check_rows(int N, int T_q, int h_q, int h_kv, int D) {
-  if (N < 0 || N > 65535 || T_q < 1 || h_q < 1 || h_kv < 1 || h_kv > 65535 || h_q % h_kv != 0)
-    return GQA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
-  if ((int64_t)(h_q / h_kv) * T_q > 64) return GQA_ERR_UNSUPPORTED;
-  return GQA_OK;
-}
-
 // ---------------------------------------------------------------- decode
-// Kernel shapes: up to 8, 16, 24 or 32 query rows for one warp, 48 or 64 for two warps that share a ring.
-// 24 and 48 beside 32 and 64, measured (us, with / without): 131071 keys, 24 rows, d 128 56.6 / 67.7, in f16 65.5 / 85.3; 10
-// sequences of 5000-53000, 35 rows 136 / 175; 43 of 50-1460, 24 rows, d 64 27.8 / 31.4.
-int kv8_class(int rows) { return rows <= 32 ? (rows + 7) / 8 - 1 : (rows <= 48 ? 4 : 5); }
-int kv8_groups(int cls) { return cls < 4 ? kKv8Warps : kKv8Warps / 2; }
-
 template <int D, int NT, int RG, bool BF16>
 cudaError_t kv8_prepare() {
   constexpr int bytes = Kv8Cfg<D, NT, RG>::SMEM;
@@ -217,45 +147,6 @@ gqa_status kv8_device(int D, int cls, int bf16, int* sms) {
   }
   *sms = dev->sms;
   return GQA_OK;
-}
-
-// Workers for each unit from which the merge gives 32 columns of a row a CTA instead of a whole row a warp, as long as those
-// are no more than kMergeCtas.  Measured (us, columns a CTA / rows a warp; CTAs in brackets): 9 pieces, 16 sequences of
-// 250-500 keys, 8 KV heads 15.5 / 12.4; 19 pieces, 8 of 8000-16000 38.7 / 40.4 [1024], 64 of 16000-32000 with one KV head of
-// 4 query heads 67.3 / 69.4 [1024], of 16 79.2 / 75.3 [4096]; 38 pieces, 4 of 8000-16000 23.8 / 30.9 [512]; 64 rows of 30 of
-// 8000-16000, d 64, 54.2 / 51.6 [3840].
-constexpr int kManyPieces = 16;
-constexpr int kMergeCtas = 2048;
-
-// CTAs of a unit in the short kernel, a cluster of 1, 2, 4 or 8: the fewest that give each worker one tile, as far as all
-// units' clusters fit on three quarters of the SMs at once (a cluster lies in one GPC).  0: the general kernel, where a
-// worker would have more than kKv8Short tiles, or more than two above what the general kernel, which uses every SM,
-// gives one.  Measured (us of a replayed call, short / general; tiles of a worker in brackets): 8 KV heads of 128: one
-// sequence of 300 keys 5.3 / 7.6 [1, 1], 2000 5.7 / 7.6 [1, 1], 8000 8.9 / 8.9 [4, 2], 16000 13.1 / 11.0 [8, 4]; 4 of 500-1000
-// 6.5 / 9.6 [1, 1]; 16 of 1000-2000 13.0 / 17.0 [8, 7]; 2 KV heads of 64: 4096 keys 5.5 / 6.6 [2, 1], 16384 10.2 / 8.3 [8, 1].
-int kv8_short_ctas(int64_t units, int64_t seq_tiles, int sms, int groups) {
-  int ctas = 1;
-  while (ctas < 8 && ctas * groups < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;
-  const int64_t here = (seq_tiles + ctas * groups - 1) / (ctas * groups);
-  const int64_t there = (units * seq_tiles + sms * groups - 1) / (sms * groups);
-  if (units * ctas > sms || here > kKv8Short || here > there + 2) return 0;
-  return ctas;
-}
-
-struct Kv8Layout {
-  size_t splits, m, l, o, total;
-};
-
-// workspace: the status header, the units that are cut and two partials for each worker
-Kv8Layout kv8_layout(int workers, int rows, int D) {
-  Kv8Layout L;
-  const size_t n = 2 * (size_t)workers * rows;
-  L.splits = kHeaderBytes;
-  L.m = L.splits + align256((size_t)workers * sizeof(int4));
-  L.l = L.m + align256(n * 4);
-  L.o = L.l + align256(n * 4);
-  L.total = L.o + align256(n * D * 4);
-  return L;
 }
 
 template <int D, int NT, int RG, bool BF16>
@@ -404,7 +295,17 @@ size_t gqa_kv8_block_bytes(int block_size, int d_head) {
 gqa_status gqa_append(const gqa_append_args* args, void* workspace, size_t ws_bytes, void* stream) {
   try {
     if (args == nullptr) return GQA_ERR_INVALID_ARG;
-    return append_impl(*args, workspace, ws_bytes, stream);
+    return append_impl(*args, nullptr, 1, workspace, ws_bytes, stream);
+  } catch (...) {
+    return GQA_ERR_CUDA;
+  }
+}
+
+gqa_status gqa_append_axes(const gqa_append_args* args, const uint8_t* pair_axes, int num_axes, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  try {
+    if (args == nullptr) return GQA_ERR_INVALID_ARG;
+    return append_impl(*args, pair_axes, num_axes, workspace, ws_bytes, stream);
   } catch (...) {
     return GQA_ERR_CUDA;
   }

@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "gqa_kernels.cuh"
+#include "gqa_kv4.cuh"
 
 namespace gqa {
 
@@ -17,6 +18,7 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendCtas = 4;    // on an SM
 constexpr int kAppendIters = 4;   // groups of heads of a warp at most
 constexpr int kAppendRun = 4;     // tokens of a warp at most
+constexpr int kAppendAxes = 32;   // position axes at most: a lane each
 constexpr int kVllmShift = 16;    // tokens from which a CTA looks where its eights begin (fewer: a load's time is not worth it)
 constexpr int kReadThreads = 256;
 
@@ -114,6 +116,8 @@ struct AppendParams {
   uint32_t* status;
   int num_tokens, h_q, h_kv, max_position, rot_dim, interleaved, num_blocks, block_size, bs_log, q_sets, k_sets, iters, run;
   float eps;
+  const uint8_t* pair_axes;   // the axis of each of the rot_dim / 2 pairs, or NULL: all on axis 0
+  int num_axes;               // rows of positions
 };
 
 // CW neighbouring 16-bit elements: one 8- or 16-byte access
@@ -224,10 +228,11 @@ __device__ __forceinline__ void append_vllm_values(const AppendParams& a, int se
     const bool there = lane < 8 && t0 + lane >= 0 && t0 + lane < a.num_tokens;
     int64_t slot = there ? a.slots[t0 + lane] : -1;
     bool bad = slot >= rows;
-    if (a.cos_sin != nullptr && there) {
-      const int pos = a.positions[t0 + lane];
-      bad |= pos < 0 || pos >= a.max_position;
-    }
+    if (a.cos_sin != nullptr && there)
+      for (int axis = 0; axis < a.num_axes; ++axis) {
+        const int pos = a.positions[(int64_t)axis * a.num_tokens + t0 + lane];
+        bad |= pos < 0 || pos >= a.max_position;
+      }
     if (bad) {
       atomicOr(a.status, kDevBadInput);
       slot = -1;
@@ -257,6 +262,15 @@ __device__ __forceinline__ void append_vllm_values(const AppendParams& a, int se
   }
 }
 
+// Where the CW elements of a head from element e on are: (lane of the head's D/(2 CW) << 1) | which of its two chunks.
+template <int D, int CW>
+__device__ __forceinline__ int append_holder(int e, int rot) {
+  const bool turned = e < rot;
+  const int half = turned ? rot / 2 : (D - rot) / 2;
+  const int i = turned ? e : e - rot, j = i >= half;
+  return (((turned ? 0 : rot / 2) + i - j * half) / CW << 1) | j;
+}
+
 // A head's D elements lie on D/(2 CW) lanes, each with two chunks of CW: elements CW s.. and rot/2 + CW s.. for
 // the lanes s < rot/(2 CW) that rotate, so that both elements of every rotated pair (i, i + rot/2) are in one
 // thread and the rotation needs no exchange; the rest of the head (rot..D) is cut the same way.  A warp takes
@@ -267,7 +281,8 @@ __device__ __forceinline__ void append_vllm_values(const AppendParams& a, int se
 // the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
 // 16384 tokens of 64 + 8 + 8 heads of 128 take 105.3 us (6.45 TB/s, 0.95 of a copy's rate); 110.5 with one token a warp,
 // 117.9 with five CTAs an SM (48 registers) instead of four (64).
-template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT>
+// AXES: pairs turned by positions of several axes, a.pair_axes.
+template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT, bool AXES>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
 gqa_append_kernel(const AppendParams a) {
   constexpr int LPH = D / (2 * CW), HPW = 32 / LPH, WARPS = kAppendThreads / 32;
@@ -309,19 +324,64 @@ gqa_append_kernel(const AppendParams a) {
       for (int j = 0; j < 2; ++j) copy_chunk<CW>(&stage[it][j][threadIdx.x], src + it * (HPW * D) + off[j]);
     }
   };
+  // AXES: the axes of this lane's four pairs, a byte each; kNoAxis: some pair's axis is none of them.  A token's position on
+  // axis i is read by lane i (the others: on axis 0).
+  constexpr uint32_t kNoAxis = 0xffffffffu;
+  uint32_t pair_axes = 0;
+  if (AXES && rot) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t axis = 4 * lane < rot ? a.pair_axes[4 * lane % (rot / 2) + i] : 0;
+      bad |= axis >= (uint32_t)a.num_axes;
+      pair_axes |= (axis & 31u) << (8 * i);
+    }
+    if (__any_sync(0xffffffffu, bad)) pair_axes = kNoAxis;
+  }
+  auto position = [&](int64_t token) {
+    return a.positions[AXES ? (int64_t)(lane < a.num_axes ? lane : 0) * a.num_tokens + token : token];
+  };
   auto copy_turn = [&](int pos, int at) {   // the cosines and sines of a position; false: it is not in the table
-    if (pos >= 0 && pos < a.max_position) {
-      if (kind < 2 && 4 * lane < rot)
+    bool in = pos >= 0 && pos < a.max_position;
+    if (AXES) in = __all_sync(0xffffffffu, in) && pair_axes != kNoAxis;
+    if (in) {
+      if constexpr (AXES) {
+        int p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xffffffffu, pos, pair_axes >> (8 * i));
+        if (kind < 2 && 4 * lane < rot) {
+          const float* from = a.cos_sin + 4 * lane;
+          float* to = &turn_rows[warp][at][place];
+          if (pair_axes == (pair_axes & 0xffu) * 0x01010101u) {
+            copy_chunk<8>(reinterpret_cast<Chunk<8>*>(to), reinterpret_cast<const uint16_t*>(from + (int64_t)p[0] * rot));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(to + i)), "l"(from + (int64_t)p[i] * rot + i)
+                           : "memory");
+          }
+        }
+      } else if (kind < 2 && 4 * lane < rot) {
         copy_chunk<8>(reinterpret_cast<Chunk<8>*>(&turn_rows[warp][at][place]),
                       reinterpret_cast<const uint16_t*>(a.cos_sin + (int64_t)pos * rot + 4 * lane));
+      }
       return true;
     }
     if (lane == 0) atomicOr(a.status, kDevBadInput);
     return false;
   };
+  // the 4-bit cache: where the other elements of the sixteen of each chunk are, (lane << 1) | chunk
+  constexpr int OTHERS = 16 / CW - 1;
+  int holder[LAYOUT == 4 ? 2 : 1][OTHERS];
+  if constexpr (LAYOUT == 4) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < OTHERS; ++i) holder[j][i] = append_holder<D, CW>(off[j] ^ ((i + 1) * CW), rot) + 2 * (lane - sub);
+  }
   // the first token
   int64_t next_slot = kind != 0 ? a.slots[t] : -1;
-  int pos = rot ? a.positions[t] : 0, next_pos = rot && left > 1 ? a.positions[t + WARPS] : 0;
+  int pos = rot ? position(t) : 0, next_pos = rot && left > 1 ? position(t + WARPS) : 0;
 #pragma unroll
   for (int it = 0; it < kAppendIters; ++it)
     if (it < iters) copy_heads(it);
@@ -358,7 +418,7 @@ gqa_append_kernel(const AppendParams a) {
         copy_heads(it);
         if (it == 0 && rot) {
           next_ok = copy_turn(next_pos, flip ^ 1);
-          if (left > 2) next_pos = a.positions[t + 2 * WARPS];
+          if (left > 2) next_pos = position(t + 2 * WARPS);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -441,6 +501,38 @@ gqa_append_kernel(const AppendParams a) {
           }
           if (sub == 0) base[2 * a.block_size * D + (kind - 1) * a.block_size + row] = (uint8_t)e;
         }
+      } else if constexpr (LAYOUT == 4) {
+        uint32_t own[2] = {0u, 0u}, top[2];     // largest magnitudes, as bits: a NaN is the largest of all
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int i = 0; i < CW; ++i) own[j] = max(own[j], __float_as_uint(x[j][i]) & 0x7fffffffu);
+          top[j] = own[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < OTHERS; ++i) {
+            const uint32_t p = __shfl_sync(0xffffffffu, own[0], holder[j][i] >> 1);
+            const uint32_t n = __shfl_sync(0xffffffffu, own[1], holder[j][i] >> 1);
+            top[j] = max(top[j], holder[j][i] & 1 ? n : p);
+          }
+        const int bb = kv4_block_bytes(a.block_size, D);
+        const int64_t at = (blk * a.h_kv + h) * bb;
+        if (h < heads && idx_ok(at + bb - 1, (int64_t)a.num_blocks * a.h_kv * bb, a.status)) {
+          uint8_t* base = reinterpret_cast<uint8_t*>(a.k_cache) + at;
+          uint8_t* codes = base + (kind - 1) * a.block_size * (D / 2);
+          uint8_t* scales = base + a.block_size * D + ((kind - 1) * a.block_size + row) * (D / 16);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t byte = kv4_scale_byte(top[j]);
+            const float s = kv4_scale(byte);
+            uint8_t* to = codes + kv4_chunk<D>(row, off[j] >> 5) + ((off[j] & 31) >> 1);
+            if constexpr (CW == 8) *reinterpret_cast<uint32_t*>(to) = kv4_codes(x[j], s) | (kv4_codes(x[j] + 4, s) << 16);
+            else *reinterpret_cast<uint16_t*>(to) = (uint16_t)kv4_codes(x[j], s);
+            if (off[j] % 16 == 0) scales[off[j] / 16] = (uint8_t)byte;
+          }
+        }
       } else if (h < heads) {
         uint16_t* pool = reinterpret_cast<uint16_t*>(kind == 1 ? a.k_cache : a.v_cache);
         const int64_t size = (int64_t)a.num_blocks * a.block_size * a.h_kv * D;
@@ -457,6 +549,10 @@ gqa_append_kernel(const AppendParams a) {
     if (left == 1) return;
   }
 }
+
+// the launch, a translation unit for each d_head and type (gqa_append_inst.cuh)
+template <int D, bool BF16>
+cudaError_t append_run(const AppendParams& p, int layout, int sms, cudaStream_t st);
 
 // =====================================================================================
 // the 8-bit cache back to 16 bits

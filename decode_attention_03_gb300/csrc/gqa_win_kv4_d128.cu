@@ -1,0 +1,4 @@
+// Decode attention over the 4-bit cache, d_head 128, binary16.
+#include "gqa_win_inst.cuh"
+
+GQA_WIN_INSTANCE(128, true, false)

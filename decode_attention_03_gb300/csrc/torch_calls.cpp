@@ -8,6 +8,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <string>
@@ -134,10 +135,29 @@ int kv8_block_size(const at::Tensor& cache, int64_t h_kv, int64_t D, int dev) {
   return as_int(cache.size(2) / row, "the blocks of the cache");
 }
 
+// the same of a 4-bit cache
+int64_t kv4_row(int64_t D) { return D + D / 8; }
+int kv4_block_size(const at::Tensor& cache, int64_t h_kv, int64_t D, int dev) {
+  const int64_t row = kv4_row(D);
+  if (cache.scalar_type() != at::kByte || cache.dim() != 3 || !cache.is_cuda() || cache.get_device() != dev ||
+      !cache.is_contiguous() || (h_kv >= 0 && cache.size(1) != h_kv) || D < 16 || cache.size(2) % row != 0)
+    refuse("a 4-bit cache",
+           "a contiguous uint8 tensor (num_blocks, h_kv, block_size * (d_head + d_head / 8)) on the device of the others");
+  return as_int(cache.size(2) / row, "the blocks of the cache");
+}
+
+// Whether a uint8 cache is a 4-bit one: for the block sizes that there are, no size of a (block, head) is one of both caches.
+bool is_kv4(const at::Tensor& cache, int64_t D) {
+  if (cache.dim() != 3 || (D != 64 && D != 128)) return false;
+  for (int64_t bs = 8; bs <= 64; bs *= 2)
+    if (cache.size(2) == bs * kv4_row(D)) return true;
+  return false;
+}
+
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
 // append(q|None, k, v, h_q, h_kv, slots, k_cache, v_cache|None, positions|None, cos_sin|None, interleaved, q_weight|None,
-//        k_weight|None, eps, q_out|None, workspace|None) -> q_out or None, or a status
+//        k_weight|None, eps, q_out|None, workspace|None, pair_axes|None) -> q_out or None, or a status
 PyObject* append(PyObject* const* p) {
   const at::Tensor *q = optional(p[0], "q"), &k = tensor(p[1], "k"), &v = tensor(p[2], "v");
   if (k.dim() != 2 || !is_half(k)) refuse("k", "a float16 or bfloat16 CUDA tensor (tokens, h_kv*d_head)");
@@ -166,15 +186,26 @@ PyObject* append(PyObject* const* p) {
     }
     a.q_out = rows(*q_out, "q_out", type, dev, T, qc, &a.q_out_stride);
   }
+  const at::Tensor* axes_t = optional(p[16], "pair_axes");
+  const uint8_t* pair_axes = nullptr;
+  int axes = 1;
   if (const at::Tensor* cs = optional(p[9], "cos_sin")) {
     const at::Tensor* pos = optional(p[8], "positions");
     if (cs->dim() != 2 || pos == nullptr) refuse("cos_sin", "(max_position, rot_dim), and comes with positions");
     a.max_position = as_int(cs->size(0), "the rows of cos_sin");
     a.rot_dim = as_int(cs->size(1), "rot_dim");
     a.cos_sin = whole<float>(*cs, "cos_sin", at::kFloat, dev, {cs->size(0), cs->size(1)});
-    a.positions = whole<int32_t>(*pos, "positions", at::kInt, dev, {T});
+    if (axes_t != nullptr) {
+      if (pos->dim() != 2 || pos->size(0) < 1 || pos->size(0) > 32) refuse("positions", "(axes, tokens) with pair_axes, 1 to 32 axes");
+      axes = (int)pos->size(0);
+      pair_axes = whole<uint8_t>(*axes_t, "pair_axes", at::kByte, dev, {cs->size(1) / 2});
+      a.positions = whole<int32_t>(*pos, "positions", at::kInt, dev, {pos->size(0), T});
+    } else {
+      a.positions = whole<int32_t>(*pos, "positions", at::kInt, dev, {T});
+    }
     if (T == 0) a.positions = reinterpret_cast<const int32_t*>(a.cos_sin);   // (an empty tensor has no address; none is read)
   }
+  if (axes_t != nullptr && a.cos_sin == nullptr) throw Refused{"pair_axes comes with cos_sin and positions"};
   a.interleaved = truth(p[10], "interleaved");
   if (const at::Tensor* w = optional(p[11], "q_weight")) a.q_weight = whole<uint16_t>(*w, "q_weight", type, dev, {D});
   if (const at::Tensor* w = optional(p[12], "k_weight")) a.k_weight = whole<uint16_t>(*w, "k_weight", type, dev, {D});
@@ -182,9 +213,10 @@ PyObject* append(PyObject* const* p) {
   a.slots = whole<int64_t>(tensor(p[5], "slots"), "slots", at::kLong, dev, {T});
   const at::Tensor &kc_t = tensor(p[6], "k_cache"), *vc_t = optional(p[7], "v_cache");
   if (kc_t.scalar_type() == at::kByte) {
-    if (vc_t != nullptr) throw Refused{"an 8-bit cache holds K and V: pass no v_cache"};
-    a.cache_layout = GQA_CACHE_KV8;
-    a.block_size = kv8_block_size(kc_t, a.h_kv, D, dev);
+    const bool kv4 = is_kv4(kc_t, D);
+    if (vc_t != nullptr) throw Refused{kv4 ? "a 4-bit cache holds K and V: pass no v_cache" : "an 8-bit cache holds K and V: pass no v_cache"};
+    a.cache_layout = kv4 ? GQA_CACHE_KV4 : GQA_CACHE_KV8;
+    a.block_size = kv4 ? kv4_block_size(kc_t, a.h_kv, D, dev) : kv8_block_size(kc_t, a.h_kv, D, dev);
     a.k_cache = kc_t.data_ptr();
   } else {
     if (vc_t == nullptr) throw Refused{"a 16-bit cache needs k_cache and v_cache"};
@@ -208,7 +240,7 @@ PyObject* append(PyObject* const* p) {
   void* st = stream_of(dev);
   gqa_status s;
   Py_BEGIN_ALLOW_THREADS
-  s = gqa_append(&a, ws.at, ws.bytes, st);
+  s = gqa_append_axes(&a, pair_axes, axes, ws.at, ws.bytes, st);
   Py_END_ALLOW_THREADS
   if (s != GQA_OK) return PyLong_FromLong(s);
   if (q_out == nullptr) Py_RETURN_NONE;
@@ -265,12 +297,80 @@ PyObject* decode(PyObject* const* p) {
   return THPVariable_Wrap(std::move(made));
 }
 
+// window(q, k_pool or cache, v_pool|None, block_tables, seq_lens, h_q, h_kv, scale|None, window, sinks, causal, out|None,
+//        workspace, status|None, timeout_us, stall) -> out, or a status
+PyObject* window(PyObject* const* p) {
+  const at::Tensor& q = tensor(p[0], "q");
+  const int64_t dim = q.dim();
+  const int h_q = small(p[5], "h_q"), h_kv = small(p[6], "h_kv");
+  if (!is_half(q) || (dim != 2 && dim != 3) || !q.is_contiguous() || h_q < 1 || q.size(dim - 1) % h_q != 0)
+    refuse("q", "a contiguous float16 or bfloat16 CUDA tensor (N, h_q*d_head) or (N, T_q, h_q*d_head)");
+  const int dev = device_of(q, "q");
+  const int64_t N = q.size(0), T_q = dim == 3 ? q.size(1) : 1, D = q.size(dim - 1) / h_q;
+  const at::Tensor &k = tensor(p[1], p[2] == Py_None ? "cache" : "k_pool"), *v = optional(p[2], "v_pool");
+  const at::Tensor& tables = tensor(p[3], "block_tables");
+  int bs;
+  if (v == nullptr) {
+    bs = kv4_block_size(k, h_kv, D, dev);
+  } else {
+    if (k.dim() != 3) refuse("k_pool", "(num_blocks, block_size, h_kv*d_head)");
+    bs = as_int(k.size(1), "block_size");
+    whole<uint16_t>(k, "k_pool", q.scalar_type(), dev, {k.size(0), k.size(1), h_kv * D});
+    whole<uint16_t>(*v, "v_pool", q.scalar_type(), dev, {k.size(0), k.size(1), h_kv * D});
+  }
+  if (tables.dim() != 2) refuse("block_tables", "(N, max_blocks)");
+  const int64_t mb = tables.size(1);
+  const int32_t* tp = whole<int32_t>(tables, "block_tables", at::kInt, dev, {N, mb});
+  const int32_t* lp = whole<int32_t>(tensor(p[4], "seq_lens"), "seq_lens", at::kInt, dev, {N});
+  const float scale = p[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)real(p[7], "scale");
+  const int64_t win = integer(p[8], "window"), sinks = integer(p[9], "sinks");
+  if (win < 0 || sinks < 0) refuse(win < 0 ? "window" : "sinks", "0 or more");
+  const at::Tensor* out = optional(p[11], "out");
+  at::Tensor made;
+  if (out == nullptr) {
+    made = at::empty(q.sizes(), q.options());
+    out = &made;
+  } else if (out->scalar_type() != q.scalar_type() || !out->is_cuda() || out->get_device() != dev ||
+             out->sizes() != q.sizes() || !out->is_contiguous()) {
+    refuse("out", "like q");
+  }
+  gqa_options opt = {};
+  const int64_t limit = integer(p[14], "timeout_us");
+  if (limit < 0 || limit > UINT32_MAX) refuse("timeout_us", "a number of microseconds in 32 bits");
+  opt.timeout_us = (uint32_t)limit;
+  opt.test_stall_cta = small(p[15], "test_stall_cta");
+  opt.causal = truth(p[10], "causal");
+  opt.bf16 = q.scalar_type() == at::kBFloat16;
+  const Workspace ws = workspace(p[12], dev), status = status_word(p[13], dev);
+  if (status.bytes < 256) return PyLong_FromLong(GQA_ERR_WORKSPACE);
+  if (status.at == nullptr) return PyLong_FromLong(GQA_ERR_CUDA);
+  void* st = stream_of(dev);
+  const int n = as_int(N, "N"), t = as_int(T_q, "T_q"), blocks = as_int(mb, "max_blocks"),
+            nb = as_int(k.size(0), "num_blocks"), d = as_int(D, "d_head");
+  // (a sequence has fewer than 2^31 keys: larger numbers hide none, and keep all)
+  const int w = (int)std::min<int64_t>(win, INT32_MAX), keep = (int)std::min<int64_t>(sinks, INT32_MAX);
+  const uint16_t* qp = static_cast<const uint16_t*>(q.data_ptr());
+  uint16_t* op = static_cast<uint16_t*>(out->data_ptr());
+  gqa_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = v == nullptr ? gqa_decode_kv4(qp, k.data_ptr(), tp, lp, op, n, t, blocks, nb, bs, h_q, h_kv, d, scale, w, keep, ws.at,
+                                    ws.bytes, status.at, st, &opt)
+                   : gqa_decode_window(qp, static_cast<const uint16_t*>(k.data_ptr()),
+                                       static_cast<const uint16_t*>(v->data_ptr()), tp, lp, op, n, t, blocks, nb, bs, h_q, h_kv,
+                                       d, scale, w, keep, ws.at, ws.bytes, status.at, st, &opt);
+  Py_END_ALLOW_THREADS
+  if (s != GQA_OK) return PyLong_FromLong(s);
+  if (out != &made) return Py_NewRef(p[11]);
+  return THPVariable_Wrap(std::move(made));
+}
+
 // read(cache, block_tables, seq_lens, d_head, begins|None, k_out|None, v_out|None, workspace|None) -> a status
+template <bool KV4>
 PyObject* read(PyObject* const* p) {
   const at::Tensor &cache = tensor(p[0], "cache"), &tables = tensor(p[1], "block_tables");
   const int dev = device_of(cache, "cache");
   const int64_t D = integer(p[3], "d_head");
-  const int bs = kv8_block_size(cache, -1, D, dev);
+  const int bs = KV4 ? kv4_block_size(cache, -1, D, dev) : kv8_block_size(cache, -1, D, dev);
   if (tables.dim() != 2) refuse("block_tables", "(N, max_blocks)");
   const int64_t N = tables.size(0), mb = tables.size(1), h_kv = cache.size(1);
   const int32_t* tp = whole<int32_t>(tables, "block_tables", at::kInt, dev, {N, mb});
@@ -293,7 +393,8 @@ PyObject* read(PyObject* const* p) {
             heads = as_int(h_kv, "h_kv"), d = as_int(D, "d_head");
   gqa_status s;
   Py_BEGIN_ALLOW_THREADS
-  s = gqa_kv8_read(cache.data_ptr(), tp, lp, bp, kp, vp, num, n, blocks, nb, bs, heads, d, ws.at, ws.bytes, st, &opt);
+  s = (KV4 ? gqa_kv4_read : gqa_kv8_read)(cache.data_ptr(), tp, lp, bp, kp, vp, num, n, blocks, nb, bs, heads, d, ws.at, ws.bytes,
+                                          st, &opt);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(s);
 }
@@ -322,9 +423,11 @@ PyCFunction function() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<CALL, ARGS>));
 }
 
-PyMethodDef kMethods[] = {{"append", function<append, 16>(), METH_FASTCALL, nullptr},
+PyMethodDef kMethods[] = {{"append", function<append, 17>(), METH_FASTCALL, nullptr},
                           {"decode", function<decode, 13>(), METH_FASTCALL, nullptr},
-                          {"read", function<read, 8>(), METH_FASTCALL, nullptr},
+                          {"read", function<read<false>, 8>(), METH_FASTCALL, nullptr},
+                          {"read4", function<read<true>, 8>(), METH_FASTCALL, nullptr},
+                          {"window", function<window, 16>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -336,7 +336,7 @@ typedef struct {
   int rot_dim;              /* leading elements of a head that are rotated: a multiple of 8 up to d_head */
   int interleaved;          /* 0: element i turns with i + rot_dim/2; 1: element 2i with 2i + 1 */
   int num_blocks, block_size;
-  int cache_layout;         /* GQA_CACHE_* */
+  int cache_layout;         /* GQA_CACHE_* (kv4, like kv8, has one array) */
   int bf16;                 /* q, k, v, the weights, q_out and a 16-bit cache hold bfloat16 instead of binary16 */
   float eps;                /* of the norms, >= 0 */
 } gqa_append_args;
@@ -397,6 +397,70 @@ void* gqa_device_status(void);
  * begins and lengths outside the table are reported by gqa_workspace_check; the workspace is that status word
  * (256 zeroed bytes, or any workspace of this library).  gqa_options used: bf16. */
 gqa_status gqa_kv8_read(const void* cache, const int32_t* block_tables, const int32_t* seq_lens, const int32_t* begins,
+                        uint16_t* k_out, uint16_t* v_out, int num_seqs, int64_t out_len, int max_blocks_per_seq,
+                        int num_blocks, int block_size, int h_kv, int d_head, void* workspace, size_t ws_bytes,
+                        void* stream, const gqa_options* opt);
+
+/* ---------------------------------------------------------------- several position axes; the 4-bit cache; windows
+ * gqa_append_axes turns the pairs of a head by positions of several axes (time, height and width of pictures and videos),
+ * gqa_append and gqa_append_axes fill the 4-bit cache "kv4" too (GQA_CACHE_KV4), gqa_decode_kv4 attends to it and
+ * gqa_kv4_read gives it back in 16 bits.  gqa_decode_window attends to 16-bit pools; both see, where a window is given, only
+ * the newest keys and a few first ones.  These calls have no counterpart on the pages.
+ *
+ * kv4: one byte array (num_blocks, h_kv, block_bytes), block_bytes = block_size * (d_head + d_head / 8), block_size in
+ * {8, 16, 32, 64}.  A (block, head) holds
+ *   block_size rows of d_head / 2 bytes of K codes, block_size rows of V codes (element 2i of a row in the low four bits of
+ *   byte i, 2i + 1 in the high ones: sign and e2m1, the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6),
+ *   block_size rows of d_head / 16 K scales, block_size rows of V scales (one for 16 elements: the upper byte of a binary16
+ *   number whose lower byte is 0);
+ * the 16-byte chunk c of row r of the codes is stored at chunk c ^ (r / 2 % 4) of the row for d_head 128 and at chunk
+ * c ^ (r / 4 % 2) for d_head 64.  Sixteen elements with the largest magnitude m are stored with the scale s = m / 6, at most
+ * 10240, rounded to the nearest such number (ties to the even byte), and the codes of x / s (fp32), rounded to nearest, ties
+ * to the even code, beyond 6 saturated: magnitudes up to 61440 are held, and where m < 6 * 2^-17 zeros.  Sixteen elements
+ * with a NaN or an infinity among them are stored with the scale byte 0x7f and are read as NaN.  (Other scale bytes from 0x7c
+ * on are not written; they are no values.) */
+#define GQA_CACHE_KV4 4    /* for gqa_append: the 4-bit cache, K and V in one array */
+
+/* Bytes of one (block, head) of the 4-bit cache: block_size * (d_head + d_head / 8); 0 for a block size or d_head that it
+ * does not have. */
+size_t gqa_kv4_block_bytes(int block_size, int d_head);
+
+/* gqa_append with positions (num_axes, num_tokens) int32: pair i of a head's rotated pairs (i, i + rot_dim/2) or
+ * (2i, 2i + 1) is turned by cosine and sine i of the table's row positions[pair_axes[i]][t].  pair_axes (rot_dim / 2) bytes
+ * in device memory; 1 <= num_axes <= 32; pair_axes NULL: num_axes is 1 and all pairs are on axis 0 (gqa_append).  Every
+ * axis' position of a token has to lie in the table, whether a pair uses it or not, and a byte of pair_axes beyond the axes
+ * is reported like a position outside the table, for all tokens. */
+gqa_status gqa_append_axes(const gqa_append_args* args, const uint8_t* pair_axes, int num_axes, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Workspace bytes of gqa_decode_kv4 (cache_layout GQA_CACHE_KV4) and gqa_decode_window (GQA_CACHE_ROWS) on the current
+ * device; 0 on invalid arguments or when no device is usable. */
+size_t gqa_decode_window_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, int d_head, int cache_layout);
+
+/* Decode step over the 4-bit cache: arguments, conventions, reports and the workspace's use as gqa_decode_kv8, and
+ *   window  0: every key is visible; else the token at place p of its sequence (len - T_q + t for token t with
+ *           gqa_options.causal, else len - 1) sees the keys j with p - window < j <= p, and
+ *   sinks   the keys j < sinks up to its own place, whatever the window (not used without one).
+ * Blocks none of whose keys any token sees are neither read nor looked up: their entries of the table may be anything.
+ * What a hidden key holds, NaN and infinities too, reaches no output.  A token that sees no key gets O = 0.
+ * status: where the call reports (256 zeroed bytes, any workspace of this library, or gqa_device_status); NULL: the
+ * workspace, whose first 256 bytes have to be zero then.
+ * A key's weight is rounded to 11 bits (f16 calls: 22), or to within 2^-36 of its row's largest where it is very small. */
+gqa_status gqa_decode_kv4(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
+                          uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
+                          int h_q, int h_kv, int d_head, float scale, int window, int sinks, void* workspace,
+                          size_t ws_bytes, void* status, void* stream, const gqa_options* opt);
+
+/* The same over the pools of gqa_decode_paged, (num_blocks, block_size, h_kv*d_head) of q's type each.  Window 0 is full
+ * attention: T_q > 1 new tokens over a paged cache.  A key's weight is rounded to 22 bits (bf16 calls: 16). */
+gqa_status gqa_decode_window(const uint16_t* q, const uint16_t* k_pool, const uint16_t* v_pool, const int32_t* block_tables,
+                             const int32_t* seq_lens, uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq,
+                             int num_blocks, int block_size, int h_q, int h_kv, int d_head, float scale, int window,
+                             int sinks, void* workspace, size_t ws_bytes, void* status, void* stream,
+                             const gqa_options* opt);
+
+/* gqa_kv8_read of the 4-bit cache: every value it holds is a binary16 and a bfloat16 number, so nothing is rounded. */
+gqa_status gqa_kv4_read(const void* cache, const int32_t* block_tables, const int32_t* seq_lens, const int32_t* begins,
                         uint16_t* k_out, uint16_t* v_out, int num_seqs, int64_t out_len, int max_blocks_per_seq,
                         int num_blocks, int block_size, int h_kv, int d_head, void* workspace, size_t ws_bytes,
                         void* stream, const gqa_options* opt);
