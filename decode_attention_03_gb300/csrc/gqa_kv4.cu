@@ -48,7 +48,7 @@ gqa_status win_device(bool kv4, int D, int cls, bool bf16, int* sms) {
 }
 
 // ---------------------------------------------------------------- decode
-int win_groups(bool kv4, int cls) { return (kv4 ? win_warps<true>() : win_warps<false>()) / (cls < 4 ? 1 : 2); }
+int win_groups(bool kv4, int cls) { return kv4 ? win_workers<true>(cls) : win_workers<false>(cls); }
 
 template <int D, bool KV4, bool BF16>
 cudaError_t win_decode(const WinParams& p, int cls, unsigned grid, bool cut, bool many_pieces, cudaStream_t st) {
@@ -69,11 +69,22 @@ cudaError_t win_decode_type(const WinParams& p, int cls, bool bf16, unsigned gri
 
 // Tiles of a sequence that can be visible: what the table holds, or the sinks' and those that a stretch of the window and the
 // other new tokens' places can touch.
-int64_t most_tiles(int64_t keys, int window, int sink_tiles, int new_tokens) {
-  const int64_t all = (keys + kKv8Keys - 1) / kKv8Keys;
+int64_t most_tiles(int64_t keys, int tile, int window, int sink_tiles, int new_tokens) {
+  const int64_t all = (keys + tile - 1) / tile;
   if (window == 0) return all;
-  const int64_t some = sink_tiles + ((int64_t)window + new_tokens - 1 + kKv8Keys - 2) / kKv8Keys + 1;
+  const int64_t some = sink_tiles + ((int64_t)window + new_tokens - 1 + tile - 2) / tile + 1;
   return some < all ? some : all;
+}
+
+// CTAs of a unit in the short kernel, as kv8_short_ctas: a cluster of 1, 2, 4 or 8, the fewest that give each worker one
+// tile; at most `most` tiles a worker.  0: the general kernel.
+int win_short_ctas(int64_t units, int64_t seq_tiles, int sms, int groups, int most) {
+  int ctas = 1;
+  while (ctas < 8 && ctas * groups < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;
+  const int64_t here = (seq_tiles + ctas * groups - 1) / (ctas * groups);
+  const int64_t there = (units * seq_tiles + sms * groups - 1) / (sms * groups);
+  if (units * ctas > sms || here > most || here > there + 2) return 0;
+  return ctas;
 }
 
 struct WinCall {
@@ -96,7 +107,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
   if (s == GQA_OK) s = check_kv8(c.N, c.h_kv, c.D, c.max_blocks, c.num_blocks, c.block_size);
   if (s != GQA_OK) return s;
   if (!std::isfinite(c.scale) || c.window < 0 || c.sinks < 0) return GQA_ERR_INVALID_ARG;
-  if ((int64_t)(c.N < kKv8Seqs ? c.N : kKv8Seqs) * c.T_q * c.h_q >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
+  if ((int64_t)(c.N < kWinSeqs ? c.N : kWinSeqs) * c.T_q * c.h_q >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;
   if (c.N == 0) return GQA_OK;
   void* status = c.status != nullptr ? c.status : c.ws;
   if (!aligned16(c.q) || !aligned16(c.o) || !aligned16(c.ws) || !aligned16(status) || !aligned_to(c.tables, 4) ||
@@ -104,6 +115,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
     return GQA_ERR_INVALID_ARG;
   if (c.ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
   const int rows = c.h_q / c.h_kv * c.T_q, cls = kv8_class(rows), groups = win_groups(kv4, cls);
+  const int tile = kv4 ? win_tile_keys<true>(cls) : win_tile_keys<false>(cls);
   int sms = 0;
   if ((s = win_device(kv4, c.D, cls, bf16, &sms)) != GQA_OK) return s;
   const Kv8Layout lay = kv8_layout(sms * groups, rows, c.D);
@@ -121,7 +133,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
   p.T_q = c.T_q; p.h_q = c.h_q; p.h_kv = c.h_kv; p.G = c.h_q / c.h_kv; p.rows = rows;
   p.max_blocks = c.max_blocks; p.num_blocks = c.num_blocks; p.block_size = c.block_size;
   p.bs_log = log2_of(c.block_size);
-  p.ids_log = p.bs_log < 5 ? 5 - p.bs_log : 0;
+  p.ids_log = c.block_size < tile ? log2_of(tile) - p.bs_log : 0;
   p.causal = opt.causal ? 1 : 0;
   p.stall = opt.test_stall_cta;
   p.scale_log2 = c.scale * kLog2e;
@@ -130,12 +142,12 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
   const int64_t keys = (int64_t)c.max_blocks * c.block_size;
   p.window = c.window < keys ? c.window : 0;
   p.sinks = p.window == 0 ? 0 : c.sinks;
-  p.sink_tiles = (int)(((int64_t)p.sinks + kKv8Keys - 1) / kKv8Keys);
+  p.sink_tiles = (int)(((int64_t)p.sinks + tile - 1) / tile);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(c.stream);
-  const int64_t seq_tiles = most_tiles(keys, p.window, p.sink_tiles, p.causal ? c.T_q : 1);
+  const int64_t seq_tiles = most_tiles(keys, tile, p.window, p.sink_tiles, p.causal ? c.T_q : 1);
   std::lock_guard<std::mutex> turn(turn_of(c.ws));
-  for (int b0 = 0; b0 < c.N; b0 += kKv8Seqs) {
-    p.N = c.N - b0 < kKv8Seqs ? c.N - b0 : kKv8Seqs;
+  for (int b0 = 0; b0 < c.N; b0 += kWinSeqs) {
+    p.N = c.N - b0 < kWinSeqs ? c.N - b0 : kWinSeqs;
     p.q = c.q + (int64_t)b0 * c.T_q * c.h_q * c.D;
     p.o = c.o + (int64_t)b0 * c.T_q * c.h_q * c.D;
     p.block_tables = c.tables + (int64_t)b0 * c.max_blocks;
@@ -145,7 +157,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
     unsigned grid = units * seq_tiles < sms ? (unsigned)(units * seq_tiles) : (unsigned)sms;
     if (units * seq_tiles / ((int64_t)grid * groups) >= (int64_t(1) << 31)) return GQA_ERR_INVALID_ARG;   // tiles of a worker
     // few units of few tiles a worker: one launch of clusters
-    p.ctas = kv8_short_ctas(units, seq_tiles, sms, groups);
+    p.ctas = win_short_ctas(units, seq_tiles, sms, groups, kKv8Short < 32 >> p.ids_log ? kKv8Short : 32 >> p.ids_log);
     if (p.ctas > 0) grid = (unsigned)(units * p.ctas);
     p.workers = (int)grid * groups;
     const bool many = p.workers / units >= kManyPieces && units * rows * (c.D / 32) <= kMergeCtas;

@@ -9,8 +9,9 @@
 // kernels share: the cut looks at no sequence, and the same call gives the same bits.
 //
 // A worker is one warp (two that share a ring for more than 32 query rows) with a ring of its own in shared memory, filled
-// by one bulk copy for each block of the 4-bit cache, and by 16-byte asynchronous copies from the 16-bit pools, whose rows
-// of a head lie apart.
+// by one bulk copy for each block of the 4-bit cache, and by 16-byte asynchronous copies from the 16-bit pools, whose rows of a
+// head lie apart: a bulk copy for each row costs its lane's turn in a loop over the lanes (64 keys' rows, four warps on an SM:
+// 322 us instead of 206 for 64 sequences under a window of 4096).
 //
 // Arithmetic of a warp, for its 8 NT query rows and the 32 keys of a tile: S^T = K Q^T and O^T += V^T P^T by mma.sync, keys
 // and columns on the M side, query rows on the N side.  kv4: a code becomes f16 by one conversion for two of them, and is
@@ -25,6 +26,8 @@
 
 namespace gqa {
 
+constexpr int kWinSeqs = 768;      // sequences of a launch (the host splits larger batches): what the rings leave room for
+
 struct WinParams : Kv8Params {
   const uint16_t *k_pool, *v_pool;   // 16-bit pools; the 4-bit cache is `cache`
   int window;                        // 0: none
@@ -32,29 +35,39 @@ struct WinParams : Kv8Params {
   int ids_log;                       // log2 of the block ids of a tile
 };
 
+// Keys of a tile: 64 where the registers allow it (two independent halves, and half the work around a tile: 12 warps with
+// two tiles of 64 keys 100.8 us instead of 119 for 64 sequences of 1K-16K keys over the 4-bit cache, 16 query rows of 64
+// sequences 164 instead of 182), 32 otherwise, and for 16 bits, whose rows fill the ring (d_head 64: no faster with 64).
+template <bool KV4, int NT>
+constexpr int win_keys = KV4 && NT <= 2 ? 64 : 32;
+
 template <int D, int NT, int RG, bool KV4>
 struct WinCfg {
-  static constexpr int WARPS = KV4 ? 8 : 4;
+  static constexpr int WARPS = NT == 1 ? 12 : 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int GROUPS = WARPS / RG;
-  static constexpr int TILE = kKv8Keys * (KV4 ? D + D / 8 : 4 * D);
-  static constexpr bool Q_SMEM = NT > 2;                              // query fragments in shared memory, else in registers
+  static constexpr int KEYS = win_keys<KV4, NT>;                   // of a tile: one or two of 32, laid out one after the other
+  static constexpr int TILE = KEYS * (KV4 ? D + D / 8 : 4 * D);
+  static constexpr bool Q_SMEM = NT > 2 || (KV4 && NT == 2);          // query fragments in shared memory, else in registers
   static constexpr int QUERIES = Q_SMEM ? 8 * NT * (D * 2 + 4) : 0;   // of a warp, and its rows' factors
   static constexpr int PREFIX_OFF = 0;
-  static constexpr int LENS_OFF = (kKv8Seqs + 2) * 8;
-  static constexpr int SUMS_OFF = LENS_OFF + kKv8Seqs * 4;
+  static constexpr int LENS_OFF = (kWinSeqs + 2) * 8;
+  static constexpr int SUMS_OFF = LENS_OFF + kWinSeqs * 4;
   static constexpr int FLAG_OFF = SUMS_OFF + WARPS * 8;
   static constexpr int BAR_OFF = FLAG_OFF + 16;
-  static constexpr int DEPTH = KV4 ? 4 : (NT > 2 ? 2 : 3);            // tiles of a warp in flight, at d_head 128
-  static constexpr int STAGES = DEPTH * (128 / D) * RG;
+  // Tiles of a warp in the ring.  The 4-bit cache takes two (NT > 2: four, of 32 keys).  16 bits: one, and the other warps
+  // compute while it comes (12 warps with one tile of 32 keys 165 us instead of 206 with 4 warps and three, 64 sequences
+  // under a window of 4096).
+  static constexpr int DEPTH = KV4 ? (NT > 2 ? 4 : 2) * 128 / D : 128 / D;
+  static constexpr int STAGES = DEPTH * RG;
   static constexpr int Q_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
   static constexpr int ML_OFF = Q_OFF + WARPS * QUERIES;
   static constexpr int RING_OFF = (ML_OFF + WARPS * 8 * NT * 8 + 127) & ~127;
   static constexpr int SMEM = RING_OFF + GROUPS * STAGES * TILE;
   static constexpr int AREA = STAGES * TILE / RG;                     // a warp's part of the ring: holds its O there
-  static constexpr int FULL = KV4 ? 1 : 32;                           // arrivals at a full barrier: the lane that expects, or all
   static_assert(GROUPS * STAGES <= THREADS && SMEM <= 232448 && AREA >= 8 * NT * D * 4 && AREA % 16 == 0, "ring");
-  static_assert(GROUPS <= 8, "the fold of a CTA's workers");
+  static constexpr int FULL = KV4 ? 1 : 32;                           // arrivals at a full barrier: the lane that expects, or all
+  static constexpr int FOLD = GROUPS > 8 ? GROUPS : 8;                // states that one fold takes: a CTA's workers, a cluster's CTAs
 };
 
 // log2 of what a weight is multiplied by: its f16 is at most 2^15
@@ -67,25 +80,43 @@ struct WinSpan {
   int first, skip, tiles;
 };
 
+template <int K>
 __device__ __forceinline__ WinSpan win_span(const WinParams& a, int len) {
-  WinSpan s = {0, 0, (int)(((int64_t)len + kKv8Keys - 1) / kKv8Keys)};
+  WinSpan s = {0, 0, (int)(((int64_t)len + K - 1) / K)};
   if (a.window > 0) {
     const int64_t first = (int64_t)len - (a.causal ? a.T_q : 1) - a.window + 1;
     if (first > 0) {
       s.first = (int)first;
-      s.skip = max(s.first / kKv8Keys - a.sink_tiles, 0);
+      s.skip = max(s.first / K - a.sink_tiles, 0);
       s.tiles -= s.skip;
     }
   }
   return s;
 }
 
+// The tiles [from, from + count) of a unit, as it numbers them, of which every token sees every key.
+struct WinClear {
+  int from;
+  uint32_t count;
+  __device__ __forceinline__ bool has(int t) const { return (uint32_t)(t - from) < count; }
+};
+
+template <int K>
+__device__ __forceinline__ WinClear win_clear_tiles(const WinParams& a, int len, int skip) {
+  const int last = a.causal ? len - a.T_q : len - 1;         // the oldest token's place
+  const int end = last >= 0 ? (int)(((int64_t)last + 1) / K) : 0;
+  int from = 0;
+  if (a.window > 0 && len > a.window && len - a.window > a.sinks)   // the newest token's oldest key
+    from = (int)(((int64_t)len - a.window + K - 1) / K);
+  return {from - skip, (uint32_t)max(end - from, 0)};
+}
+
 __device__ __forceinline__ int win_tile_of(const WinParams& a, int skip, int t) { return t < a.sink_tiles ? t : t + skip; }
 
 // Tiles (of one head) before each sequence of the launch, in shared memory.
-template <int THREADS>
+template <int K, int THREADS>
 __device__ __forceinline__ void win_prefix(const WinParams& a, int64_t* prefix, int* lens, int64_t* sums) {
-  constexpr int PER = kKv8Seqs / THREADS;
+  constexpr int PER = (kWinSeqs + THREADS - 1) / THREADS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t cap = (int64_t)a.max_blocks * a.block_size;
   int64_t v[PER], run = 0;
@@ -97,8 +128,8 @@ __device__ __forceinline__ void win_prefix(const WinParams& a, int64_t* prefix, 
       if (blockIdx.x == 0) atomicOr(a.status, kDevBadInput);
       len = len < 0 ? 0 : (int)cap;
     }
-    lens[b] = len;
-    run += win_span(a, len).tiles;
+    if (b < kWinSeqs) lens[b] = len;
+    run += win_span<K>(a, len).tiles;
     v[i] = run;
   }
   int64_t incl = run;
@@ -140,60 +171,71 @@ struct WinStream {
   Kv8Place ahead;    // first tile after the current window
   int id, id_next;   // this lane's block id in the current window and the one after it (-1: no block, or a bad id)
   bool want, want_next;   // the lane has a block that some token sees
-  int len, skip;     // of at's sequence
+  int len, skip, first;   // of at's sequence
   int t_end;         // tile of at's unit where the current window ends
   int k;             // at's place in the window
+  bool all;          // every block of the window that some token sees has a good id
   // kv4, the same for every tile: lanes 0 .. n - 1 copy `size` bytes from `off` of a (block, head) to `to` of the tile,
-  // + step in the second half of a block of 64
+  // + step in the second half of a block of 64; `head` is `off` in head at.g of block 0, `stride` the bytes of a block
+  const uint8_t* head;
   int n;
-  uint32_t size, to, off, step;
+  uint32_t size, to, off, step, stride;
 };
 
-template <int D, bool KV4>
+template <int D, bool KV4, int K>
 __device__ __forceinline__ void win_stream_setup(WinStream& s, const WinParams& a, int lane) {
+  s.off = 0;
   if constexpr (KV4) {
     const int bs = a.block_size, bb = kv4_block_bytes(bs, D);
-    if (bs <= kKv8Keys) {        // whole blocks
-      s.n = kKv8Keys >> a.bs_log;
+    s.stride = (uint32_t)a.h_kv * (uint32_t)bb;
+    if (bs <= 32) {              // whole blocks
+      s.n = K >> a.bs_log;
       s.size = bb;
       s.to = lane * bb;
       s.off = s.step = 0;
-    } else {                     // half a block: K codes, V codes, K scales, V scales
-      const bool codes = lane < 2;
-      s.n = 4;
-      s.size = s.step = kKv8Keys * (codes ? D / 2 : D / 16);
-      s.to = codes ? lane * s.size : kKv8Keys * D + (lane - 2) * s.size;
-      s.off = codes ? lane * bs * (D / 2) : bs * D + (lane - 2) * bs * (D / 16);
+    } else {                     // half a block, or each half: K codes, V codes, K scales, V scales
+      const int part = lane & 3, h = lane >> 2;
+      const bool codes = part < 2;
+      s.n = K / 8;
+      s.size = s.step = 32 * (codes ? D / 2 : D / 16);
+      s.to = h * 32 * (D + D / 8) + (codes ? part * s.size : 32 * D + (part - 2) * s.size);
+      s.off = (codes ? part * bs * (D / 2) : bs * D + (part - 2) * bs * (D / 16)) + h * s.size;
     }
   }
 }
 
 // this lane's block id of the window that starts at p
+template <int K>
 __device__ __forceinline__ int win_ids(const WinParams& a, const Kv8Place& p, int len, bool& want, int lane) {
-  const WinSpan span = win_span(a, len);
+  const WinSpan span = win_span<K>(a, len);
   const int t = p.t + (lane >> a.ids_log), tile = win_tile_of(a, span.skip, t);
-  const int64_t j = a.block_size <= kKv8Keys ? ((int64_t)tile << a.ids_log) + (lane & ((1 << a.ids_log) - 1)) : tile >> 1;
+  const int64_t j = a.block_size <= K ? ((int64_t)tile << a.ids_log) + (lane & ((1 << a.ids_log) - 1)) : tile >> 1;
   const int64_t key = j << a.bs_log, end = key + a.block_size;
   want = t < p.tiles && key < len && (key < a.sinks || end > span.first) &&
          idx_ok((int64_t)p.b * a.max_blocks + j, (int64_t)a.N * a.max_blocks, a.status);
   return want ? __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + j) : -1;
 }
 
+template <int D>
 __device__ __forceinline__ void win_ids_check(WinStream& s, const WinParams& a) {
+  s.head = a.cache + (int64_t)s.at.g * kv4_block_bytes(a.block_size, D) + s.off;
   if (s.want && (s.id < 0 || s.id >= a.num_blocks)) {
     atomicOr(a.status, kDevBadInput);
     s.id = -1;
   }
   s.k = 0;
+  s.all = __all_sync(0xffffffffu, s.id >= 0);
 }
 
 // Enters the window at s.at, whose ids are in s.id: reports bad ids, finds where the next window begins and starts
 // loading its ids.
-template <int D>
+template <int D, int K>
 __device__ __forceinline__ void win_enter(WinStream& s, const WinParams& a, const int64_t* prefix, const int* lens, int lane) {
   s.len = lens[s.at.b];
-  s.skip = win_span(a, s.len).skip;
-  win_ids_check(s, a);
+  const WinSpan span = win_span<K>(a, s.len);
+  s.skip = span.skip;
+  s.first = span.first;
+  win_ids_check<D>(s, a);
   s.t_end = min(s.at.tiles, s.at.t + (32 >> a.ids_log));
   s.ahead = s.at;
   s.ahead.t = s.t_end;
@@ -208,46 +250,54 @@ __device__ __forceinline__ void win_enter(WinStream& s, const WinParams& a, cons
               a.q + (((int64_t)s.ahead.b * a.T_q + t) * a.h_q + (int64_t)s.ahead.g * a.G) * D) + i));
   }
   s.want_next = false;
-  s.id_next = s.ahead.b < a.N ? win_ids(a, s.ahead, lens[s.ahead.b], s.want_next, lane) : -1;
+  s.id_next = s.ahead.b < a.N ? win_ids<K>(a, s.ahead, lens[s.ahead.b], s.want_next, lane) : -1;
 }
 
 // Copies the stream's next tile to `dst`; on to the next tile of the window (true: the window ends).  Every lane of the
 // warp calls this.
-template <int D, bool KV4>
+template <int D, bool KV4, int K>
 __device__ __forceinline__ bool win_issue(WinStream& s, const WinParams& a, uint32_t dst, uint32_t bar, uint64_t policy,
                                           int lane, const Win& ring) {
-  const bool half = a.block_size > kKv8Keys;
+  const bool half = a.block_size > 32;       // the 32 rows of a copy are a part of a block
   const int tile = win_tile_of(a, s.skip, s.at.t);
   if constexpr (KV4) {
     const int id = __shfl_sync(0xffffffffu, s.id, ((s.k << a.ids_log) + (half ? 0 : lane)) & 31);
     const bool go = lane < s.n && id >= 0;
-    const uint32_t went = __popc(__ballot_sync(0xffffffffu, go));
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, half ? (went ? kKv8Keys * (D + D / 8) : 0) : went * s.size);
+    uint32_t bytes = K * (D + D / 8);
+    if (!s.all) {
+      const uint32_t went = __popc(__ballot_sync(0xffffffffu, go));
+      if (!half || went == 0) bytes = went * s.size;
+    }
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
     if (go) {
-      const int bb = kv4_block_bytes(a.block_size, D);
-      const uint8_t* src = a.cache + ((int64_t)id * a.h_kv + s.at.g) * bb + s.off + (tile & 1) * s.step;
-      if (idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * a.h_kv * bb, a.status) &&
+      const uint8_t* src = s.head + (uint64_t)(uint32_t)id * s.stride + (K == 32 ? (tile & 1) * s.step : 0u);
+      if (idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status) &&
           smem_ok(dst + s.to, s.size, ring.lo, ring.hi, ring.status))
         bulk_load(dst + s.to, src, s.size, bar, policy);
     }
   } else {
     constexpr int CH = D / 8, KEYS = 32 / CH;     // chunks of a row; keys that the lanes copy at once
-    const int valid = s.len - tile * kKv8Keys, first = half ? (tile & 1) * kKv8Keys : 0, c = lane % CH;
-    const int64_t rows = (int64_t)a.num_blocks * a.block_size;
-#pragma unroll 4
-    for (int i = 0; i < CH; ++i) {
-      const int key = i * KEYS + lane / CH;
-      const int id = __shfl_sync(0xffffffffu, s.id, ((s.k << a.ids_log) + (half ? 0 : key >> a.bs_log)) & 31);
-      const int64_t row = (int64_t)id * a.block_size + (half ? first + key : key & (a.block_size - 1));
-      const int64_t at = (row * a.h_kv + s.at.g) * D + 8 * c;
-      const uint32_t to = dst + key * (2 * D) + ((c ^ (key & 7)) << 4);
-      if (id >= 0 && key < valid && idx_ok(at + 7, rows * a.h_kv * D, a.status) &&
-          smem_ok(to, kKv8Keys * 2 * D + 16, ring.lo, ring.hi, ring.status)) {
-        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(a.k_pool + at), "l"(policy)
-                     : "memory");
-        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to + kKv8Keys * 2 * D),
-                     "l"(a.v_pool + at), "l"(policy)
-                     : "memory");
+    const int key0 = tile * K, first = a.block_size > K ? (tile & 1) * K : 0, c = lane % CH;
+    const int valid = s.len - key0, sinks = a.sinks - key0, old = s.first - key0;
+    const bool whole = valid >= K && (old <= 0 || sinks >= K);
+    const int64_t row = (int64_t)a.h_kv * D, apart = a.v_pool - a.k_pool;
+#pragma unroll
+    for (int o = 0; o < K / 8; ++o) {       // eight keys lie in one block
+      const int id = __shfl_sync(0xffffffffu, s.id, ((s.k << a.ids_log) + (8 * o >> a.bs_log)) & 31);
+      const int r = lane / CH + ((first + 8 * o) & (a.block_size - 1));
+      const uint16_t* from = a.k_pool + ((int64_t)id * a.block_size + r) * row + s.at.g * D + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 8 / KEYS; ++i, from += KEYS * row) {
+        const int key = 8 * o + i * KEYS + lane / CH;
+        const uint32_t to = dst + key * (2 * D) + ((c ^ (key & 7)) << 4);
+        if (id >= 0 && (whole || (key < valid && (key >= old || key < sinks))) &&
+            idx_ok(from + 7 - a.k_pool, (int64_t)a.num_blocks * a.block_size * row, a.status) &&
+            smem_ok(to, K * 2 * D + 16, ring.lo, ring.hi, ring.status)) {
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to + K * 2 * D),
+                       "l"(from + apart), "l"(policy)
+                       : "memory");
+        }
       }
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -258,14 +308,14 @@ __device__ __forceinline__ bool win_issue(WinStream& s, const WinParams& a, uint
 }
 
 // the same, and on to the next window
-template <int D, bool KV4>
+template <int D, bool KV4, int K>
 __device__ __forceinline__ void win_copy(WinStream& s, const WinParams& a, const int64_t* prefix, const int* lens, uint32_t dst,
                                          uint32_t bar, uint64_t policy, int lane, const Win& ring) {
-  if (!win_issue<D, KV4>(s, a, dst, bar, policy, lane, ring)) return;
+  if (!win_issue<D, KV4, K>(s, a, dst, bar, policy, lane, ring)) return;
   s.at = s.ahead;
   s.id = s.id_next;
   s.want = s.want_next;
-  if (s.at.b < a.N) win_enter<D>(s, a, prefix, lens, lane);
+  if (s.at.b < a.N) win_enter<D, K>(s, a, prefix, lens, lane);
 }
 
 // ---------------------------------------------------------------- the computing side
@@ -273,40 +323,64 @@ __device__ __forceinline__ void win_copy(WinStream& s, const WinParams& a, const
 template <int D, int NT, int RG, bool KV4>
 struct WinWarp {
   static constexpr int KD = D / 16;
-  static constexpr bool Q_SMEM = NT > 2;
+  static constexpr bool Q_SMEM = WinCfg<D, NT, RG, KV4>::Q_SMEM;
   uint32_t qf[Q_SMEM ? 1 : NT][Q_SMEM ? 1 : KD][2];   // Q^T fragments, or, in shared memory at q_at, [KD][NT][lane] ...
   float qs[Q_SMEM ? 1 : NT][2];                       // ... followed by the rows' factors
   uint32_t q_at;
   float acc[KD][NT][4];
   float m[NT][2], l[NT][2];
   // the same for every unit and tile
-  uint32_t octet[4];    // kv4: byte offset in a tile of the block that holds keys 8o .. 8o + 7, and of ...
-  uint32_t row[4];      // ... the first of them among that block's rows
-  uint32_t k_at, v_at;  // this lane's place: of its part of a K row, of its row of V for ldmatrix (without the swizzled chunk)
+  // byte offsets in a tile.  kv4: this lane's part of the K rows 8o + lane / 4 and their scales, from which the scales of
+  // the V rows 8o + 2 (lane % 4) are v_scale away, and its rows of V for ldmatrix (without the swizzled chunk); 16 bits:
+  // k_at[0] and v_at[0], of the first sixteen keys
+  uint32_t k_at[KV4 ? 4 : 1], k_scale[KV4 ? 4 : 1], v_at[KV4 ? 2 : 1], v_scale;
   uint32_t k_turn, v_turn;
   uint32_t pick[2];
 };
 
+// a value that stays in its register
+__device__ __forceinline__ void win_keep(uint32_t& x) { asm volatile("" : "+r"(x)); }
+
 template <int D, int NT, int RG, bool KV4>
 __device__ __forceinline__ void win_setup(WinWarp<D, NT, RG, KV4>& w, const WinParams& a, uint32_t q_at, int lane) {
-  w.q_at = q_at;
+  w.q_at = q_at + lane * 8;
   const int r = lane >> 2, c = lane & 3, q = lane >> 3, i = lane & 7;
   if constexpr (KV4) {
-    const int eb = min(a.block_size, kKv8Keys);
+    const int eb = min(a.block_size, 32), bb = kv4_block_bytes(eb, D);
+    const int part = D == 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 32 + (((c >> 1) ^ ((r >> 2) & 1)) << 4) + (c & 1) * 8;
 #pragma unroll
     for (int o = 0; o < 4; ++o) {
-      w.octet[o] = 8 * o / eb * kv4_block_bytes(eb, D);
-      w.row[o] = 8 * o % eb;
+      const int block = 8 * o / eb * bb, row = 8 * o % eb;
+      w.k_at[o] = block + row * (D / 2) + part;
+      w.k_scale[o] = block + eb * D + (row + r) * (D / 16) + (D / 64) * c;
     }
-    w.k_at = D == 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 32 + (((c >> 1) ^ ((r >> 2) & 1)) << 4) + (c & 1) * 8;
-    w.v_at = i * (D / 2);
+    w.v_scale = eb * (D / 16) + (2 * c - r) * (D / 16) - (D / 64) * c;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int key = 16 * p + 8 * (q & 1) + i;
+      w.v_at[p] = key / eb * bb + (eb + key % eb) * (D / 2);
+    }
     w.v_turn = ((q >> 1) ^ (D == 128 ? ((i >> 1) & 3) : ((i >> 2) & 1))) << 4;
     w.pick[0] = kv4_pick(r >> 2, r >> 2);
     w.pick[1] = kv4_pick(2 + (r >> 2), 2 + (r >> 2));
+    // Worked out once: without this the compiler does it again for every tile.
+    win_keep(w.q_at);
+    win_keep(w.v_scale);
+    win_keep(w.v_turn);
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+      win_keep(w.k_at[o]);
+      win_keep(w.k_scale[o]);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      win_keep(w.v_at[p]);
+      win_keep(w.pick[p]);
+    }
   } else {
-    w.k_at = (8 * (q & 1) + i) * (2 * D);
+    w.k_at[0] = (8 * (q & 1) + i) * (2 * D);
     w.k_turn = ((q >> 1) ^ i) << 4;
-    w.v_at = kKv8Keys * 2 * D + (8 * (q >> 1) + i) * (2 * D);
+    w.v_at[0] = win_keys<KV4, NT> * 2 * D + (8 * (q >> 1) + i) * (2 * D);
     w.v_turn = ((q & 1) ^ i) << 4;
   }
 }
@@ -376,10 +450,10 @@ __device__ __forceinline__ void win_begin(WinWarp<D, NT, RG, KV4>& w, uint2 (&ra
     if constexpr (W::Q_SMEM) {
 #pragma unroll
       for (int j = 0; j < KD; ++j)
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(w.q_at + ((j * NT + nt) * 32 + lane) * 8), "r"(raw[nt][j].x),
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(w.q_at + (j * NT + nt) * 256), "r"(raw[nt][j].x),
                      "r"(raw[nt][j].y)
                      : "memory");
-      if (c == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.q_at + KD * NT * 256 + (nt * 8 + r) * 4), "f"(qs) : "memory");
+      if (c == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(w.q_at - lane * 8 + KD * NT * 256 + (nt * 8 + r) * 4), "f"(qs) : "memory");
     } else {
 #pragma unroll
       for (int j = 0; j < KD; ++j) {
@@ -438,13 +512,6 @@ __device__ __forceinline__ WinMask win_mask(const WinParams& a, int len, int key
   return k;
 }
 
-// Whether some token does not see some key of the tile.
-__device__ __forceinline__ bool win_masked(const WinParams& a, int len, int key0) {
-  const int sees = a.causal ? len - a.T_q : len - 1;       // the oldest token's place
-  if (kKv8Keys - 1 > sees - key0) return true;
-  return a.window > 0 && max(key0, a.sinks) <= min(key0 + kKv8Keys - 1, len - 1 - a.window);
-}
-
 // byte offsets in a tile of the V scales of a key (kv4)
 template <int D>
 __device__ __forceinline__ uint32_t win_v_scales(int key, int eb) {
@@ -452,22 +519,33 @@ __device__ __forceinline__ uint32_t win_v_scales(int key, int eb) {
 }
 
 // Values of keys that no token sees: zeros, so that a weight of 0 meets no NaN (kv4: their scales).
-template <int D, bool KV4>
+template <int D, bool KV4, int K>
 __device__ __forceinline__ void win_clear(const WinMask& k, uint32_t st, int eb, int lane, const Win& ring) {
   if constexpr (KV4) {
-    const uint32_t to = st + win_v_scales<D>(lane, eb);
-    if (!k.any(lane) && smem_ok(to, D / 16, ring.lo, ring.hi, ring.status)) {
-      if constexpr (D == 128) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
-      else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
+#pragma unroll
+    for (int key = lane; key < K; key += 32) {
+      const uint32_t to = st + win_v_scales<D>(key, eb);
+      if (!k.any(key) && smem_ok(to, D / 16, ring.lo, ring.hi, ring.status)) {
+        if constexpr (D == 128) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
+        else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
+      }
     }
-    ptx::fence_proxy_async_smem();     // before the next bulk copy into this place
   } else {
-    for (int i = lane; i < kKv8Keys * (D / 8); i += 32) {
-      const uint32_t to = st + kKv8Keys * 2 * D + i * 16;
-      if (!k.any(i / (D / 8)) && smem_ok(to, 16, ring.lo, ring.hi, ring.status))
+    constexpr int CH = D / 8;
+    for (int base = 0; base < K; base += 32)
+    for (uint32_t hidden = __ballot_sync(0xffffffffu, !k.any(base + lane)); hidden != 0;) {      // 32 / CH keys at once
+      int key = -1;
+#pragma unroll
+      for (int i = 0; i < 32 / CH; ++i) {
+        if (i == lane / CH && hidden != 0) key = base + __ffs(hidden) - 1;
+        hidden &= hidden - 1;
+      }
+      const uint32_t to = st + (K + key) * (2 * D) + lane % CH * 16;
+      if (key >= 0 && smem_ok(to, 16, ring.lo, ring.hi, ring.status))
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
     }
   }
+  ptx::fence_proxy_async_smem();     // before the next bulk copy into this place
   __syncwarp();
 }
 
@@ -478,13 +556,14 @@ __device__ __forceinline__ bool win_infinite(uint32_t x) {     // one of two 16-
 }
 
 // Whether a value of a key that some token sees and another does not is not finite: then a weight of 0 is not enough.
-template <int D, bool KV4, bool BF16>
+template <int D, bool KV4, bool BF16, int K>
 __device__ __noinline__ bool win_hidden_infinite(WinMask k, uint32_t st, int eb, Win ring) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   if constexpr (KV4) {
-    if (k.any(lane) && !k.all(lane)) {
-      const uint32_t at = smem_clamp(st + win_v_scales<D>(lane, eb), D / 16, ring.lo, ring.hi, ring.status);
+    for (int key = lane; key < K; key += 32) {
+      if (!k.any(key) || k.all(key)) continue;
+      const uint32_t at = smem_clamp(st + win_v_scales<D>(key, eb), D / 16, ring.lo, ring.hi, ring.status);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t s;
@@ -493,26 +572,27 @@ __device__ __noinline__ bool win_hidden_infinite(WinMask k, uint32_t st, int eb,
       }
     }
   } else {
-    for (int i = lane; i < kKv8Keys * (D / 8); i += 32) {
-      const int key = i / (D / 8);
-      if (!k.any(key) || k.all(key)) continue;
-      uint32_t v[4];
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                   : "r"(smem_clamp(st + kKv8Keys * 2 * D + i * 16, 16, ring.lo, ring.hi, ring.status)));
+    for (int base = 0; base < K; base += 32)
+    for (uint32_t some = __ballot_sync(0xffffffffu, k.any(base + lane) && !k.all(base + lane)); some != 0; some &= some - 1) {
+      uint32_t v[D / 64];
+      const uint32_t at = smem_clamp(st + (K + base + __ffs(some) - 1) * (2 * D) + lane * (D / 16), D / 16, ring.lo,
+                                     ring.hi, ring.status);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= win_infinite<BF16>(v[j]);
+      for (int j = 0; j < D / 64; ++j) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[j]) : "r"(at + 4 * j));
+        bad |= win_infinite<BF16>(v[j]);
+      }
     }
   }
   return __any_sync(0xffffffffu, bad);
 }
 
-// O += the values of such a tile that are not finite, each by the rows that see its key (the MMAs take zeros for them).
-// Rare: a call with its arrays in local memory, so that the common form keeps its registers.
-template <int D, int NT>
-struct WinInfinite {
+// O += the values of such a tile, each by the rows that see its key.  Rare: one key and column after the other, and a call
+// with its arrays in local memory, so that the common form keeps its registers.
+template <int D, int NT, int K>
+struct WinSlow {
   float acc[D / 16][NT][4];
-  float2 p[4][NT];          // weights of keys 8o + lane / 4
+  float2 p[K / 8][NT];      // weights of keys 8o + lane / 4
   int behind[NT][2];        // this lane's rows: distance of their token from the newest one
   WinMask mask;
   uint32_t st;
@@ -520,51 +600,44 @@ struct WinInfinite {
   Win ring;
 };
 
-template <int D, int NT, bool KV4, bool BF16>
-__device__ __noinline__ void win_infinite_values(WinInfinite<D, NT>& w) {
+template <int D, int NT, bool KV4, bool BF16, int K>
+__device__ __noinline__ void win_slow_values(WinSlow<D, NT, K>& w) {
   constexpr int KD = D / 16;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll 1
-  for (int o = 0; o < 4; ++o)
+  for (int key = 0; key < K; ++key) {
+    if (!w.mask.any(key)) continue;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const int key = 8 * o + i;
-      if (!w.mask.any(key)) continue;
+    for (int j = 0; j < KD; ++j)
 #pragma unroll 1
-      for (int j = 0; j < KD; ++j)
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const int d = win_column<KV4>(j, half, r);
-          float v = 0.f;
-          if constexpr (KV4) {
-            uint32_t s;
-            asm volatile("ld.shared.u8 %0, [%1];"
-                         : "=r"(s)
-                         : "r"(smem_clamp(w.st + win_v_scales<D>(key, w.eb) + d / 16, 1, w.ring.lo, w.ring.hi, w.ring.status)));
-            if (s >= kKv4Infinite) v = CUDART_NAN_F;
-          } else {
-            uint16_t x;
-            const uint32_t at = w.st + kKv8Keys * 2 * D + key * (2 * D) + (((d >> 3) ^ (key & 7)) << 4) + (d & 7) * 2;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(smem_clamp(at, 2, w.ring.lo, w.ring.hi, w.ring.status)));
-            if (win_infinite<BF16>(x))
-              v = BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(*reinterpret_cast<const __half*>(&x));
-          }
-#pragma unroll 1
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 p = make_float2(__shfl_sync(0xffffffffu, w.p[o][nt].x, i * 4 + c),
-                                         __shfl_sync(0xffffffffu, w.p[o][nt].y, i * 4 + c));
-            if (v != 0.f && w.mask.sees(key, w.behind[nt][0])) w.acc[j][nt][2 * half] += fmaxf(p.x, 1e-30f) * v;
-            if (v != 0.f && w.mask.sees(key, w.behind[nt][1])) w.acc[j][nt][2 * half + 1] += fmaxf(p.y, 1e-30f) * v;
-          }
+      for (int half = 0; half < 2; ++half) {
+        const int d = win_column<KV4>(j, half, r);
+        float v;
+        if constexpr (KV4) {
+          const int row = key % w.eb;
+          const uint32_t at = w.st + key / w.eb * kv4_block_bytes(w.eb, D) + w.eb * (D / 2) + kv4_chunk<D>(row, d / 32) + d % 32 / 2;
+          const uint32_t sat = w.st + win_v_scales<D>(key, w.eb) + d / 16;
+          uint32_t x, s, h[4];
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(smem_clamp(at, 1, w.ring.lo, w.ring.hi, w.ring.status)));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s) : "r"(smem_clamp(sat, 1, w.ring.lo, w.ring.hi, w.ring.status)));
+          kv4_unpack(x >> (d % 2 * 4), h);
+          v = s >= kKv4Infinite ? CUDART_NAN_F : half2_floats(h[0]).x * kv4_scale(s);
+        } else {
+          uint16_t x;
+          const uint32_t at = w.st + (K + key) * (2 * D) + (((d >> 3) ^ (key & 7)) << 4) + (d & 7) * 2;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(smem_clamp(at, 2, w.ring.lo, w.ring.hi, w.ring.status)));
+          v = BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(*reinterpret_cast<const __half*>(&x));
         }
-    }
-}
-
-// 16-bit values of a register that are not finite become zeros
-template <bool BF16>
-__device__ __forceinline__ uint32_t win_finite(uint32_t x) {
-  constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
-  return ((x & E) == E ? 0u : x & 0xffffu) | ((x >> 16 & E) == E ? 0u : x & 0xffff0000u);
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 mine = w.p[key >> 3][nt];
+          const float2 p = make_float2(__shfl_sync(0xffffffffu, mine.x, (key & 7) * 4 + c),
+                                       __shfl_sync(0xffffffffu, mine.y, (key & 7) * 4 + c));
+          if (w.mask.sees(key, w.behind[nt][0])) w.acc[j][nt][2 * half] += p.x * v;
+          if (w.mask.sees(key, w.behind[nt][1])) w.acc[j][nt][2 * half + 1] += p.y * v;
+        }
+      }
+  }
 }
 
 // the shared-memory reads of a tile, free to be scheduled among the products
@@ -579,26 +652,32 @@ __device__ __forceinline__ uint2 win_lds2(uint32_t at) {
   return v;
 }
 
-// One tile.  FINE: the weights as two 16-bit numbers, the rounded one and what was lost.
+// the low four bits of a's bytes, the high ones of b's
+__device__ __forceinline__ uint32_t win_low_nibbles(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
+// One tile of keys key0 ..; masked: some token may not see some key of it.  FINE: the weights as two 16-bit numbers, the rounded one and what was lost.
 template <int D, int NT, int RG, bool KV4, bool BF16, bool FINE>
 __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinParams& a, uint32_t st, int eb, int len, int key0,
-                                         int rg, int lane, const Win& ring) {
+                                         bool masked, int rg, int lane, const Win& ring) {
   using W = WinWarp<D, NT, RG, KV4>;
-  constexpr int KD = W::KD;
+  constexpr int KD = W::KD, K = win_keys<KV4, NT>, OCTETS = K / 8, SUB = 32 * (D + D / 8);   // SUB: bytes of 32 keys (kv4)
   constexpr bool B = !KV4 && BF16;      // bf16 products
   const int r = lane >> 2, c = lane & 3;
-  const bool masked = win_masked(a, len, key0);
   const bool apart = masked && a.causal && a.T_q > 1;     // tokens see different keys
   bool infinite = false;
   if (masked) {
     const WinMask mask = win_mask(a, len, key0);
-    if (apart) infinite = win_hidden_infinite<D, KV4, BF16>(mask, st, eb, ring);
-    win_clear<D, KV4>(mask, st, eb, lane, ring);
+    if (apart) infinite = win_hidden_infinite<D, KV4, BF16, K>(mask, st, eb, ring);
+    win_clear<D, KV4, K>(mask, st, eb, lane, ring);
   }
   // ---- S^T = K Q^T
-  float s[2][NT][4];
+  float s[K / 16][NT][4];
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+  for (int p = 0; p < K / 16; ++p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[p][nt][0] = s[p][nt][1] = s[p][nt][2] = s[p][nt][3] = 0.f;
   auto query = [&](uint32_t (&q)[NT][2], int j) {
@@ -607,7 +686,7 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
       if constexpr (W::Q_SMEM) {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                      : "=r"(q[nt][0]), "=r"(q[nt][1])
-                     : "r"(w.q_at + ((j * NT + nt) * 32 + lane) * 8));
+                     : "r"(w.q_at + (j * NT + nt) * 256));
       } else {
         q[nt][0] = w.qf[nt][j][0];
         q[nt][1] = w.qf[nt][j][1];
@@ -616,43 +695,45 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
   };
   if constexpr (KV4) {
     constexpr int WORDS = D / 32;
-    uint32_t x[4][WORDS], sc[4][WORDS / 2];
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      const uint32_t at = smem_clamp(st + w.octet[o] + w.row[o] * (D / 2) + w.k_at, D / 8, ring.lo, ring.hi, ring.status);
-      const uint32_t sat = smem_clamp(st + w.octet[o] + eb * D + (w.row[o] + r) * (D / 16) + (D / 64) * c, D / 64, ring.lo,
-                                      ring.hi, ring.status);
-      if constexpr (D == 128) {
-        const uint4 v = win_lds4(at);
-        x[o][0] = v.x; x[o][1] = v.y; x[o][2] = v.z; x[o][3] = v.w;
-        uint16_t two;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(two) : "r"(sat));
-        sc[o][0] = kv4_scales(two, two, kv4_pick(0, 0));
-        sc[o][1] = kv4_scales(two, two, kv4_pick(1, 1));
-      } else {
-        const uint2 v = win_lds2(at);
-        x[o][0] = v.x; x[o][1] = v.y;
-        uint32_t one;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(one) : "r"(sat));
-        sc[o][0] = kv4_scales(one, one, kv4_pick(0, 0));
+    for (int h = 0; h < K / 32; ++h) {
+      uint32_t x[4][WORDS], sc[4][WORDS / 2];
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const uint32_t at = smem_clamp(st + w.k_at[o] + h * SUB, D / 8, ring.lo, ring.hi, ring.status);
+        const uint32_t sat = smem_clamp(st + w.k_scale[o] + h * SUB, D / 64, ring.lo, ring.hi, ring.status);
+        if constexpr (D == 128) {
+          const uint4 v = win_lds4(at);
+          x[o][0] = v.x; x[o][1] = v.y; x[o][2] = v.z; x[o][3] = v.w;
+          uint16_t two;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(two) : "r"(sat));
+          sc[o][0] = kv4_scales(two, two, kv4_pick(0, 0));
+          sc[o][1] = kv4_scales(two, two, kv4_pick(1, 1));
+        } else {
+          const uint2 v = win_lds2(at);
+          x[o][0] = v.x; x[o][1] = v.y;
+          uint32_t one;
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(one) : "r"(sat));
+          sc[o][0] = kv4_scales(one, one, kv4_pick(0, 0));
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      uint32_t q[2][NT][2];
-      query(q[0], 2 * i);
-      query(q[1], 2 * i + 1);
+      for (int i = 0; i < WORDS; ++i) {
+        uint32_t q[2][NT][2];
+        query(q[0], 2 * i);
+        query(q[1], 2 * i + 1);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint32_t lo[4], hi[4];
-        kv4_unpack(x[2 * p][i], lo);
-        kv4_unpack(x[2 * p + 1][i], hi);
+        for (int p = 0; p < 2; ++p) {
+          uint32_t lo[4], hi[4];
+          kv4_unpack(x[2 * p][i], lo);
+          kv4_unpack(x[2 * p + 1][i], hi);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t f[4] = {kv4_mul(lo[2 * k], sc[2 * p][i / 2]), kv4_mul(hi[2 * k], sc[2 * p + 1][i / 2]),
-                                 kv4_mul(lo[2 * k + 1], sc[2 * p][i / 2]), kv4_mul(hi[2 * k + 1], sc[2 * p + 1][i / 2])};
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t f[4] = {kv4_mul(lo[2 * k], sc[2 * p][i / 2]), kv4_mul(hi[2 * k], sc[2 * p + 1][i / 2]),
+                                   kv4_mul(lo[2 * k + 1], sc[2 * p][i / 2]), kv4_mul(hi[2 * k + 1], sc[2 * p + 1][i / 2])};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) kv8_mma(s[p][nt], f, q[k][nt]);
+            for (int nt = 0; nt < NT; ++nt) kv8_mma(s[2 * h + p][nt], f, q[k][nt]);
+          }
         }
       }
     }
@@ -662,9 +743,9 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
       uint32_t q[NT][2];
       query(q, j);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int p = 0; p < K / 16; ++p) {
         uint32_t f[4];
-        ptx::ldmatrix_x4(f, smem_clamp(st + p * 16 * (2 * D) + w.k_at + ((uint32_t)(j << 5) ^ w.k_turn), 16, ring.lo, ring.hi,
+        ptx::ldmatrix_x4(f, smem_clamp(st + p * 16 * (2 * D) + w.k_at[0] + ((uint32_t)(j << 5) ^ w.k_turn), 16, ring.lo, ring.hi,
                                        ring.status));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) win_mma<B>(s[p][nt], f, q[nt]);
@@ -675,18 +756,18 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
   // s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
   bool over = false;     // a score far above the running maximum
   float mx[NT][2];
-  Two y[4][NT], qs[NT];
+  Two y[OCTETS][NT], qs[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if constexpr (W::Q_SMEM) {
       float2 f;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(w.q_at + KD * NT * 256 + (nt * 8 + 2 * c) * 4));
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(w.q_at - lane * 8 + KD * NT * 256 + (nt * 8 + 2 * c) * 4));
       qs[nt] = two(f.x, f.y);
     } else {
       qs[nt] = two(w.qs[nt][0], w.qs[nt][1]);
     }
 #pragma unroll
-    for (int o = 0; o < 4; ++o) y[o][nt] = two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]);
+    for (int o = 0; o < OCTETS; ++o) y[o][nt] = two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]);
   }
   // rows beyond the last (padding of the n-tile) are taken for the newest token's
   auto behind = [&](int nt, int i) {
@@ -699,7 +780,7 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
     for (int nt = 0; nt < NT; ++nt) {
       const int b0 = behind(nt, 0), b1 = behind(nt, 1);
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
+      for (int o = 0; o < OCTETS; ++o) {
         const float2 f = split(y[o][nt]);
         y[o][nt] = two(mask.sees(8 * o + r, b0) ? f.x : -CUDART_INF_F, mask.sees(8 * o + r, b1) ? f.y : -CUDART_INF_F);
       }
@@ -707,9 +788,13 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float2 f0 = split(y[0][nt]), f1 = split(y[1][nt]), f2 = split(y[2][nt]), f3 = split(y[3][nt]);
-    const float2 t = split(mul2(two(fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x)), fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y))),
-                                qs[nt]));
+    float2 top = split(y[0][nt]);
+#pragma unroll
+    for (int o = 1; o < OCTETS; ++o) {
+      const float2 f = split(y[o][nt]);
+      top = make_float2(fmaxf(top.x, f.x), fmaxf(top.y, f.y));
+    }
+    const float2 t = split(mul2(two(top.x, top.y), qs[nt]));
     mx[nt][0] = t.x;
     mx[nt][1] = t.y;
     over |= t.x > w.m[nt][0] + kKv8Slack || t.y > w.m[nt][1] + kKv8Slack;
@@ -737,14 +822,14 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
         for (int i = 0; i < 4; ++i) w.acc[j][nt][i] *= f[nt][i & 1];
   }
   // ---- weights, and P as the B operand
-  uint32_t pf[2][NT][2], pl[2][NT][2];
+  uint32_t pf[K / 16][NT][2], pl[K / 16][NT][2];
   constexpr float kUp = (float)(1 << kWinLift<KV4, BF16>);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const Two off = two(w.m[nt][0] == -CUDART_INF_F ? 0.f : -w.m[nt][0], w.m[nt][1] == -CUDART_INF_F ? 0.f : -w.m[nt][1]);
     Two sum = two(w.l[nt][0], w.l[nt][1]);
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
+    for (int o = 0; o < OCTETS; ++o) {
       const float2 x = split(fma2(y[o][nt], qs[nt], off));
       const Two p = two(ptx::ex2(x.x), ptx::ex2(x.y));
       sum = add2(sum, p);
@@ -763,11 +848,11 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
     w.l[nt][1] = f.y;
   }
   if (infinite) {
-    WinInfinite<D, NT> t;
+    WinSlow<D, NT, K> t;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int o = 0; o < 4; ++o) t.p[o][nt] = split(y[o][nt]);
+      for (int o = 0; o < OCTETS; ++o) t.p[o][nt] = split(y[o][nt]);
       t.behind[nt][0] = behind(nt, 0);
       t.behind[nt][1] = behind(nt, 1);
 #pragma unroll
@@ -779,13 +864,14 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
     t.st = st;
     t.eb = eb;
     t.ring = ring;
-    win_infinite_values<D, NT, KV4, BF16>(t);
+    win_slow_values<D, NT, KV4, BF16, K>(t);
 #pragma unroll
     for (int j = 0; j < KD; ++j)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) w.acc[j][nt][i] = t.acc[j][nt][i];
+    return;
   }
   // ---- O^T += V^T P^T
   auto product = [&](int j, int p, const uint32_t (&f)[4]) {
@@ -798,13 +884,12 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
   if constexpr (KV4) {
     constexpr int CHUNKS = D / 32;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < K / 16; ++p) {
       uint32_t sc[2][CHUNKS];       // scales of keys 16p + 8h + 2c, + 1 for this lane's columns of chunk mt
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int o = 2 * p + h;
-        const uint32_t at = smem_clamp(st + w.octet[o] + eb * (D + D / 16) + (w.row[o] + 2 * c) * (D / 16), D / 8, ring.lo,
-                                       ring.hi, ring.status);
+        const int o = 2 * (p & 1) + h;
+        const uint32_t at = smem_clamp(st + w.k_scale[o] + w.v_scale + p / 2 * SUB, D / 8, ring.lo, ring.hi, ring.status);
         if constexpr (D == 128) {
           const uint4 v = win_lds4(at);
           sc[h][0] = kv4_scales(v.x, v.z, w.pick[0]);
@@ -816,24 +901,18 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
           sc[h][0] = kv4_scales(v.x, v.y, w.pick[0]);
           sc[h][1] = kv4_scales(v.x, v.y, w.pick[1]);
         }
-        if (infinite) {
-#pragma unroll
-          for (int k = 0; k < CHUNKS; ++k) sc[h][k] = win_finite<false>(sc[h][k]);
-        }
       }
-      const uint32_t row = st + (lane & 8 ? w.octet[2 * p + 1] + w.row[2 * p + 1] * (D / 2)
-                                          : w.octet[2 * p] + w.row[2 * p] * (D / 2)) + eb * (D / 2) + w.v_at;
 #pragma unroll
       for (int mt = 0; mt < CHUNKS; mt += 2) {
         uint32_t x[4];     // chunk mt of the first and second eight keys, chunk mt + 1
-        ptx::ldmatrix_x4_trans(x, smem_clamp(row + ((uint32_t)(mt << 4) ^ w.v_turn), 16, ring.lo, ring.hi, ring.status));
+        ptx::ldmatrix_x4_trans(x, smem_clamp(st + w.v_at[p & 1] + ((uint32_t)(mt << 4) ^ w.v_turn) + p / 2 * SUB, 16, ring.lo, ring.hi, ring.status));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // a word: columns 4r .. 4r + 3 of key 2c in the lower half, of key 2c + 1 in the upper one
           const uint32_t k0 = __byte_perm(x[2 * h], x[2 * h + 1], 0x5410), k1 = __byte_perm(x[2 * h], x[2 * h + 1], 0x7632);
           uint32_t even[4], odd[4];    // columns 0 and 2 of the first eight keys, of the second; 1 and 3
-          kv4_unpack((k0 & 0x0f0f0f0fu) | ((k1 << 4) & 0xf0f0f0f0u), even);
-          kv4_unpack(((k0 >> 4) & 0x0f0f0f0fu) | (k1 & 0xf0f0f0f0u), odd);
+          kv4_unpack(win_low_nibbles(k0, k1 << 4), even);
+          kv4_unpack(win_low_nibbles(k0 >> 4, k1), odd);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t f[4] = {kv4_mul(even[k], sc[0][mt + h]), kv4_mul(odd[k], sc[0][mt + h]),
@@ -845,16 +924,12 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
     }
   } else {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < K / 16; ++p)
 #pragma unroll
       for (int j = 0; j < KD; ++j) {
         uint32_t f[4];
-        ptx::ldmatrix_x4_trans(f, smem_clamp(st + p * 16 * (2 * D) + w.v_at + ((uint32_t)(j << 5) ^ w.v_turn), 16, ring.lo,
+        ptx::ldmatrix_x4_trans(f, smem_clamp(st + p * 16 * (2 * D) + w.v_at[0] + ((uint32_t)(j << 5) ^ w.v_turn), 16, ring.lo,
                                              ring.hi, ring.status));
-        if (infinite) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = win_finite<BF16>(f[i]);
-        }
         product(j, p, f);
       }
   }
@@ -936,6 +1011,28 @@ __device__ __forceinline__ void win_leave(WinWarp<D, NT, RG, KV4>& w, float2* ml
     }
 }
 
+// One row's four columns of n <= MOST states, folded in the order of the keys: state i has its m and l at ml(i), its O at o(i).
+template <int MOST, typename ML, typename O>
+__device__ __forceinline__ void win_fold(int n, ML ml, O o, float& m, float& l, float4& acc) {
+  if constexpr (MOST <= 8) {
+    kv8_fold(n, ml, o, m, l, acc);
+  } else {
+    m = -CUDART_INF_F;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; i += 8) {
+      float mi, li;
+      float4 v;
+      kv8_fold(n - i, [&](int k) { return ml(i + k); }, [&](int k) { return o(i + k); }, mi, li, v);
+      const float top = fmaxf(m, mi), base = top == -CUDART_INF_F ? 0.f : top;
+      const float f = ptx::ex2(m - base), g = ptx::ex2(mi - base);
+      m = top;
+      l = l * f + li * g;
+      acc = make_float4(acc.x * f + v.x * g, acc.y * f + v.y * g, acc.z * f + v.z * g, acc.w * f + v.w * g);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- kernels
 template <int D, int NT, int RG, bool KV4, bool BF16>
 __global__ void __launch_bounds__(WinCfg<D, NT, RG, KV4>::THREADS, 1)
@@ -958,7 +1055,7 @@ gqa_win_kernel(const WinParams a) {
   if (threadIdx.x == 0) *abort = 0;
   ptx::fence_mbar_init();
   ptx::grid_dependency_wait();
-  win_prefix<C::THREADS>(a, prefix, lens, reinterpret_cast<int64_t*>(smem + C::SUMS_OFF));
+  win_prefix<C::KEYS, C::THREADS>(a, prefix, lens, reinterpret_cast<int64_t*>(smem + C::SUMS_OFF));
   if (threadIdx.x == 0) ptx::grid_launch_dependents();
   win_empty_rows<D, C::THREADS>(a, lens);
 
@@ -983,31 +1080,32 @@ gqa_win_kernel(const WinParams a) {
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
   const uint64_t policy = ptx::policy_evict_first();
-  const int eb = min(a.block_size, kKv8Keys);
+  const int eb = min(a.block_size, 32);
   uint2 raw[NT][D / 16];
   win_load_q<D, NT, RG, KV4>(raw, a, at.b, at.g, rg, lane);
   WinStream str;
   int issued = 0;
   if (rg == 0) {
     str.at = at;
-    win_stream_setup<D, KV4>(str, a, lane);
-    str.id = win_ids(a, at, lens[at.b], str.want, lane);
-    win_enter<D>(str, a, prefix, lens, lane);
+    win_stream_setup<D, KV4, C::KEYS>(str, a, lane);
+    str.id = win_ids<C::KEYS>(a, at, lens[at.b], str.want, lane);
+    win_enter<D, C::KEYS>(str, a, prefix, lens, lane);
     for (; issued < n && issued < STAGES; ++issued)
       if (!(issued == 1 && wk == a.stall))
-        win_copy<D, KV4>(str, a, prefix, lens, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
+        win_copy<D, KV4, C::KEYS>(str, a, prefix, lens, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
   }
   WinWarp<D, NT, RG, KV4> w;
   win_setup(w, a, ptx::smem_u32(smem + C::Q_OFF) + warp * C::QUERIES, lane);
-  int len = lens[at.b], skip = win_span(a, len).skip;
+  int len = lens[at.b], skip = win_span<C::KEYS>(a, len).skip;
+  WinClear clear = win_clear_tiles<C::KEYS>(a, len, skip);
   win_begin<D, NT, RG, KV4, BF16>(w, raw, a, lane);
   bool fresh = at.t == 0;        // this piece begins with its unit
   int64_t slot = 2 * wk;         // where it goes when it is not the whole unit
   int i = 0, stage = 0, phase = 0;
   for (; i < n; ++i) {
     if (!ptx::mbar_wait_bounded(full + stage * 8, phase, a.timeout_ns, abort)) break;
-    win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, skip, at.t) * kKv8Keys, rg, lane,
-                                         ring);
+    win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, skip, at.t) * C::KEYS,
+                                         !clear.has(at.t), rg, lane, ring);
     __syncwarp();
     if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
     if (rg == 0 && i + STAGES < n) {
@@ -1015,7 +1113,8 @@ gqa_win_kernel(const WinParams a) {
         ++i;
         break;
       }
-      win_copy<D, KV4>(str, a, prefix, lens, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
+      if (!(STAGES == 1 && i == 0 && wk == a.stall))
+        win_copy<D, KV4, C::KEYS>(str, a, prefix, lens, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
       ++issued;
     }
     if (++stage == STAGES) {
@@ -1029,7 +1128,8 @@ gqa_win_kernel(const WinParams a) {
       if (i + 1 < n) {
         kv8_next_unit(at, prefix, a.N, a.h_kv);
         len = lens[at.b];
-        skip = win_span(a, len).skip;
+        skip = win_span<C::KEYS>(a, len).skip;
+        clear = win_clear_tiles<C::KEYS>(a, len, skip);
         win_load_q<D, NT, RG, KV4>(raw, a, at.b, at.g, rg, lane);
         win_begin<D, NT, RG, KV4, BF16>(w, raw, a, lane);
         fresh = true;
@@ -1080,7 +1180,7 @@ gqa_win_short_kernel(const WinParams a) {
     if (threadIdx.x == 0) atomicOr(a.status, kDevBadInput);
     len = len < 0 ? 0 : (int)cap;
   }
-  const WinSpan span = win_span(a, len);
+  const WinSpan span = win_span<C::KEYS>(a, len);
   const int tiles = span.tiles;
   const int per = max((tiles + a.ctas * C::GROUPS - 1) / (a.ctas * C::GROUPS), 1);
   const int busy_ctas = (tiles + per * C::GROUPS - 1) / (per * C::GROUPS);
@@ -1090,7 +1190,7 @@ gqa_win_short_kernel(const WinParams a) {
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
   const uint64_t policy = ptx::policy_evict_first();
-  const int eb = min(a.block_size, kKv8Keys);
+  const int eb = min(a.block_size, 32);
   const bool stalled = a.stall >= 0 && a.stall == (int)blockIdx.x * C::GROUPS + grp;
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
   bool good = true;
@@ -1101,27 +1201,29 @@ gqa_win_short_kernel(const WinParams a) {
       str.at = {b, g, t0, tiles};
       str.len = len;
       str.skip = span.skip;
-      win_stream_setup<D, KV4>(str, a, lane);
-      str.id = win_ids(a, str.at, len, str.want, lane);
+      str.first = span.first;
+      win_stream_setup<D, KV4, C::KEYS>(str, a, lane);
+      str.id = win_ids<C::KEYS>(a, str.at, len, str.want, lane);
     }
     uint2 raw[NT][D / 16];
     win_load_q<D, NT, RG, KV4>(raw, a, b, g, rg, lane);
     if (rg == 0) {
-      win_ids_check(str, a);
+      win_ids_check<D>(str, a);
       str.t_end = t0 + n;
       for (; issued < n && issued < STAGES; ++issued)
         if (!(stalled && issued == 1))
-          win_issue<D, KV4>(str, a, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
+          win_issue<D, KV4, C::KEYS>(str, a, ring0 + issued * C::TILE, full + issued * 8, policy, lane, ring);
     }
     WinWarp<D, NT, RG, KV4> w;
     win_setup(w, a, ptx::smem_u32(smem + C::Q_OFF) + warp * C::QUERIES, lane);
     win_begin<D, NT, RG, KV4, BF16>(w, raw, a, lane);
+    const WinClear clear = win_clear_tiles<C::KEYS>(a, len, span.skip);
     int i = 0, stage = 0, phase = 0;
     for (; i < n; ++i) {
       good = ptx::mbar_wait_bounded(full + stage * 8, phase, a.timeout_ns, flags);
       if (!good) break;
-      win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, span.skip, t0 + i) * kKv8Keys,
-                                           rg, lane, ring);
+      win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, span.skip, t0 + i) * C::KEYS,
+                                           !clear.has(t0 + i), rg, lane, ring);
       __syncwarp();
       if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
       if (rg == 0 && i + STAGES < n) {
@@ -1129,7 +1231,8 @@ gqa_win_short_kernel(const WinParams a) {
           good = ptx::mbar_wait_bounded(empty + stage * 8, phase, a.timeout_ns, flags);
           if (!good) break;
         }
-        win_issue<D, KV4>(str, a, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
+        if (!(STAGES == 1 && i == 0 && stalled))
+          win_issue<D, KV4, C::KEYS>(str, a, ring0 + stage * C::TILE, full + stage * 8, policy, lane, ring);
         ++issued;
       }
       if (++stage == STAGES) {
@@ -1163,7 +1266,7 @@ gqa_win_short_kernel(const WinParams a) {
       const int row = i / (D / 4), d = i % (D / 4) * 4, part = row / (8 * NT), wrow = row % (8 * NT);
       float m, l;
       float4 v;
-      kv8_fold(busy, [&](int k) { return ml[(k * RG + part) * 8 * NT + wrow]; },
+      win_fold<C::FOLD>(busy, [&](int k) { return ml[(k * RG + part) * 8 * NT + wrow]; },
                [&](int k) {
                  return *reinterpret_cast<const float4*>(areas + (k * RG + part) * C::AREA + (wrow * D + d) * 4);
                }, m, l, v);
@@ -1183,7 +1286,7 @@ gqa_win_short_kernel(const WinParams a) {
       const int row = i / (D / 4), d = i % (D / 4) * 4, part = row / (8 * NT), wrow = row % (8 * NT);
       float m, l;
       float4 v;
-      kv8_fold(busy_ctas, [&](int k) { return ld_cluster_v2(ptx::mapa(ml_at + row * 8, k)); },
+      win_fold<8>(busy_ctas, [&](int k) { return ld_cluster_v2(ptx::mapa(ml_at + row * 8, k)); },
                [&](int k) { return ld_cluster_v4(ptx::mapa(o_at + part * C::AREA + (wrow * D + d) * 4, k)); }, m, l, v);
       kv8_store4<BF16>(a, b, g, row, d, D, l, v);
     }
@@ -1198,7 +1301,24 @@ cudaError_t win_prepare(int cls);
 template <int D, bool KV4, bool BF16>
 cudaError_t win_launch(const WinParams& p, int cls, unsigned grid, cudaStream_t st);
 
+// The n-tiles of a warp and the warps of a ring for a class of query rows (8, 16, 24, 32, 48, 64).  32 rows over the 4-bit
+// cache: two warps of 16 rows and tiles of 64 keys (131071 keys 88 us instead of 95; four such warps for 64 rows 227 us instead
+// of 221).
 template <bool KV4>
-constexpr int win_warps() { return WinCfg<64, 1, 1, KV4>::WARPS; }
+constexpr int win_rows_nt(int cls) {
+  return cls < 2 ? cls + 1 : (cls == 2 || cls == 4 ? 3 : (KV4 && cls == 3 ? 2 : 4));
+}
+template <bool KV4>
+constexpr int win_rows_rg(int cls) {
+  return cls < 3 ? 1 : (cls == 3 ? (KV4 ? 2 : 1) : (cls == 4 ? 2 : 2));
+}
+
+// keys of a tile and workers of a CTA for a class of query rows
+template <bool KV4>
+constexpr int win_tile_keys(int cls) { return win_rows_nt<KV4>(cls) <= 2 ? win_keys<KV4, 2> : win_keys<KV4, 3>; }
+template <bool KV4>
+constexpr int win_workers(int cls) {
+  return (win_rows_nt<KV4>(cls) == 1 ? WinCfg<128, 1, 1, KV4>::WARPS : WinCfg<128, 2, 1, KV4>::WARPS) / win_rows_rg<KV4>(cls);
+}
 
 }  // namespace gqa

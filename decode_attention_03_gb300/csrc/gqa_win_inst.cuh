@@ -24,24 +24,24 @@ cudaError_t win_launch_one(const WinParams& p, unsigned grid, cudaStream_t st) {
 template <int D, bool KV4, bool BF16>
 cudaError_t win_prepare_class(int cls) {
   switch (cls) {
-    case 0: return win_prepare_one<D, 1, 1, KV4, BF16>();
-    case 1: return win_prepare_one<D, 2, 1, KV4, BF16>();
-    case 2: return win_prepare_one<D, 3, 1, KV4, BF16>();
-    case 3: return win_prepare_one<D, 4, 1, KV4, BF16>();
-    case 4: return win_prepare_one<D, 3, 2, KV4, BF16>();
-    default: return win_prepare_one<D, 4, 2, KV4, BF16>();
+    case 0: return win_prepare_one<D, win_rows_nt<KV4>(0), win_rows_rg<KV4>(0), KV4, BF16>();
+    case 1: return win_prepare_one<D, win_rows_nt<KV4>(1), win_rows_rg<KV4>(1), KV4, BF16>();
+    case 2: return win_prepare_one<D, win_rows_nt<KV4>(2), win_rows_rg<KV4>(2), KV4, BF16>();
+    case 3: return win_prepare_one<D, win_rows_nt<KV4>(3), win_rows_rg<KV4>(3), KV4, BF16>();
+    case 4: return win_prepare_one<D, win_rows_nt<KV4>(4), win_rows_rg<KV4>(4), KV4, BF16>();
+    default: return win_prepare_one<D, win_rows_nt<KV4>(5), win_rows_rg<KV4>(5), KV4, BF16>();
   }
 }
 
 template <int D, bool KV4, bool BF16>
 cudaError_t win_launch_class(const WinParams& p, int cls, unsigned grid, cudaStream_t st) {
   switch (cls) {
-    case 0: return win_launch_one<D, 1, 1, KV4, BF16>(p, grid, st);
-    case 1: return win_launch_one<D, 2, 1, KV4, BF16>(p, grid, st);
-    case 2: return win_launch_one<D, 3, 1, KV4, BF16>(p, grid, st);
-    case 3: return win_launch_one<D, 4, 1, KV4, BF16>(p, grid, st);
-    case 4: return win_launch_one<D, 3, 2, KV4, BF16>(p, grid, st);
-    default: return win_launch_one<D, 4, 2, KV4, BF16>(p, grid, st);
+    case 0: return win_launch_one<D, win_rows_nt<KV4>(0), win_rows_rg<KV4>(0), KV4, BF16>(p, grid, st);
+    case 1: return win_launch_one<D, win_rows_nt<KV4>(1), win_rows_rg<KV4>(1), KV4, BF16>(p, grid, st);
+    case 2: return win_launch_one<D, win_rows_nt<KV4>(2), win_rows_rg<KV4>(2), KV4, BF16>(p, grid, st);
+    case 3: return win_launch_one<D, win_rows_nt<KV4>(3), win_rows_rg<KV4>(3), KV4, BF16>(p, grid, st);
+    case 4: return win_launch_one<D, win_rows_nt<KV4>(4), win_rows_rg<KV4>(4), KV4, BF16>(p, grid, st);
+    default: return win_launch_one<D, win_rows_nt<KV4>(5), win_rows_rg<KV4>(5), KV4, BF16>(p, grid, st);
   }
 }
 
