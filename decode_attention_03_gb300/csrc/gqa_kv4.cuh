@@ -30,10 +30,18 @@ __host__ __device__ constexpr int kv4_chunk(int r, int c) {
   return r * (D / 2) + ((c ^ (D == 128 ? ((r >> 1) & 3) : ((r >> 2) & 1))) << 4);
 }
 
+// x / s in fp32, rounded to nearest, where inv is the fp32 number nearest to 1 / s and nothing overflows: a product and one
+// correction by its exact remainder (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  A value on the border of two codes must come out there: x * inv alone misses it for s = 1.75 * 2^k.
+__device__ __forceinline__ float kv4_quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+
 // scale byte of 16 elements whose largest magnitude has the bits `top`: m / 6 rounded to nearest even
 __device__ __forceinline__ uint32_t kv4_scale_byte(uint32_t top) {
   if (top >= 0x7f800000u) return kKv4NanScale;
-  const float s = fminf(__fdiv_rn(__uint_as_float(top), 6.f), kKv4MaxScale);
+  const float s = fminf(kv4_quotient(__uint_as_float(top), 6.f, 1.f / 6.f), kKv4MaxScale);
   uint16_t two;
   asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(s));
   return two & 0xffu;
@@ -45,12 +53,19 @@ __device__ __forceinline__ float kv4_scale(uint32_t byte) {
   return f;
 }
 
-// codes of x[0..3] / s in the low 16 bits, nearest even, beyond 6 saturated; signed zeros where the scale is 0 or not finite
-__device__ __forceinline__ uint32_t kv4_codes(const float* x, float s) {
+// the fp32 number nearest to 1 / s of a scale s > 0: one of four significands
+__device__ __forceinline__ float kv4_inverse(float s) {
+  const uint32_t b = __float_as_uint(s);
+  const float f = b & 0x400000u ? (b & 0x200000u ? 4.f / 7.f : 2.f / 3.f) : (b & 0x200000u ? 0.8f : 1.f);
+  return __uint_as_float(__float_as_uint(f) + 0x3f800000u - (b & 0x7f800000u));
+}
+
+// codes of x[0..3] / s in the low 16 bits, nearest even, beyond 6 saturated; inv: kv4_inverse(s).  (Codes below a scale that
+// is not finite are no values.)
+__device__ __forceinline__ uint32_t kv4_codes(const float* x, float s, float inv) {
   float z[4];
-  const bool flat = !(s > 0.f && s < CUDART_INF_F);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = flat ? copysignf(0.f, x[i]) : __fdiv_rn(x[i], s);
+  for (int i = 0; i < 4; ++i) z[i] = kv4_quotient(x[i], s, inv);
   uint32_t r;
   asm("{\n\t.reg .b8 a, b;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "mov.b32 %0, {a, b, a, b};\n\t}"

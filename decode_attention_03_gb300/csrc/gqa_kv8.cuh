@@ -281,9 +281,11 @@ __device__ __forceinline__ int append_holder(int e, int rot) {
 // the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
 // 16384 tokens of 64 + 8 + 8 heads of 128 take 105.3 us (6.45 TB/s, 0.95 of a copy's rate); 110.5 with one token a warp,
 // 117.9 with five CTAs an SM (48 registers) instead of four (64).
-// AXES: pairs turned by positions of several axes, a.pair_axes.
+// AXES: pairs turned by positions of several axes, a.pair_axes: 16384 tokens of text and pictures 103.3 us.
+// Into the 4-bit cache (LAYOUT 4) a lane's chunks find the other elements of their sixteen by shuffles; three CTAs an SM, as
+// four have too few registers for it (8192 tokens of 32 + 8 + 8 heads, with a read-back: 59.3 us instead of 61.3).
 template <int D, bool BF16, int CW, bool PAIRS, int LAYOUT, bool AXES>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
+__global__ void __launch_bounds__(kAppendThreads, LAYOUT == 4 ? 3 : kAppendCtas)
 gqa_append_kernel(const AppendParams a) {
   constexpr int LPH = D / (2 * CW), HPW = 32 / LPH, WARPS = kAppendThreads / 32;
   __shared__ __align__(16) Chunk<CW> stage[kAppendIters][2][kAppendThreads];   // a thread's own places
@@ -502,12 +504,13 @@ gqa_append_kernel(const AppendParams a) {
           if (sub == 0) base[2 * a.block_size * D + (kind - 1) * a.block_size + row] = (uint8_t)e;
         }
       } else if constexpr (LAYOUT == 4) {
-        uint32_t own[2] = {0u, 0u}, top[2];     // largest magnitudes, as bits: a NaN is the largest of all
+        uint32_t own[2], top[2];     // largest magnitudes, as bits: a NaN is the largest of all
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          float m = fabsf(x[j][0]);
 #pragma unroll
-          for (int i = 0; i < CW; ++i) own[j] = max(own[j], __float_as_uint(x[j][i]) & 0x7fffffffu);
-          top[j] = own[j];
+          for (int i = 1; i < CW; ++i) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(x[j][i])));
+          top[j] = own[j] = __float_as_uint(m);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -526,10 +529,10 @@ gqa_append_kernel(const AppendParams a) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t byte = kv4_scale_byte(top[j]);
-            const float s = kv4_scale(byte);
+            const float s = byte == 0 ? 1.f : kv4_scale(byte), inv = kv4_inverse(s);   // (0: elements far below a half)
             uint8_t* to = codes + kv4_chunk<D>(row, off[j] >> 5) + ((off[j] & 31) >> 1);
-            if constexpr (CW == 8) *reinterpret_cast<uint32_t*>(to) = kv4_codes(x[j], s) | (kv4_codes(x[j] + 4, s) << 16);
-            else *reinterpret_cast<uint16_t*>(to) = (uint16_t)kv4_codes(x[j], s);
+            if constexpr (CW == 8) *reinterpret_cast<uint32_t*>(to) = kv4_codes(x[j], s, inv) | (kv4_codes(x[j] + 4, s, inv) << 16);
+            else *reinterpret_cast<uint16_t*>(to) = (uint16_t)kv4_codes(x[j], s, inv);
             if (off[j] % 16 == 0) scales[off[j] / 16] = (uint8_t)byte;
           }
         }
