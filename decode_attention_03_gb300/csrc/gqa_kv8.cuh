@@ -206,6 +206,14 @@ __device__ __forceinline__ void append_vllm_values(const AppendParams& a, int se
   constexpr int WARPS = kAppendThreads / 32, PARTS = D / 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h0 = set * (a.iters * HPW), heads = min(a.iters * HPW, a.h_kv - h0);
+  if (a.cos_sin != nullptr && a.pair_axes != nullptr) {      // a pair on an axis that is none: no token is taken
+    bool bad = false;
+    for (int i = lane; i < a.rot_dim / 2; i += 32) bad |= a.pair_axes[i] >= (uint32_t)a.num_axes;
+    if (__any_sync(0xffffffffu, bad)) {
+      if (threadIdx.x == 0) atomicOr(a.status, kDevBadInput);
+      return;
+    }
+  }
   const int64_t first = (int64_t)blockIdx.x * (8 * a.run);
   const int64_t end = min(first + 8 * a.run, (int64_t)a.num_tokens);       // the CTA's tokens
   int shift = 0;

@@ -491,7 +491,7 @@ __device__ __forceinline__ void win_mma(float (&d)[4], const uint32_t (&a)[4], c
 
 // Which keys of a tile a query token sees; places are counted from the tile's first key.
 struct WinMask {
-  int64_t last, lo;    // the newest token's place, and the oldest key in its window
+  int last, lo;        // the newest token's place, and the oldest key in its window (or one far before the tile)
   int sinks;           // keys below stay visible
   int back;            // the oldest token's distance from the newest
   // seen by the token `back` places before the newest
@@ -505,8 +505,8 @@ struct WinMask {
 
 __device__ __forceinline__ WinMask win_mask(const WinParams& a, int len, int key0) {
   WinMask k;
-  k.last = (int64_t)len - 1 - key0;
-  k.lo = a.window > 0 ? k.last - a.window + 1 : INT64_MIN / 2;
+  k.last = len - 1 - key0;
+  k.lo = a.window > 0 ? max(k.last - (a.window - 1), -(1 << 20)) : -(1 << 20);
   k.sinks = a.sinks - key0;
   k.back = a.causal ? a.T_q - 1 : 0;
   return k;
@@ -532,12 +532,13 @@ __device__ __forceinline__ void win_clear(const WinMask& k, uint32_t st, int eb,
     }
   } else {
     constexpr int CH = D / 8;
-    for (int base = 0; base < K; base += 32)
-    for (uint32_t hidden = __ballot_sync(0xffffffffu, !k.any(base + lane)); hidden != 0;) {      // 32 / CH keys at once
+    static_assert(K == 32, "a key a lane");
+    uint32_t hidden = __ballot_sync(0xffffffffu, !k.any(lane));
+    while (hidden != 0) {      // 32 / CH keys at once
       int key = -1;
 #pragma unroll
       for (int i = 0; i < 32 / CH; ++i) {
-        if (i == lane / CH && hidden != 0) key = base + __ffs(hidden) - 1;
+        if (i == lane / CH && hidden != 0) key = __ffs(hidden) - 1;
         hidden &= hidden - 1;
       }
       const uint32_t to = st + (K + key) * (2 * D) + lane % CH * 16;
@@ -572,10 +573,9 @@ __device__ __noinline__ bool win_hidden_infinite(WinMask k, uint32_t st, int eb,
       }
     }
   } else {
-    for (int base = 0; base < K; base += 32)
-    for (uint32_t some = __ballot_sync(0xffffffffu, k.any(base + lane) && !k.all(base + lane)); some != 0; some &= some - 1) {
+    for (uint32_t some = __ballot_sync(0xffffffffu, k.any(lane) && !k.all(lane)); some != 0; some &= some - 1) {
       uint32_t v[D / 64];
-      const uint32_t at = smem_clamp(st + (K + base + __ffs(some) - 1) * (2 * D) + lane * (D / 16), D / 16, ring.lo,
+      const uint32_t at = smem_clamp(st + (K + __ffs(some) - 1) * (2 * D) + lane * (D / 16), D / 16, ring.lo,
                                      ring.hi, ring.status);
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {

@@ -303,6 +303,26 @@ def test_append_reports(gqa):
     assert gqa.gqa_workspace_check(ws) == gqa.GQA_ERR_INVALID_ARG and written(cache) == [] and (q == 3.0).all()
 
 
+@pytest.mark.parametrize("layout", ["rows", "vllm", "kv8", "kv4"])
+@pytest.mark.parametrize("T", [5, 40])
+def test_a_pair_on_an_axis_that_is_none(gqa, layout, T):
+    """No query, key or value is written, into any cache, and the call reports."""
+    D, hk, bs, nb = 64, 2, 8, 8
+    c = case("f16", D, 4, hk, T, 12, axes=2)
+    c["axes"][7] = 2
+    if layout in ("kv8", "kv4"):
+        caches = [torch.full((nb, hk, bs * (2 * D + 2 if layout == "kv8" else D + D // 8)), 9, dtype=torch.uint8, device="cuda")]
+    elif layout == "rows":
+        caches = [torch.full((nb, bs, hk * D), 3.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    else:
+        caches = [torch.full(s, 3.0, dtype=torch.float16, device="cuda") for s in ((nb, hk, D // 8, bs, 8), (nb, hk, D, bs))]
+    before, q = [x.clone() for x in caches], torch.full((T, 4 * D), 3.0, dtype=torch.float16, device="cuda")
+    assert gqa.gqa_status_check() == gqa.GQA_OK
+    run(gqa, c, torch.arange(T), *caches, q_out=q)
+    assert gqa.gqa_status_check() == gqa.GQA_ERR_INVALID_ARG
+    assert (q == 3.0).all() and all(torch.equal(a, b) for a, b in zip(caches, before))
+
+
 def test_append_in_place_and_no_tokens(gqa):
     c = case("f16", 128, 8, 2, 19, 5, axes=3)
     cache, again = gqa.gqa_kv4_cache(4, 16, 2, 128), gqa.gqa_kv4_cache(4, 16, 2, 128)
