@@ -620,3 +620,78 @@ def test_bounds_checked_build(gqa):
     q2 = gqa.gqa_append(qkv[:, :hq * D], qkv[:, hq * D:(hq + hk) * D], qkv[:, (hq + hk) * D:], hq, hk, slots, again, positions=pos,
                         cos_sin=cs, pair_axes=axes, q_weight=w, k_weight=w)
     assert torch.equal(again, cache) and torch.equal(q2, q_out)
+
+
+def test_the_first_call_of_a_process_is_captured(gqa):
+    """Nothing of the library was called before on the device: the capture makes everything that it needs."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, decode_attention_03_gb300 as gqa
+dev = "cuda"
+cache = gqa.gqa_kv4_cache(4, 16, 2, 128)
+pools = [torch.zeros(4, 16, 256, dtype=torch.float16, device=dev) for _ in range(2)]
+x, q = torch.randn(3, 512, device=dev).half(), torch.randn(1, 1024, device=dev).half()
+slots, tab = torch.arange(3, device=dev), torch.arange(4, dtype=torch.int32, device=dev)[None]
+ln = torch.tensor([3], dtype=torch.int32, device=dev)
+cs = torch.rand(9, 128, device=dev)
+kw = dict(positions=torch.randint(0, 9, (3, 3), device=dev).int(), cos_sin=cs, pair_axes=gqa.gqa_pair_axes([16, 24, 24]))
+back = [torch.zeros(1, 8, 256, dtype=torch.float16, device=dev) for _ in range(2)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gqa.gqa_append(None, x[:, :256], x[:, 256:], 2, 2, slots, cache, **kw)
+    gqa.gqa_append(None, x[:, :256], x[:, 256:], 2, 2, slots, *pools, **kw)
+    a = gqa.gqa_decode_kv4(q, cache, tab, ln, 8, 2, window=2, sinks=1)
+    b = gqa.gqa_decode_window(q, *pools, tab, ln, 8, 2, window=2, sinks=1)
+    gqa.gqa_kv4_read(cache, tab, ln, 128, k_out=back[0], v_out=back[1])
+g.replay()
+assert gqa.gqa_status_check() == gqa.GQA_OK
+assert torch.equal(a, gqa.gqa_decode_kv4(q, cache, tab, ln, 8, 2, window=2, sinks=1))
+assert torch.equal(b, gqa.gqa_decode_window(q, *pools, tab, ln, 8, 2, window=2, sinks=1))
+k, v = gqa.gqa_kv4_read(cache, tab, ln, 128, 8)
+assert torch.equal(k, back[0]) and torch.equal(v, back[1]) and bool((k != 0).any())
+tab[0, 0] = 4
+g.replay()
+assert gqa.gqa_status_check() == gqa.GQA_ERR_INVALID_ARG and gqa.gqa_status_check() == gqa.GQA_OK
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_no_sequences_and_no_keys(gqa, kind):
+    c = Case(kind, "bf16", [0, 0, 0], 128, 2, 16, 119)
+    q = queries("bf16", 3, 2, 8 * 128, 50)
+    for window in (0, 5):
+        for causal in (False, True):
+            out = torch.full_like(q, 7.0).cuda()
+            assert (c.run(gqa, q, 8, causal=causal, window=window, sinks=1, out=out) == 0).all()
+    wide = np.full((3, 4000), -1, np.int32)                  # the general form
+    assert (c.run(gqa, q, 8, tab=wide, window=0) == 0).all()
+    none = c.run(gqa, q[:0], 8, tab=np.zeros((0, 4), np.int32), lens=[])
+    assert none.shape == (0, 2, 8 * 128) and gqa.gqa_status_check() == gqa.GQA_OK
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_configurations(gqa, seed):
+    import random
+    r = random.Random(1000 + seed)
+    kind, elem, D, bs = r.choice(KINDS), r.choice(["f16", "bf16"]), r.choice([64, 128]), r.choice([8, 16, 32, 64])
+    hk = r.choice([1, 2, 3, 5, 8])
+    G = r.choice([1, 2, 3, 4, 5, 7, 8, 16])
+    T = r.randint(1, max(1, min(9, 64 // G)))
+    N = r.choice([1, 2, 5, 17, 60])
+    top = r.choice([40, 300, 2500]) if N < 60 else 300
+    lens = [r.randint(0, top) for _ in range(N)]
+    c = Case(kind, elem, lens, D, hk, bs, 2000 + seed)
+    q = queries(elem, N, T, G * hk * D, 3000 + seed)
+    some = r.sample(range(N), min(N, 6))
+    for _ in range(3):
+        window, sinks, causal = r.choice([0, 1, r.randint(1, 60), r.randint(1, top)]), r.choice([0, 1, 4, r.randint(0, top)]), r.random() < 0.6
+        ws = c.workspace(gqa, N, T, G * hk)
+        o = c.run(gqa, q, G * hk, causal=causal, window=window, sinks=sinks, workspace_tensor=ws)
+        assert gqa.gqa_workspace_check(ws) == gqa.GQA_OK
+        c.check(o, q, G * hk, f"window {window}, sinks {sinks}, causal {causal}", some=some, causal=causal, window=window, sinks=sinks)
