@@ -48,7 +48,10 @@ gqa_status win_device(bool kv4, int D, int cls, bool bf16, int* sms) {
 }
 
 // ---------------------------------------------------------------- decode
-int win_groups(bool kv4, int cls) { return kv4 ? win_workers<true>(cls) : win_workers<false>(cls); }
+int win_groups(bool kv4, int D, int cls) {
+  if (D == 64) return kv4 ? win_workers<true, 64>(cls) : win_workers<false, 64>(cls);
+  return kv4 ? win_workers<true, 128>(cls) : win_workers<false, 128>(cls);
+}
 
 template <int D, bool KV4, bool BF16>
 cudaError_t win_decode(const WinParams& p, int cls, unsigned grid, bool cut, bool many_pieces, cudaStream_t st) {
@@ -114,7 +117,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
       !aligned_to(c.lens, 4) || (kv4 ? !aligned16(c.cache) : !aligned16(c.k_pool) || !aligned16(c.v_pool)))
     return GQA_ERR_INVALID_ARG;
   if (c.ws_bytes < kHeaderBytes) return GQA_ERR_WORKSPACE;
-  const int rows = c.h_q / c.h_kv * c.T_q, cls = kv8_class(rows), groups = win_groups(kv4, cls);
+  const int rows = c.h_q / c.h_kv * c.T_q, cls = kv8_class(rows), groups = win_groups(kv4, c.D, cls);
   const int tile = kv4 ? win_tile_keys<true>(cls) : win_tile_keys<false>(cls);
   int sms = 0;
   if ((s = win_device(kv4, c.D, cls, bf16, &sms)) != GQA_OK) return s;
@@ -313,7 +316,7 @@ size_t gqa_decode_window_workspace_size(int num_seqs, int T_q, int h_q, int h_kv
     const int rows = h_q / h_kv * T_q, cls = kv8_class(rows);
     int sms = 0;
     if (win_device(kv4, d_head, cls, false, &sms) != GQA_OK) return 0;
-    return kv8_layout(sms * win_groups(kv4, cls), rows, d_head).total;
+    return kv8_layout(sms * win_groups(kv4, d_head, cls), rows, d_head).total;
   } catch (...) {
     return 0;
   }

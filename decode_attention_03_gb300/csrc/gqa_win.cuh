@@ -43,7 +43,9 @@ constexpr int win_keys = KV4 && NT <= 2 ? 64 : 32;
 
 template <int D, int NT, int RG, bool KV4>
 struct WinCfg {
-  static constexpr int WARPS = NT == 1 ? 12 : 8;
+  // 16 rows of 64 elements leave the registers for twelve warps too (64 sequences of 1K-16K keys 104 us instead of 115); of
+  // 128 they do not (spills: 194 us instead of 164)
+  static constexpr int WARPS = NT == 1 || (KV4 && NT == 2 && D == 64) ? 12 : 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int GROUPS = WARPS / RG;
   static constexpr int KEYS = win_keys<KV4, NT>;                   // of a tile: one or two of 32, laid out one after the other
@@ -58,7 +60,7 @@ struct WinCfg {
   // Tiles of a warp in the ring.  The 4-bit cache takes two (NT > 2: four, of 32 keys).  16 bits: one, and the other warps
   // compute while it comes (12 warps with one tile of 32 keys 165 us instead of 206 with 4 warps and three, 64 sequences
   // under a window of 4096).
-  static constexpr int DEPTH = KV4 ? (NT > 2 ? 4 : 2) * 128 / D : 128 / D;
+  static constexpr int DEPTH = KV4 ? (NT > 2 ? 4 : 2) * (NT == 2 ? 1 : 128 / D) : 128 / D;
   static constexpr int STAGES = DEPTH * RG;
   static constexpr int Q_OFF = (BAR_OFF + GROUPS * STAGES * 16 + 127) & ~127;
   static constexpr int ML_OFF = Q_OFF + WARPS * QUERIES;
@@ -1316,9 +1318,11 @@ constexpr int win_rows_rg(int cls) {
 // keys of a tile and workers of a CTA for a class of query rows
 template <bool KV4>
 constexpr int win_tile_keys(int cls) { return win_rows_nt<KV4>(cls) <= 2 ? win_keys<KV4, 2> : win_keys<KV4, 3>; }
-template <bool KV4>
+template <bool KV4, int D>
 constexpr int win_workers(int cls) {
-  return (win_rows_nt<KV4>(cls) == 1 ? WinCfg<128, 1, 1, KV4>::WARPS : WinCfg<128, 2, 1, KV4>::WARPS) / win_rows_rg<KV4>(cls);
+  const int nt = win_rows_nt<KV4>(cls);
+  return (nt == 1 ? WinCfg<D, 1, 1, KV4>::WARPS : (nt == 2 ? WinCfg<D, 2, 1, KV4>::WARPS : WinCfg<D, 3, 1, KV4>::WARPS)) /
+         win_rows_rg<KV4>(cls);
 }
 
 }  // namespace gqa
