@@ -58,7 +58,7 @@ struct WinCfg {
   static constexpr int FLAG_OFF = SUMS_OFF + WARPS * 8;
   static constexpr int BAR_OFF = FLAG_OFF + 16;
   // Tiles of a warp in the ring.  The 4-bit cache takes two (NT > 2: four, of 32 keys).  16 bits: one, and the other warps
-  // compute while it comes (12 warps with one tile of 32 keys 165 us instead of 206 with 4 warps and three, 64 sequences
+  // compute while it comes (12 warps with one tile of 32 keys 160 us instead of 206 with 4 warps and three, 64 sequences
   // under a window of 4096).
   static constexpr int DEPTH = KV4 ? (NT > 2 ? 4 : 2) * (NT == 2 ? 1 : 128 / D) : 128 / D;
   static constexpr int STAGES = DEPTH * RG;
@@ -255,6 +255,9 @@ __device__ __forceinline__ void win_enter(WinStream& s, const WinParams& a, cons
   s.id_next = s.ahead.b < a.N ? win_ids<K>(a, s.ahead, lens[s.ahead.b], s.want_next, lane) : -1;
 }
 
+// bits 0 .. n - 1
+__device__ __forceinline__ uint32_t win_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
+
 // Copies the stream's next tile to `dst`; on to the next tile of the window (true: the window ends).  Every lane of the
 // warp calls this.
 template <int D, bool KV4, int K>
@@ -278,27 +281,28 @@ __device__ __forceinline__ bool win_issue(WinStream& s, const WinParams& a, uint
         bulk_load(dst + s.to, src, s.size, bar, policy);
     }
   } else {
+    // Every lane copies as often as every other: rows that no token sees, or of a block with a bad id, are zeros, so that a
+    // weight of 0 meets no NaN there.  No branch, and no cache hint, which would take two more instructions a copy.
+    static_assert(K == 32, "a key for each bit of a register");
     constexpr int CH = D / 8, KEYS = 32 / CH;     // chunks of a row; keys that the lanes copy at once
     const int key0 = tile * K, first = a.block_size > K ? (tile & 1) * K : 0, c = lane % CH;
-    const int valid = s.len - key0, sinks = a.sinks - key0, old = s.first - key0;
-    const bool whole = valid >= K && (old <= 0 || sinks >= K);
+    const uint32_t seen = (win_below(s.len - key0) & (~win_below(s.first - key0) | win_below(a.sinks - key0))) >> (lane / CH);
     const int64_t row = (int64_t)a.h_kv * D, apart = a.v_pool - a.k_pool;
+    const uint32_t to = dst + lane / CH * (2 * D);
 #pragma unroll
     for (int o = 0; o < K / 8; ++o) {       // eight keys lie in one block
       const int id = __shfl_sync(0xffffffffu, s.id, ((s.k << a.ids_log) + (8 * o >> a.bs_log)) & 31);
       const int r = lane / CH + ((first + 8 * o) & (a.block_size - 1));
-      const uint16_t* from = a.k_pool + ((int64_t)id * a.block_size + r) * row + s.at.g * D + 8 * c;
+      const uint16_t* from = a.k_pool + ((int64_t)max(id, 0) * a.block_size + r) * row + s.at.g * D + 8 * c;
+      const uint32_t some = id < 0 ? 0u : seen >> (8 * o);
 #pragma unroll
       for (int i = 0; i < 8 / KEYS; ++i, from += KEYS * row) {
-        const int key = 8 * o + i * KEYS + lane / CH;
-        const uint32_t to = dst + key * (2 * D) + ((c ^ (key & 7)) << 4);
-        if (id >= 0 && (whole || (key < valid && (key >= old || key < sinks))) &&
-            idx_ok(from + 7 - a.k_pool, (int64_t)a.num_blocks * a.block_size * row, a.status) &&
-            smem_ok(to, K * 2 * D + 16, ring.lo, ring.hi, ring.status)) {
-          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
-          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to + K * 2 * D),
-                       "l"(from + apart), "l"(policy)
-                       : "memory");
+        const uint32_t at = to + (8 * o + i * KEYS) * (2 * D) + ((c ^ ((i * KEYS + lane / CH) & 7)) << 4);
+        uint32_t bytes = (some >> (i * KEYS) & 1) << 4;
+        if (!idx_ok(from + 7 - a.k_pool, (int64_t)a.num_blocks * a.block_size * row, a.status)) bytes = 0;
+        if (smem_ok(at, K * 2 * D + 16, ring.lo, ring.hi, ring.status)) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + K * 2 * D), "l"(from + apart), "r"(bytes) : "memory");
         }
       }
     }
@@ -520,32 +524,16 @@ __device__ __forceinline__ uint32_t win_v_scales(int key, int eb) {
   return key / eb * kv4_block_bytes(eb, D) + eb * (D + D / 16) + key % eb * (D / 16);
 }
 
-// Values of keys that no token sees: zeros, so that a weight of 0 meets no NaN (kv4: their scales).
-template <int D, bool KV4, int K>
+// Values of keys that no token sees: zeros, by their scales, so that a weight of 0 meets no NaN.  (Rows of 16 bits come as
+// zeros.)
+template <int D, int K>
 __device__ __forceinline__ void win_clear(const WinMask& k, uint32_t st, int eb, int lane, const Win& ring) {
-  if constexpr (KV4) {
 #pragma unroll
-    for (int key = lane; key < K; key += 32) {
-      const uint32_t to = st + win_v_scales<D>(key, eb);
-      if (!k.any(key) && smem_ok(to, D / 16, ring.lo, ring.hi, ring.status)) {
-        if constexpr (D == 128) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
-        else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
-      }
-    }
-  } else {
-    constexpr int CH = D / 8;
-    static_assert(K == 32, "a key a lane");
-    uint32_t hidden = __ballot_sync(0xffffffffu, !k.any(lane));
-    while (hidden != 0) {      // 32 / CH keys at once
-      int key = -1;
-#pragma unroll
-      for (int i = 0; i < 32 / CH; ++i) {
-        if (i == lane / CH && hidden != 0) key = __ffs(hidden) - 1;
-        hidden &= hidden - 1;
-      }
-      const uint32_t to = st + (K + key) * (2 * D) + lane % CH * 16;
-      if (key >= 0 && smem_ok(to, 16, ring.lo, ring.hi, ring.status))
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+  for (int key = lane; key < K; key += 32) {
+    const uint32_t to = st + win_v_scales<D>(key, eb);
+    if (!k.any(key) && smem_ok(to, D / 16, ring.lo, ring.hi, ring.status)) {
+      if constexpr (D == 128) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
+      else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
     }
   }
   ptx::fence_proxy_async_smem();     // before the next bulk copy into this place
@@ -674,7 +662,7 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
   if (masked) {
     const WinMask mask = win_mask(a, len, key0);
     if (apart) infinite = win_hidden_infinite<D, KV4, BF16, K>(mask, st, eb, ring);
-    win_clear<D, KV4, K>(mask, st, eb, lane, ring);
+    if constexpr (KV4) win_clear<D, K>(mask, st, eb, lane, ring);
   }
   // ---- S^T = K Q^T
   float s[K / 16][NT][4];
