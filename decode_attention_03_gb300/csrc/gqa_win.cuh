@@ -2,18 +2,20 @@
 // 16-bit pools (num_blocks, block_size, h_kv * D).
 //
 // Query token t of T_q newest has the place p = len - T_q + t (causal; else len - 1) and sees key j <= p if j > p - window or
-// j < sinks.  A row of keys with a window is a short row: the 32-key tiles that no token of it sees are left out, and what
-// remains, the sinks' tiles and those from the oldest visible key on, is numbered through; blocks that no token sees are
+// j < sinks.  A row of keys with a window is a short row: the tiles that no token of it sees are left out, and what remains, the sinks' tiles and those from the oldest visible key on, is numbered through; blocks that no token sees are
 // neither copied nor looked up, so that their pages may be gone.  All tiles of a launch then lie on one axis that is cut
 // into equal shares, one for each worker, as in the kernels of the 8-bit cache, whose plan, partials and merge these
 // kernels share: the cut looks at no sequence, and the same call gives the same bits.
 //
-// A worker is one warp (two that share a ring for more than 32 query rows) with a ring of its own in shared memory, filled
+// A worker is one warp (two that share a ring for 32 query rows over the 4-bit cache, and for more) with a ring of its own in shared memory, filled
 // by one bulk copy for each block of the 4-bit cache, and by 16-byte asynchronous copies from the 16-bit pools, whose rows of a
-// head lie apart: a bulk copy for each row costs its lane's turn in a loop over the lanes (64 keys' rows, four warps on an SM:
-// 322 us instead of 206 for 64 sequences under a window of 4096).
+// head lie apart: a bulk copy for each row costs its lane's turn in a loop over the lanes (four warps on an SM: 322 us
+// instead of 206 for 64 sequences under a window of 4096).
 //
-// Arithmetic of a warp, for its 8 NT query rows and the 32 keys of a tile: S^T = K Q^T and O^T += V^T P^T by mma.sync, keys
+// Measured: 64 sequences of 1K-16K keys, 32 + 8 heads of 128, over the 4-bit cache 102 us (5.5 TB/s, 0.82 of a copy's rate; bound
+// by issue slots and the ALU's conversions); 64 of 1K-32K over 16 bits under a window of 4096 160 us (6.4 TB/s, 0.95; DRAM).
+//
+// Arithmetic of a warp, for its 8 NT query rows and the keys of a tile: S^T = K Q^T and O^T += V^T P^T by mma.sync, keys
 // and columns on the M side, query rows on the N side.  kv4: a code becomes f16 by one conversion for two of them, and is
 // multiplied by its scale there, exactly; with K, lane c of a row's four holds the elements 32c .. 32c + 31 (D = 128), two
 // whole groups, and since the order of the summed index is free, Q is laid out to match; with V, a transposing ldmatrix
@@ -325,7 +327,7 @@ __device__ __forceinline__ void win_copy(WinStream& s, const WinParams& a, const
 }
 
 // ---------------------------------------------------------------- the computing side
-// RG warps share a ring (RG = 2: more than 32 rows), each with NT n-tiles of 8 query rows.
+// RG warps share a ring, each with NT n-tiles of 8 query rows.
 template <int D, int NT, int RG, bool KV4>
 struct WinWarp {
   static constexpr int KD = D / 16;
