@@ -79,11 +79,14 @@ int64_t most_tiles(int64_t keys, int tile, int window, int sink_tiles, int new_t
   return some < all ? some : all;
 }
 
-// CTAs of a unit in the short kernel, as kv8_short_ctas: a cluster of 1, 2, 4 or 8, the fewest that give each worker one
-// tile; at most `most` tiles a worker.  0: the general kernel.
+// CTAs of a unit in the short kernel, as kv8_short_ctas: a cluster of 1, 2, 4 or 8, the fewest that give every second worker one
+// tile; at most `most` tiles a worker.  0: the general kernel.  The tiles go evenly to a unit's CTAs (window
+// 1024 + 4, 8 KV heads of 128, f16, a call 6.9 us with the first CTAs full, 6.2 now).  Measured (us of a replayed call, a tile for
+// each worker / every second / third): that one 5.8 / 5.4 / 5.4; window 128 + 4 4.1 / 4.2 / 4.7; 300 keys over the 4-bit cache
+// 5.2 / 5.3 / 5.7.
 int win_short_ctas(int64_t units, int64_t seq_tiles, int sms, int groups, int most) {
   int ctas = 1;
-  while (ctas < 8 && ctas * groups < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;
+  while (ctas < 8 && ctas * (groups / 2) < seq_tiles && units * ctas * 2 <= sms * 3 / 4) ctas *= 2;
   const int64_t here = (seq_tiles + ctas * groups - 1) / (ctas * groups);
   const int64_t there = (units * seq_tiles + sms * groups - 1) / (sms * groups);
   if (units * ctas > sms || here > most || here > there + 2) return 0;

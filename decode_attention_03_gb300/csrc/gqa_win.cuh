@@ -1180,11 +1180,12 @@ gqa_win_short_kernel(const WinParams a) {
   }
   const WinSpan span = win_span<C::KEYS>(a, len);
   const int tiles = span.tiles;
-  const int per = max((tiles + a.ctas * C::GROUPS - 1) / (a.ctas * C::GROUPS), 1);
-  const int busy_ctas = (tiles + per * C::GROUPS - 1) / (per * C::GROUPS);
-  // workers of this CTA that have tiles
-  const int busy = max(min((tiles - c * C::GROUPS * per + per - 1) / per, C::GROUPS), 0);
-  const int wk = c * C::GROUPS + grp, t0 = wk * per, n = grp < busy ? min(per, tiles - t0) : 0;
+  // the tiles go evenly to the CTAs, and a CTA's in runs of `per` to its workers
+  const int share = max((tiles + a.ctas - 1) / a.ctas, 1), per = (share + C::GROUPS - 1) / C::GROUPS;
+  const int busy_ctas = (tiles + share - 1) / share;
+  const int mine = max(min(tiles - c * share, share), 0);
+  const int busy = (mine + per - 1) / per;       // workers of this CTA that have tiles
+  const int t0 = c * share + grp * per, n = grp < busy ? min(per, mine - grp * per) : 0;
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
   const uint64_t policy = ptx::policy_evict_first();
