@@ -454,7 +454,6 @@ __device__ __forceinline__ void win_begin(WinWarp<D, NT, RG, KV4>& w, uint2 (&ra
         raw[nt][j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
       }
     }
-    qs = fmaxf(qs, 1.2e-38f);      // not 0: a hidden key's y is -inf
     if constexpr (W::Q_SMEM) {
 #pragma unroll
       for (int j = 0; j < KD; ++j)
@@ -744,22 +743,25 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
       }
     }
   }
-  // ---- the logit in log2 units is y qs, qs >= 0 of the row.
+  // ---- y: the logits in log2 units, the scores by their row's factor, rounded here once: the weight of a row's largest is
+  // 2^0 to 2^kKv8Slack then, however large the logits are.  (An exponent fma(score, factor, -m) would be what rounding the maximum left: from
+  // 2^27 on more than f16's weights have room for.)
   // s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
   bool over = false;     // a score far above the running maximum
   float mx[NT][2];
-  Two y[OCTETS][NT], qs[NT];
+  Two y[OCTETS][NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    Two qs;
     if constexpr (W::Q_SMEM) {
       float2 f;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(w.q_at - lane * 8 + KD * NT * 256 + (nt * 8 + 2 * c) * 4));
-      qs[nt] = two(f.x, f.y);
+      qs = two(f.x, f.y);
     } else {
-      qs[nt] = two(w.qs[nt][0], w.qs[nt][1]);
+      qs = two(w.qs[nt][0], w.qs[nt][1]);
     }
 #pragma unroll
-    for (int o = 0; o < OCTETS; ++o) y[o][nt] = two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]);
+    for (int o = 0; o < OCTETS; ++o) y[o][nt] = mul2(two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]), qs);
   }
   // rows beyond the last (padding of the n-tile) are taken for the newest token's
   auto behind = [&](int nt, int i) {
@@ -786,10 +788,9 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
       const float2 f = split(y[o][nt]);
       top = make_float2(fmaxf(top.x, f.x), fmaxf(top.y, f.y));
     }
-    const float2 t = split(mul2(two(top.x, top.y), qs[nt]));
-    mx[nt][0] = t.x;
-    mx[nt][1] = t.y;
-    over |= t.x > w.m[nt][0] + kKv8Slack || t.y > w.m[nt][1] + kKv8Slack;
+    mx[nt][0] = top.x;
+    mx[nt][1] = top.y;
+    over |= top.x - w.m[nt][0] > kKv8Slack || top.y - w.m[nt][1] > kKv8Slack;      // (m + slack would be rounded)
   }
   if (__any_sync(0xffffffffu, over)) {
     float f[NT][2];
@@ -822,7 +823,7 @@ __device__ __forceinline__ void win_tile(WinWarp<D, NT, RG, KV4>& w, const WinPa
     Two sum = two(w.l[nt][0], w.l[nt][1]);
 #pragma unroll
     for (int o = 0; o < OCTETS; ++o) {
-      const float2 x = split(fma2(y[o][nt], qs[nt], off));
+      const float2 x = split(add2(y[o][nt], off));
       const Two p = two(ptx::ex2(x.x), ptx::ex2(x.y));
       sum = add2(sum, p);
       const Two up = mul2(p, two(kUp, kUp));
