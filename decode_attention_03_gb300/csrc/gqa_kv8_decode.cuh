@@ -402,7 +402,6 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT
         raw[nt][j] = make_uint2(ptx::pack_half2(x[0] * up, x[1] * up), ptx::pack_half2(x[2] * up, x[3] * up));
       }
     }
-    qs = fmaxf(qs, 1.2e-38f);      // not 0: a hidden key's y is -inf
     if constexpr (W::Q_SMEM) {
 #pragma unroll
       for (int j = 0; j < KD; ++j)
@@ -436,7 +435,7 @@ __device__ __forceinline__ void kv8_begin(Kv8Warp<D, NT, RG>& w, uint2 (&raw)[NT
   if constexpr (W::Q_SMEM) __syncwarp();
 }
 
-// O += the products of a tile whose V exponents, or those before it, lie far apart.  y qs + off: a key's weight in log2
+// O += the products of a tile whose V exponents, or those before it, lie far apart.  y + off: a key's weight in log2
 // units, -inf where it is hidden.  The keys go by ranges of 11 exponents from the largest on, and a row's weights in a
 // range are relative to its largest one there: a product too small for f16 is at most 2^-29 of the largest of its tile,
 // row and range.  The sums of a range start from zero and are added to O in fp32, whose unit is 2^kKv8WideUnit.
@@ -646,7 +645,9 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
       for (int nt = 0; nt < NT; ++nt) kv8_mma(s[p][nt], f[1], q[1][nt]);
     }
   }
-  // ---- y = the scores by the K scales; the logit in log2 units is y qs, qs >= 0 of the row.
+  // ---- y: the logits in log2 units, the scores by the K scales and their row's factor, rounded here once: the weight of a
+  // row's largest is 2^0 to 2^kKv8Slack then, however large the logits are.  (An exponent fma(score, factor, -m) would be what
+  // rounding the maximum left: from 2^27 on more than f16's weights have room for.)
   // s[p][nt][i]: key 16p + 8 (i / 2) + r, row 2c + i % 2 of n-tile nt
   // over: a score far above the running maximum, or a V exponent outside of what has been seen
   bool over = max(max(ev[0], ev[1]), max(ev[2], ev[3])) > w.e || min(min(ev[0], ev[1]), min(ev[2], ev[3])) < w.lo;
@@ -668,7 +669,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
   for (int o = 0; o < 4; ++o) {
     const float k = kv8_scale((uint32_t)ek[o]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) y[o][nt] = mul2(two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]), two(k, k));
+    for (int nt = 0; nt < NT; ++nt) y[o][nt] = mul2(mul2(two(s[o >> 1][nt][(o & 1) * 2], s[o >> 1][nt][(o & 1) * 2 + 1]), two(k, k)), qs[nt]);
   }
   if (masked) {
 #pragma unroll
@@ -690,11 +691,9 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2 f0 = split(y[0][nt]), f1 = split(y[1][nt]), f2 = split(y[2][nt]), f3 = split(y[3][nt]);
-    const float2 t = split(mul2(two(fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x)), fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y))),
-                                qs[nt]));
-    mx[nt][0] = t.x;
-    mx[nt][1] = t.y;
-    over |= t.x > w.m[nt][0] + kKv8Slack || t.y > w.m[nt][1] + kKv8Slack;
+    mx[nt][0] = fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x));
+    mx[nt][1] = fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y));
+    over |= mx[nt][0] - w.m[nt][0] > kKv8Slack || mx[nt][1] - w.m[nt][1] > kKv8Slack;
   }
   bool wide = false;
   if (__any_sync(0xffffffffu, over)) {
@@ -759,7 +758,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-        const float2 x = split(fma2(y[o][nt], qs[nt], off[nt]));
+        const float2 x = split(add2(y[o][nt], off[nt]));
         sum[nt] = add2(sum[nt], two(ptx::ex2(x.x), ptx::ex2(x.y)));
         t.x[o][nt] = x;
       }
@@ -798,7 +797,7 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
     const float v = kv8_ratio(ev[o] - w.e + kKv8Lift);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float2 x = split(fma2(y[o][nt], qs[nt], off[nt]));
+      const float2 x = split(add2(y[o][nt], off[nt]));
       const Two p = two(ptx::ex2(x.x), ptx::ex2(x.y));
       sum[nt] = add2(sum[nt], p);
       const float2 pv = split(mul2(p, two(v, v)));

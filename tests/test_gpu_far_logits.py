@@ -75,14 +75,10 @@ ROWS = [(2, 1), (4, 4), (8, 3), (16, 2), (5, 8), (8, 8)]      # query heads of a
 
 
 @pytest.mark.parametrize("elem", ["f16", "bf16"])
-@pytest.mark.parametrize("op", ["rows", "kv4"])
+@pytest.mark.parametrize("op", ["rows", "kv4", "kv8"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G,T", ROWS)
 def test_paged_calls(gqa, elem, op, D, G, T):
-    paged_calls(gqa, elem, op, D, G, T)
-
-
-def paged_calls(gqa, elem, op, D, G, T):
     hk, bs = 2, 16
     for n, same, sign in ((1000, False, 1), (1000, False, -1), (700, True, 1), (9000, False, 1)):
         q, k, v = case(elem, D, hk, G, T, n, G + T + n, same)
