@@ -838,15 +838,24 @@ __device__ __forceinline__ void kv8_tile(Kv8Warp<D, NT, RG>& w, const Kv8Params&
 }
 
 // A state as it leaves the worker: m + shift, l times `l` = 2^-shift and O times `o` stand for m, l and O.  The shift
-// keeps sums of the largest values, and of the smallest, in float's range.
+// keeps sums of the largest values, and of the smallest, in float's range.  Where it would be lost in m (logits of 2^24 and
+// more) a row leaves without it.
 template <int D, int NT, int RG>
 struct Kv8Units {
-  float shift, l, o;
+  float shift, l, o, far;      // far: what O is multiplied by without the shift
   __device__ __forceinline__ explicit Kv8Units(const Kv8Warp<D, NT, RG>& w) {
     const int s = w.lo >= kKv8Wide || w.e >= 192 ? kKv8WideUnit : (w.e < 64 ? -64 : 0);
     shift = (float)s;
     l = kv8_ratio(-s);
     o = w.lo >= kKv8Wide ? 1.f : kv8_ratio(w.e - 127 - kKv8Lift - s);
+    far = kv8_ratio((w.lo >= kKv8Wide ? 0 : w.e - 127 - kKv8Lift - s) + s);
+  }
+  // a row's m, its l and the factor of its O, as they leave
+  __device__ __forceinline__ void leave(float& m, float& sum, float& unit) const {
+    const bool apart = fabsf(m) >= 16777216.f;
+    m = apart ? m : m + shift;
+    sum = apart ? sum : sum * l;
+    unit = apart ? far : o;
   }
 };
 
@@ -857,7 +866,6 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2, c = lane & 3;
   const Kv8Units<D, NT, RG> u(w);
-  const float unit = u.o;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -866,7 +874,8 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      l *= u.l;
+      float m = w.m[nt][i], unit;
+      u.leave(m, l, unit);
       const int row = (rg * NT + nt) * 8 + 2 * c + i;
       if (row >= a.rows) continue;
       if (slot < 0) {
@@ -886,7 +895,7 @@ __device__ __forceinline__ void kv8_end(Kv8Warp<D, NT, RG>& w, const Kv8Params& 
           *reinterpret_cast<float2*>(a.ws_o + at * D + 16 * j + 2 * r) =
               make_float2(w.acc[j][nt][i] * unit, w.acc[j][nt][2 + i] * unit);
         if (r == 0) {
-          a.ws_m[at] = l == l ? w.m[nt][i] + u.shift : 0.f;   // NaN scores move no maximum: not to be taken for an empty piece
+          a.ws_m[at] = l == l ? m : 0.f;   // NaN scores move no maximum: not to be taken for an empty piece
           a.ws_l[at] = l;
         }
       }
@@ -1012,7 +1021,6 @@ __device__ __forceinline__ void kv8_leave(Kv8Warp<D, NT, RG>& w, float2* ml, flo
   constexpr int KD = Kv8Warp<D, NT, RG>::KD;
   const int r = lane >> 2, c = lane & 3;
   const Kv8Units<D, NT, RG> u(w);
-  const float unit = u.o;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1021,9 +1029,10 @@ __device__ __forceinline__ void kv8_leave(Kv8Warp<D, NT, RG>& w, float2* ml, flo
       l += __shfl_xor_sync(0xffffffffu, l, 4);
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
-      l *= u.l;
+      float m = w.m[nt][i], unit;
+      u.leave(m, l, unit);
       const int row = nt * 8 + 2 * c + i;
-      if (r == 0) ml[row] = make_float2(w.m[nt][i] + u.shift, l);
+      if (r == 0) ml[row] = make_float2(m, l);
 #pragma unroll
       for (int j = 0; j < KD; ++j)
         *reinterpret_cast<float2*>(o + row * D + 16 * j + 2 * r) =

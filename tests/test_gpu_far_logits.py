@@ -88,3 +88,14 @@ def test_paged_calls(gqa, elem, op, D, G, T):
             o = call(q.cuda()[None], *cache, tab, lens, hk * G, hk, sign * scale)
             check(o[0], k, v, hk, G, D, elem, sign)
     assert gqa.gqa_status_check() == gqa.GQA_OK
+
+
+def test_8_bit_values_far_apart(gqa):
+    """The same where a token's values are 0, so that the exponents of its sequence lie far apart."""
+    D, hk, G, bs = 128, 2, 4, 16
+    for n in (1000, 9000):
+        q, k, v = case("f16", D, hk, G, 1, n, n, False)
+        v[::64] = 0
+        cache, tab, lens, k, v = pools(gqa, "kv8", k, v, hk, D, bs)
+        o = gqa.gqa_decode_kv8(q.cuda()[None], *cache, tab, lens, hk * G, hk)
+        check(o[0], k, v, hk, G, D, "f16", 1)
