@@ -43,6 +43,7 @@ constexpr int kTcCols = 512;        // TMEM columns allocated: S buffers at [0, 
 constexpr int kTcOCol = 128;        //   O accumulators at [128, 128 + D) and [256, 256 + D)
 constexpr int kTcOStride = 128;
 constexpr float kTcRescale = 8.f;   // log2 growth of a row max that forces an O rescale
+constexpr float kTcFar = 1048576.f; // a row max of this size: exponents from rounded products
 // tensor-memory columns: two S buffers below the first O accumulator, two O accumulators of up to
 // 128 columns inside the allocation
 static_assert(2 * kTcKeys <= kTcOCol && kTcOCol + kTcOStride + 128 <= kTcCols, "TMEM column map");
@@ -368,7 +369,7 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         // before O is rescaled or P rewritten; it signals the stage barrier of tile it - 2
         bool prev_done = it < 2;
         const int tp = it - 2;
-        const bool need = mt > m_used + kTcRescale;
+        const bool need = mt - m_used > kTcRescale;            // (m_used + kTcRescale would be rounded)
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? mt : m_used;
           const float alpha = need ? ptx::ex2(m_used - m_new) : 1.f;   // m_used = -inf -> 0
@@ -394,7 +395,14 @@ gqa_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         float lp[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) lp[i] = 0.f;
-        if (whole) {
+        // A maximum is a rounded product, so that a fused exponent is what rounding it left, not 0, at the largest key: below
+        // 2^20 less than 2^-4, from 2^28 on more than P has room for.  From 2^20 on all products are rounded like it.
+        const bool far = __any_sync(0xffffffffu, whole && fabsf(mu) >= kTcFar);
+        if (far && whole) {
+#pragma unroll
+          for (int j = 0; j < kTcKeys; ++j) x[j] *= c2;
+        }
+        if (whole && !far) {
           const float nmu = -mu;
 #pragma unroll
           for (int j = 0; j < kTcKeys; j += 2) {

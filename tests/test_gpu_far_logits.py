@@ -99,3 +99,16 @@ def test_8_bit_values_far_apart(gqa):
         cache, tab, lens, k, v = pools(gqa, "kv8", k, v, hk, D, bs)
         o = gqa.gqa_decode_kv8(q.cuda()[None], *cache, tab, lens, hk * G, hk)
         check(o[0], k, v, hk, G, D, "f16", 1)
+
+
+@pytest.mark.parametrize("elem", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,T", ROWS + [(16, 8)])
+def test_contiguous_calls(gqa, elem, D, G, T):
+    """gqa_decode: mma.sync kernels below 16 query rows, tcgen05 from there on."""
+    hk = 2
+    for n, same, sign in ((1000, False, 1), (1000, False, -1), (700, True, 1), (9000, False, 1)):
+        q, k, v = case(elem, D, hk, G, T, n, G + T + n, same)
+        for scale in (D ** -0.5, 2.0 ** 20):
+            o = gqa.gqa_decode(q.cuda()[None], k.cuda()[None], v.cuda()[None], hk * G, hk, sign * scale)
+            check(o[0], k.double(), v.double(), hk, G, D, elem, sign)
