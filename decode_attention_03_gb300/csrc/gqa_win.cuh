@@ -30,6 +30,9 @@ namespace gqa {
 
 constexpr int kWinSeqs = 768;      // sequences of a launch (the host splits larger batches): what the rings leave room for
 
+// What is copied where the 4-bit cache has no block: zeros, as many as one copy brings at most.
+__device__ const uint4 kWinZeros[kv4_block_bytes(32, 128) / 16] = {};
+
 struct WinParams : Kv8Params {
   const uint16_t *k_pool, *v_pool;   // 16-bit pools; the 4-bit cache is `cache`
   int window;                        // 0: none
@@ -178,7 +181,6 @@ struct WinStream {
   int len, skip, first;   // of at's sequence
   int t_end;         // tile of at's unit where the current window ends
   int k;             // at's place in the window
-  bool all;          // every block of the window that some token sees has a good id
   // kv4, the same for every tile: lanes 0 .. n - 1 copy `size` bytes from `off` of a (block, head) to `to` of the tile,
   // + step in the second half of a block of 64; `head` is `off` in head at.g of block 0, `stride` the bytes of a block
   const uint8_t* head;
@@ -228,7 +230,6 @@ __device__ __forceinline__ void win_ids_check(WinStream& s, const WinParams& a) 
     s.id = -1;
   }
   s.k = 0;
-  s.all = __all_sync(0xffffffffu, s.id >= 0);
 }
 
 // Enters the window at s.at, whose ids are in s.id: reports bad ids, finds where the next window begins and starts
@@ -269,16 +270,11 @@ __device__ __forceinline__ bool win_issue(WinStream& s, const WinParams& a, uint
   const int tile = win_tile_of(a, s.skip, s.at.t);
   if constexpr (KV4) {
     const int id = __shfl_sync(0xffffffffu, s.id, ((s.k << a.ids_log) + (half ? 0 : lane)) & 31);
-    const bool go = lane < s.n && id >= 0;
-    uint32_t bytes = K * (D + D / 8);
-    if (!s.all) {
-      const uint32_t went = __popc(__ballot_sync(0xffffffffu, go));
-      if (!half || went == 0) bytes = went * s.size;
-    }
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
-    if (go) {
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, K * (D + D / 8));
+    if (lane < s.n) {
       const uint8_t* src = s.head + (uint64_t)(uint32_t)id * s.stride + (K == 32 ? (tile & 1) * s.step : 0u);
-      if (idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status) &&
+      if (id < 0) src = reinterpret_cast<const uint8_t*>(kWinZeros);       // no block, or one with a bad id
+      if ((id < 0 || idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status)) &&
           smem_ok(dst + s.to, s.size, ring.lo, ring.hi, ring.status))
         bulk_load(dst + s.to, src, s.size, bar, policy);
     }

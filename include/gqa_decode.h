@@ -443,7 +443,7 @@ size_t gqa_decode_window_workspace_size(int num_seqs, int T_q, int h_q, int h_kv
  *   sinks   the keys j < sinks up to its own place, whatever the window (not used without one).
  * Blocks none of whose keys any token sees are neither read nor looked up: their entries of the table may be anything.
  * What a hidden key holds, NaN and infinities too, reaches no output; an infinite value that a token sees makes its
- * output infinite or NaN.  A token that sees no key gets O = 0.
+ * output infinite or NaN.  A token that sees no key gets O = 0.  The keys and values of a block with a bad id are zeros.
  * status: where the call reports (256 zeroed bytes, any workspace of this library, or gqa_device_status); NULL: the
  * workspace, whose first 256 bytes have to be zero then.
  * A key's weight is rounded to 11 bits (f16 calls: 22), or to within 2^-36 of its row's largest where it is very small. */
