@@ -50,6 +50,10 @@ constexpr int kKv8ByToken = 1025;              // the same, and a row is not to 
 constexpr int kKv8ToToken = 1026;              // that, from the next products on
 constexpr int kKv8WideUnit = 16;               // log2 of the unit of its O: sums of many values of 448 * 2^120 fit
 
+// What is copied where the cache has no block: zeros, as many as one copy brings at most.  (An exponent byte of 0 stands for
+// the scale 0.)
+__device__ const uint4 kKv8Zeros[kv8_block_bytes(kKv8Keys, 128) / 16] = {};
+
 struct Kv8Params {
   const uint16_t* q;
   uint16_t* o;
@@ -295,13 +299,12 @@ __device__ __forceinline__ bool kv8_issue(Kv8Stream& s, const Kv8Params& a, uint
                                           int lane, const Win& ring) {
   const bool half = a.block_size > kKv8Keys;
   const int id = __shfl_sync(0xffffffffu, s.id, (s.k + (half ? 0 : lane)) & 31);
-  const bool go = lane < s.n && id >= 0;
-  const uint32_t went = __popc(__ballot_sync(0xffffffffu, go));
-  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, half ? (went ? kKv8Keys * (2 * D + 2) : 0) : went * s.size);
-  if (go) {
+  if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kKv8Keys * (2 * D + 2));
+  if (lane < s.n) {
     const uint32_t off = s.off + (s.at.t & 1) * s.step;
     const uint8_t* src = s.head + (uint64_t)(uint32_t)id * s.stride + off;
-    if (idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status) &&
+    if (id < 0) src = reinterpret_cast<const uint8_t*>(kKv8Zeros);       // no block, or one with a bad id
+    if ((id < 0 || idx_ok(src + s.size - 1 - a.cache, (int64_t)a.num_blocks * s.stride, a.status)) &&
         smem_ok(dst + s.to, s.size, ring.lo, ring.hi, ring.status))
       bulk_load(dst + s.to, src, s.size, bar, policy);
   }

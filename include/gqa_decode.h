@@ -364,8 +364,8 @@ size_t gqa_decode_kv8_workspace_size(int num_seqs, int T_q, int h_q, int h_kv, i
  * key gets O = 0, as does a sequence of length 0), timeout_us, test_stall_cta (the index of one worker --
  * one or two warps that stream an equal share of all keys -- whose second tile is never loaded).  The keys of
  * all sequences are split evenly over the workers, whatever the lengths, and joined in the order of the
- * keys: the same call gives the same bits.  Block ids outside [0, num_blocks) are not loaded, lengths outside
- * [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check.
+ * keys: the same call gives the same bits.  Block ids outside [0, num_blocks) are not loaded (their keys and values are
+ * zeros), lengths outside [0, max_blocks_per_seq*block_size] are clamped; both are reported by gqa_workspace_check.
  * A key's weight is rounded to 11 bits (f16 calls: 22) or, where it is very small, to within 2^-26 of its row's largest
  * term, a weight times the scale of its value; values below 2^-88 may be lost where the same sequence and head has values
  * more than 2^10 times as large.
