@@ -1022,12 +1022,6 @@ __device__ __forceinline__ void win_fold(int n, ML ml, O o, float& m, float& l, 
   }
 }
 
-// Waits, bounded, for a phase of a barrier; the warp's lanes give up together (a lane that went on alone would wait for the
-// others in the next shuffle).  The vote costs 0.8 % of a long call over the 4-bit cache.
-__device__ __forceinline__ bool win_wait(uint32_t bar, uint32_t phase, uint64_t timeout_ns, const volatile int* abort) {
-  return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, phase, timeout_ns, abort));
-}
-
 // ---------------------------------------------------------------- kernels
 template <int D, int NT, int RG, bool KV4, bool BF16>
 __global__ void __launch_bounds__(WinCfg<D, NT, RG, KV4>::THREADS, 1)
@@ -1098,13 +1092,13 @@ gqa_win_kernel(const WinParams a) {
   int64_t slot = 2 * wk;         // where it goes when it is not the whole unit
   int i = 0, stage = 0, phase = 0;
   for (; i < n; ++i) {
-    if (!win_wait(full + stage * 8, phase, a.timeout_ns, abort)) break;
+    if (!kv8_wait(full + stage * 8, phase, a.timeout_ns, abort)) break;
     win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, skip, at.t) * C::KEYS,
                                          !clear.has(at.t), rg, lane, ring);
     __syncwarp();
     if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
     if (rg == 0 && i + STAGES < n) {
-      if (RG > 1 && !win_wait(empty + stage * 8, phase, a.timeout_ns, abort)) {
+      if (RG > 1 && !kv8_wait(empty + stage * 8, phase, a.timeout_ns, abort)) {
         ++i;
         break;
       }
@@ -1216,7 +1210,7 @@ gqa_win_short_kernel(const WinParams a) {
     const WinClear clear = win_clear_tiles<C::KEYS>(a, len, span.skip);
     int i = 0, stage = 0, phase = 0;
     for (; i < n; ++i) {
-      good = win_wait(full + stage * 8, phase, a.timeout_ns, flags);
+      good = kv8_wait(full + stage * 8, phase, a.timeout_ns, flags);
       if (!good) break;
       win_tile<D, NT, RG, KV4, BF16, FINE>(w, a, ring0 + stage * C::TILE, eb, len, win_tile_of(a, span.skip, t0 + i) * C::KEYS,
                                            !clear.has(t0 + i), rg, lane, ring);
@@ -1224,7 +1218,7 @@ gqa_win_short_kernel(const WinParams a) {
       if (RG > 1 && lane == 0) ptx::mbar_arrive(empty + stage * 8);
       if (rg == 0 && i + STAGES < n) {
         if (RG > 1) {
-          good = win_wait(empty + stage * 8, phase, a.timeout_ns, flags);
+          good = kv8_wait(empty + stage * 8, phase, a.timeout_ns, flags);
           if (!good) break;
         }
         if (!(STAGES == 1 && i == 0 && stalled))
