@@ -554,7 +554,7 @@ gqa_status decode_impl(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
   a.merge_in_kernel = merge_in_kernel(p, opt.merge_mode) ? 1 : 0;
   a.causal = opt.causal ? 1 : 0;
   a.scale_log2 = scale * kLog2e;
-  a.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
+  a.timeout_ns = wait_limit_ns(opt.timeout_us);
   a.stall_cta = opt.test_stall_cta;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -685,7 +685,7 @@ gqa_status paged_impl(const uint16_t* q, const uint16_t* k_pool, const uint16_t*
   a.n_splits = p.max_parts;
   a.merge_in_kernel = 1;
   a.scale_log2 = scale * kLog2e;
-  a.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
+  a.timeout_ns = wait_limit_ns(opt.timeout_us);
   a.stall_cta = opt.test_stall_cta;
 
   // persistent: one wave of CTAs pulling (sequence, partition, KV head) items from a queue;

@@ -10,6 +10,14 @@ namespace gqa {
 
 constexpr size_t kHeaderBytes = 256;        // status word (+ reserved) at the start of every workspace
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
+constexpr uint64_t kMinTimeoutNs = 1000000ull;
+
+// The limit of a kernel's waits.  A CTA that gives one up waits as long for its own copies before it leaves its shared memory:
+// a limit near the memory's latency would let it leave while they are on their way.
+inline uint64_t wait_limit_ns(uint32_t timeout_us) {
+  const uint64_t ns = (uint64_t)timeout_us * 1000ull;
+  return timeout_us == 0 ? kDefaultTimeoutNs : (ns < kMinTimeoutNs ? kMinTimeoutNs : ns);
+}
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

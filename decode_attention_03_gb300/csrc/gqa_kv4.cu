@@ -143,7 +143,7 @@ gqa_status decode_impl(const WinCall& c, const gqa_options* opt_in) {
   p.causal = opt.causal ? 1 : 0;
   p.stall = opt.test_stall_cta;
   p.scale_log2 = c.scale * kLog2e;
-  p.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
+  p.timeout_ns = wait_limit_ns(opt.timeout_us);
   // a window of all that the table holds hides nothing
   const int64_t keys = (int64_t)c.max_blocks * c.block_size;
   p.window = c.window < keys ? c.window : 0;

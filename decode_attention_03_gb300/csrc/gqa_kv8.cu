@@ -210,7 +210,7 @@ gqa_status decode_kv8_impl(const uint16_t* q, const void* cache, const int32_t* 
   p.causal = opt.causal ? 1 : 0;
   p.stall = opt.test_stall_cta;
   p.scale_log2 = scale * kLog2e;
-  p.timeout_ns = opt.timeout_us ? (uint64_t)opt.timeout_us * 1000ull : kDefaultTimeoutNs;
+  p.timeout_ns = wait_limit_ns(opt.timeout_us);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t seq_tiles = ((int64_t)max_blocks * block_size + kKv8Keys - 1) / kKv8Keys;
   std::lock_guard<std::mutex> turn(turn_of(ws));

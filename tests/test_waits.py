@@ -15,3 +15,17 @@ def test_cache_decode_kernels_vote():
     for name in ("gqa_kv8_decode.cuh", "gqa_win.cuh"):
         for line in waits(name):
             assert line.startswith("ptx::mbar_wait_bounded(") or "__all_sync(" in line, (name, line)
+
+
+def test_the_limit_has_one_origin():
+    """Every call's limit goes through the function that keeps it above the memory's latency."""
+    found = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith((".cu", ".cuh")):
+            continue
+        with open(os.path.join(CSRC, name)) as f:
+            for line in f:
+                if "timeout_ns = " in line:
+                    assert "wait_limit_ns(opt.timeout_us)" in line, (name, line)
+                    found += 1
+    assert found == 4
