@@ -20,7 +20,7 @@ namespace gqa {
 
 constexpr float kKv4MaxScale = 10240.f;     // 6 times this is the largest value: binary16 holds it
 constexpr uint32_t kKv4NanScale = 0x7f;     // scale byte of 16 elements with a NaN or an infinity among them
-constexpr uint32_t kKv4Infinite = 0x7c;     // scale bytes from here on are not finite
+constexpr uint32_t kKv4Infinite = 0x7c;     // scale bytes from here on are not finite (those above 0x71 = 10240 are not written)
 
 __host__ __device__ constexpr int kv4_block_bytes(int block_size, int D) { return block_size * (D + D / 8); }
 

@@ -287,7 +287,7 @@ __device__ __forceinline__ int append_holder(int e, int rot) {
 // its first group, so that the next token is on its way while this one is worked on.  Bound by its bytes, the
 // heads read and written once, when there are many tokens; the sums of squares and maxima go through log2 of
 // the lanes' number of shuffles.  CW = 8 (16-byte accesses) where rot/2 is a multiple of 8, else 4.
-// 16384 tokens of 64 + 8 + 8 heads of 128 take 105.3 us (6.45 TB/s, 0.95 of a copy's rate); 110.5 with one token a warp,
+// 16384 tokens of 64 + 8 + 8 heads of 128 take 105.3 us (6.45 TB/s; a copy 6.69); 110.5 with one token a warp,
 // 117.9 with five CTAs an SM (48 registers) instead of four (64).
 // AXES: pairs turned by positions of several axes, a.pair_axes: 16384 tokens of text and pictures 103.3 us.
 // Into the 4-bit cache (LAYOUT 4) a lane's chunks find the other elements of their sixteen by shuffles; three CTAs an SM, as

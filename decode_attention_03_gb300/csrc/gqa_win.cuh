@@ -2,18 +2,20 @@
 // 16-bit pools (num_blocks, block_size, h_kv * D).
 //
 // Query token t of T_q newest has the place p = len - T_q + t (causal; else len - 1) and sees key j <= p if j > p - window or
-// j < sinks.  A row of keys with a window is a short row: the tiles that no token of it sees are left out, and what remains, the sinks' tiles and those from the oldest visible key on, is numbered through; blocks that no token sees are
-// neither copied nor looked up, so that their pages may be gone.  All tiles of a launch then lie on one axis that is cut
-// into equal shares, one for each worker, as in the kernels of the 8-bit cache, whose plan, partials and merge these
-// kernels share: the cut looks at no sequence, and the same call gives the same bits.
+// j < sinks.  A row of keys with a window is a short row: the tiles that no token of it sees are left out, and what remains,
+// the sinks' tiles and those from the oldest visible key on, is numbered through; blocks that no token sees are neither copied
+// nor looked up, so that their pages may be gone.  All tiles of a launch then lie on one axis that is cut into equal shares,
+// one for each worker, as in the kernels of the 8-bit cache, whose plan, partials and merge these kernels share: the cut looks
+// at no sequence, and the same call gives the same bits.
 //
-// A worker is one warp (two that share a ring for 32 query rows over the 4-bit cache, and for more) with a ring of its own in shared memory, filled
-// by one bulk copy for each block of the 4-bit cache, and by 16-byte asynchronous copies from the 16-bit pools, whose rows of a
-// head lie apart: a bulk copy for each row costs its lane's turn in a loop over the lanes (four warps on an SM: 322 us
-// instead of 206 for 64 sequences under a window of 4096).
+// A worker is one warp, or two that share a ring (more than 32 query rows; over the 4-bit cache more than 24), with a ring of
+// its own in shared memory, filled by one bulk copy for each block of the 4-bit cache, and by 16-byte asynchronous copies from
+// the 16-bit pools, whose rows of a head lie apart: a bulk copy for each row costs its lane's turn in a loop over the lanes
+// (four warps on an SM: 322 us instead of 206 for 64 sequences under a window of 4096).  Two warps of a ring both convert all
+// of its tiles' codes, each for its own query rows.
 //
-// Measured: 64 sequences of 1K-16K keys, 32 + 8 heads of 128, over the 4-bit cache 102 us (5.5 TB/s, 0.82 of a copy's rate; bound
-// by issue slots and the ALU's conversions); 64 of 1K-32K over 16 bits under a window of 4096 160 us (6.4 TB/s, 0.95; DRAM).
+// Measured: 64 sequences of 1K-16K keys, 32 + 8 heads of 128, over the 4-bit cache 100 us (5.6 TB/s of a copy's 6.69;
+// bound by issue slots and the ALU's conversions); 64 of 1K-32K over 16 bits under a window of 4096 160 us (6.4 TB/s; DRAM).
 //
 // Arithmetic of a warp, for its 8 NT query rows and the keys of a tile: S^T = K Q^T and O^T += V^T P^T by mma.sync, keys
 // and columns on the M side, query rows on the N side.  kv4: a code becomes f16 by one conversion for two of them, and is
@@ -1068,7 +1070,7 @@ gqa_win_kernel(const WinParams a) {
   }
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
-  const uint64_t policy = ptx::policy_evict_first();
+  const uint64_t policy = KV4 ? ptx::policy_evict_first() : 0;       // (of bulk copies)
   const int eb = min(a.block_size, 32);
   uint2 raw[NT][D / 16];
   win_load_q<D, NT, RG, KV4>(raw, a, at.b, at.g, rg, lane);
@@ -1179,7 +1181,7 @@ gqa_win_short_kernel(const WinParams a) {
   const int t0 = c * share + grp * per, n = grp < busy ? min(per, mine - grp * per) : 0;
   const uint32_t ring0 = ptx::smem_u32(smem + C::RING_OFF) + grp * STAGES * C::TILE;
   const Win ring = {ring0, ring0 + STAGES * C::TILE, a.status};
-  const uint64_t policy = ptx::policy_evict_first();
+  const uint64_t policy = KV4 ? ptx::policy_evict_first() : 0;       // (of bulk copies)
   const int eb = min(a.block_size, 32);
   const bool stalled = a.stall >= 0 && a.stall == (int)blockIdx.x * C::GROUPS + grp;
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
@@ -1300,7 +1302,7 @@ constexpr int win_rows_nt(int cls) {
 }
 template <bool KV4>
 constexpr int win_rows_rg(int cls) {
-  return cls < 3 ? 1 : (cls == 3 ? (KV4 ? 2 : 1) : (cls == 4 ? 2 : 2));
+  return cls < 3 ? 1 : (cls == 3 && !KV4 ? 1 : 2);
 }
 
 // keys of a tile and workers of a CTA for a class of query rows

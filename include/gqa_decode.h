@@ -254,7 +254,8 @@ gqa_status gqa_merge_partial(const float* m, const float* l, const float* o_part
  * one pass over each whole sequence and no merge launch; on GB300 it measured no faster than v2
  * on any batch tried, so the automatic choice does not take it.  max_seq_len (host-known bound
  * on seq_lens) sizes the grid.  Block ids outside [0, num_blocks) are not loaded and are
- * reported by gqa_workspace_check. */
+ * reported by gqa_workspace_check; the output of a sequence that has one among its blocks is not
+ * defined. */
 gqa_status gqa_decode_paged(const uint16_t* q, const uint16_t* k_pool, const uint16_t* v_pool,
                             const int32_t* block_tables, const int32_t* seq_lens, uint16_t* o,
                             int num_seqs, int max_blocks_per_seq, int num_blocks, int block_size,
@@ -418,8 +419,8 @@ gqa_status gqa_kv8_read(const void* cache, const int32_t* block_tables, const in
  * c ^ (r / 4 % 2) for d_head 64.  Sixteen elements with the largest magnitude m are stored with the scale s = m / 6, at most
  * 10240, rounded to the nearest such number (ties to the even byte), and the codes of x / s (fp32), rounded to nearest, ties
  * to the even code, beyond 6 saturated: magnitudes up to 61440 are held, and where m < 6 * 2^-17 zeros.  Sixteen elements
- * with a NaN or an infinity among them are stored with the scale byte 0x7f and are read as NaN.  (Other scale bytes from 0x7c
- * on are not written; they are no values.) */
+ * with a NaN or an infinity among them are stored with the scale byte 0x7f and are read as NaN.  (Other scale bytes above 0x71,
+ * which is 10240, are not written; they are no values, and what is read or computed from them is not defined.) */
 #define GQA_CACHE_KV4 4    /* for gqa_append: the 4-bit cache, K and V in one array */
 
 /* Bytes of one (block, head) of the 4-bit cache: block_size * (d_head + d_head / 8); 0 for a block size or d_head that it
@@ -447,7 +448,9 @@ size_t gqa_decode_window_workspace_size(int num_seqs, int T_q, int h_q, int h_kv
  * output infinite or NaN.  A token that sees no key gets O = 0.  The keys and values of a block with a bad id are zeros.
  * status: where the call reports (256 zeroed bytes, any workspace of this library, or gqa_device_status); NULL: the
  * workspace, whose first 256 bytes have to be zero then.
- * A key's weight is rounded to 11 bits (f16 calls: 22), or to within 2^-36 of its row's largest where it is very small. */
+ * A key's weight is rounded to 11 bits (f16 calls: 22), or to within 2^-36 of its row's largest where it is very small.
+ * bfloat16 queries are brought into binary16's range by a power of two for each token and head: an element is kept to within
+ * 2^-39 of the largest of its D. */
 gqa_status gqa_decode_kv4(const uint16_t* q, const void* cache, const int32_t* block_tables, const int32_t* seq_lens,
                           uint16_t* o, int num_seqs, int T_q, int max_blocks_per_seq, int num_blocks, int block_size,
                           int h_q, int h_kv, int d_head, float scale, int window, int sinks, void* workspace,
