@@ -10,7 +10,7 @@ namespace gqa {
 
 constexpr size_t kHeaderBytes = 256;        // status word (+ reserved) at the start of every workspace
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
-constexpr uint64_t kMinTimeoutNs = 1000000ull;
+constexpr uint64_t kMinTimeoutNs = 5000000ull;
 
 // The limit of a kernel's waits.  A CTA that gives one up waits as long for its own copies before it leaves its shared memory:
 // a limit near the memory's latency would let it leave while they are on their way.

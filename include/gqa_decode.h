@@ -89,7 +89,7 @@ typedef struct {
                             workspace partials and one launch (mma.sync kernel only: the automatic
                             mma_path takes it for up to 64 rows; GQA_ERR_UNSUPPORTED on the tcgen05
                             kernel) */
-  uint32_t timeout_us;   /* limit of every device wait; 0 = 1,000,000 us, less than 1000 is taken for 1000 (a kernel
+  uint32_t timeout_us;   /* limit of every device wait; 0 = 1,000,000 us, less than 5000 is taken for 5000 (a kernel
                             that gives up has to outlast its own copies in flight) */
   int test_stall_cta;    /* test hook, -1 = off.  Contiguous calls: linear id (x + X*(y + Y*z)) of
                             one CTA whose producer never loads its second tile; paged calls: the
